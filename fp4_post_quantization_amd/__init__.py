@@ -1,8 +1,8 @@
 """fp4_post_quantization_amd -- FP4 microscaling block quantization with
 block-scale search on AMD MI355X (gfx950).
 
-Thin Python binding over the C ABI in include/fp4q.h (libfp4q.so, built in
-place).  It only marshals arguments: torch supplies device memory and the
+Thin Python binding over the C ABI in include/fp4q.h, fp4q_gemm.h and
+fp4q_kv.h (libfp4q.so, built in place).  It only marshals arguments: torch supplies device memory and the
 current HIP stream, and every step of the computation runs in the library's
 HIP kernels.  There is no CPU fallback; a missing library raises.
 
@@ -12,8 +12,14 @@ HIP kernels.  There is no CPU fallback; a missing library raises.
     gptq_nvfp4(w, hinv_chol, importance=None, window=None, global_scale=None, ...)
     dequantize(fmt, codes, scales, global_scale=None)
     block_hadamard(x, n)
+    rotate_heads(x, positions=None, table=None, *, norm_weight=None, hadamard_n=0, ...)
+    kv_append_mxfp4(cache, k, v, slots, positions=None, table=None, ...)
+    kv_read_mxfp4(cache, slots)
+    attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, ...)
 """
 
+import ctypes
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,6 +31,7 @@ __all__ = [
     "quantize_nvfp4", "quantize_nvfp4_noalloc", "global_scale_nvfp4", "quantize_mxfp4", "quantize_relaxed",
     "gptq_nvfp4", "gptq_mxfp4", "gptq_static_nvfp4", "gptq_static_mxfp4", "dequantize",
     "block_hadamard", "gemm_mxfp4", "gemm_nvfp4",
+    "rotate_heads", "kv_cache_mxfp4", "kv_append_mxfp4", "kv_read_mxfp4", "attention_mxfp4", "KVCacheMXFP4",
     "NVFP4Result", "MXFP4Result", "workspace", "read_status", "clear_status", "FP4QError",
 ]
 
@@ -90,6 +97,12 @@ def _check_data(ws):
             names.append("invalid inverse-Hessian factor")
         if st & L.DATA_BAD_PERM:
             names.append("processing order is not a permutation")
+        if st & L.DATA_BAD_POSITION:
+            names.append("position outside the rotation table")
+        if st & L.DATA_BAD_SLOT:
+            names.append("slot past the end of the cache")
+        if st & L.DATA_BAD_TABLE:
+            names.append("page number, sequence length or row offset out of range")
         raise FP4QError("data error: " + ", ".join(names))
 
 
@@ -646,3 +659,253 @@ def gemm_nvfp4(a, b, *, out_dtype=torch.float32, out=None, workspace_buf=None):
                                 _ptr(workspace_buf) if need else None, workspace_buf.numel() if need else 0,
                                 _stream(dev)))
     return out
+
+
+class KVCacheMXFP4(NamedTuple):
+    """An MXFP4 key/value cache in pages (page_size a power of two, 16 to
+    1024; head_dim 64, 128 or 256).  The tensors may be views in another
+    order of the first three axes, the same one for all four, with a dense
+    last axis; ``kv_cache_mxfp4`` allocates one."""
+    k_codes: torch.Tensor   # uint8 [pages, heads, page_size, head_dim/2] packed E2M1 codes
+    k_scales: torch.Tensor  # uint8 [pages, heads, page_size, head_dim/32] E8M0 bytes
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def kv_cache_mxfp4(pages, heads, page_size, head_dim, device=None):
+    """A zero-filled KVCacheMXFP4 on the device (2 * pages * heads *
+    page_size * head_dim * 17/32 bytes)."""
+    device = torch.device("cuda") if device is None else torch.device(device)
+    codes, scales = (pages, heads, page_size, head_dim // 2), (pages, heads, page_size, head_dim // 32)
+    return KVCacheMXFP4(*(torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, scales, codes, scales)))
+
+
+def _cache_struct(cache):
+    kc, ks, vc, vs = cache
+    dev = kc.device
+    if dev.type != "cuda":
+        raise ValueError("the cache must be device tensors")
+    if kc.dim() != 4:
+        raise ValueError("cache codes must be [pages, heads, page_size, head_dim/2]")
+    pages, heads, page, half = kc.shape
+    st = kc.stride()
+    sub = (pages, heads, page, half // 16)
+    sst = (st[0] // 16, st[1] // 16, st[2] // 16, 1)
+    for name, t, shape, stride in (("k_codes", kc, kc.shape, (st[0], st[1], st[2], 1)), ("k_scales", ks, sub, sst),
+                                   ("v_codes", vc, kc.shape, (st[0], st[1], st[2], 1)), ("v_scales", vs, sub, sst)):
+        if t.dtype != torch.uint8 or t.device != dev or t.shape != shape:
+            raise ValueError(f"cache.{name} must be a uint8 tensor of shape {tuple(shape)} on {dev}")
+        if t.stride() != stride and any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), stride)):
+            raise ValueError(f"cache.{name} must have strides {stride}: a dense last axis, codes and scales of keys "
+                             "and values in one order")
+    return L.KVCacheStruct(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page, heads, 2 * half,
+                           st[0], st[1], st[2]), dev
+
+
+def _heads(t, name, device=None):
+    """A [tokens, heads, head_dim] device tensor with a dense last axis."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}, must be on {device or 'a GPU'}")
+    return t if t.stride(2) == 1 else t.contiguous()
+
+
+def _index(t, shape, dtype, device, name):
+    """An index vector the library reads in place."""
+    return t if t is None else _given(t, shape, dtype, device, name)
+
+
+def _head_map(tokens, dim, device, positions, table, interleaved, norm_weight, eps, hadamard_n):
+    """fp4q_head_map_t and the tensors it points into."""
+    if (positions is None) != (table is None):
+        raise ValueError("positions and table go together")
+    rot = n_pos = 0
+    if table is not None:
+        if table.dim() != 2 or table.dtype != torch.float32 or table.device != device or not table.is_contiguous():
+            raise ValueError(f"table must be a contiguous float32 [positions, rotary_dim] tensor on {device}")
+        n_pos, rot = table.shape
+        if rot == 0:
+            raise ValueError("table must have rotary_dim columns")
+        _index(positions, (tokens,), torch.int64, device, "positions")
+    w = norm_weight
+    if w is not None:
+        w = w.to(device=device, dtype=torch.float32).contiguous()
+        if w.shape != (dim,):
+            raise ValueError("norm_weight must have head_dim entries")
+        if w.data_ptr() % 16:
+            w = w.clone()
+    m = L.HeadMapStruct(_ptr(w), float(eps), _ptr(positions), _ptr(table), n_pos, rot, int(bool(interleaved)),
+                        int(hadamard_n))
+    return m, w
+
+
+class _OnDevice:
+    """Makes a tensor's device current for a launch; free where it is already."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def rotate_heads(x, positions=None, table=None, *, interleaved=False, norm_weight=None, eps=1e-6, hadamard_n=0,
+                 out_dtype=None, out=None, ws=None, check=False):
+    """Norm, rotary position and block Hadamard of each head of x [tokens,
+    heads, head_dim] (float32 or bfloat16; head_dim 64, 128 or 256), each
+    optional, in one pass, rounded once to the output type (x's by default).
+
+    norm_weight: [head_dim] weights of a root-mean-square norm of each head
+    (eps added to the mean square).  positions: int64 [tokens]; table: float32
+    [positions, rotary_dim], the cosines then the sines of a position's
+    rotary_dim / 2 angles, with any scaling for long contexts in them:
+    the first rotary_dim elements of a head are rotated (a multiple of 16),
+    element i paired with i + rotary_dim/2, or 2i with 2i + 1 when
+    interleaved.  hadamard_n: rotate by the block Hadamard matrix at the end.
+    out: a dense tensor to write into (x itself is allowed).  check:
+    synchronize and raise on data errors."""
+    lib = L.load()
+    x = _heads(x, "x")
+    tokens, heads, dim = x.shape
+    dev = x.device
+    m, keep = _head_map(tokens, dim, dev, positions, table, interleaved, norm_weight, eps, hadamard_n)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=out_dtype or x.dtype, device=dev)
+    else:
+        _given(out, (tokens, heads, dim), out_dtype or out.dtype, dev, "out")
+    with _OnDevice(dev):
+        ws = _ws(ws, dev)
+        L.check(lib.fp4q_rotate_heads(x.data_ptr(), _dtype_code(x), tokens, heads, dim, x.stride(0), x.stride(1),
+                                      ctypes.byref(m), _dtype_code(out), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                      _stream(dev)))
+    if check:
+        _check_data(ws)
+    return out
+
+
+def kv_append_mxfp4(cache, k, v, slots, positions=None, table=None, *, interleaved=False, norm_weight=None, eps=1e-6,
+                    hadamard_n=0, window=(-1, 0), ws=None, check=False):
+    """Quantizes keys and values [tokens, heads, head_dim] (float32 or
+    bfloat16) into cache slots, in place: keys normed and rotated as
+    ``rotate_heads`` does (kept in float32), then both as ``quantize_mxfp4``
+    does with the same window.  slots: int64 [tokens], slot s is row
+    s % page_size of page s // page_size; negative: the token is skipped;
+    the others of a call must be distinct.  With hadamard_n the queries need
+    the same rotation."""
+    lib = L.load()
+    c, dev = _cache_struct(cache)
+    k, v = _heads(k, "k", dev), _heads(v, "v", dev)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and type")
+    tokens, heads, dim = k.shape
+    if heads != c.heads or dim != c.head_dim:
+        raise ValueError(f"k must be [tokens, {c.heads}, {c.head_dim}]")
+    _index(slots, (tokens,), torch.int64, dev, "slots")
+    if slots is None:
+        raise ValueError("slots is required")
+    m, keep = _head_map(tokens, dim, dev, positions, table, interleaved, norm_weight, eps, hadamard_n)
+    with _OnDevice(dev):
+        ws = _ws(ws, dev)
+        L.check(lib.fp4q_kv_append_mxfp4(ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
+                                         v.stride(0), v.stride(1), _dtype_code(k), tokens, slots.data_ptr(),
+                                         ctypes.byref(m), int(window[0]), int(window[1]), ws.data_ptr(), ws.numel(),
+                                         _stream(dev)))
+    if check:
+        _check_data(ws)
+
+
+def kv_read_mxfp4(cache, slots, *, out_dtype=torch.bfloat16, out=None, ws=None, check=False):
+    """The decoded keys and values of cache slots (int64 [tokens]; a negative
+    slot gives zeros): (k, v), each [tokens, heads, head_dim] in bfloat16 or
+    float32.  out: a pair of dense tensors to write into."""
+    lib = L.load()
+    c, dev = _cache_struct(cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D int64 tensor")
+    _index(slots, slots.shape, torch.int64, dev, "slots")
+    shape = (slots.numel(), c.heads, c.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        for t in out:
+            _given(t, shape, out[0].dtype, dev, "out")
+    k, v = out
+    with _OnDevice(dev):
+        ws = _ws(ws, dev)
+        L.check(lib.fp4q_kv_read_mxfp4(ctypes.byref(c), slots.data_ptr(), shape[0], _dtype_code(k), k.data_ptr(),
+                                       v.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+    if check:
+        _check_data(ws)
+    return k, v
+
+
+def attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, *, max_new=None, max_len=None, scale=None, causal=True,
+                    window=0, out=None, return_lse=False, ws=None, check=False):
+    """softmax(scale q K^T + mask) V over the cached keys and values of each
+    sequence, for bfloat16 queries [tokens, q_heads, head_dim] (rotated by
+    the caller; q_heads a multiple of the cache's heads, whose head h serves
+    query heads h * groups ...).
+
+    block_table: int32 [batch, pages of a sequence]; seq_lens: int32 [batch]
+    cached tokens, the new ones included.  cu_q: int32 [batch + 1] offsets of
+    each sequence's rows of q, its last tokens; None: one row each.  max_new,
+    max_len: host bounds of a sequence's rows and length (default: 1 or the
+    rows of q, and what the table can hold); tighter ones serve the choice of
+    kernel and workspace.  scale: default head_dim ** -0.5.  causal: rows see
+    keys up to their own position.  window: rows see only the last `window`
+    positions (0: all).  A row that sees nothing gives zeros.
+
+    Returns out [tokens, q_heads, head_dim] in bfloat16, with return_lse
+    also the float32 [tokens, q_heads] natural log-sum-exp of the scores.
+    Rows of q beyond cu_q's last offset are left as they are in a given out
+    (unspecified in a fresh one).  ws: a workspace of
+    ``fp4q_attention_mxfp4_workspace_bytes`` bytes (a fresh one by default);
+    calls that may overlap need one each.  check: synchronize and raise on
+    data errors."""
+    lib = L.load()
+    c, dev = _cache_struct(cache)
+    q = _heads(q, "q", dev)
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    tokens, q_heads, dim = q.shape
+    if dim != c.head_dim or q_heads % c.heads:
+        raise ValueError(f"q must be [tokens, a multiple of {c.heads}, {c.head_dim}]")
+    if (not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.dtype != torch.int32
+            or block_table.device != dev or (block_table.stride(1) != 1 and block_table.size(1) > 1)
+            or (block_table.size(0) > 1 and block_table.stride(0) < block_table.size(1))):
+        raise ValueError(f"block_table must be a row-major int32 [batch, pages] tensor on {dev}")
+    batch, width = block_table.shape
+    _given(seq_lens, (batch,), torch.int32, dev, "seq_lens")
+    if cu_q is not None:
+        _given(cu_q, (batch + 1,), torch.int32, dev, "cu_q")
+    elif tokens != batch:
+        raise ValueError("without cu_q there is one row of q for each sequence")
+    max_new = min(tokens, tokens if cu_q is not None else 1) if max_new is None else min(int(max_new), tokens)
+    max_len = width * c.page_size if max_len is None else min(int(max_len), width * c.page_size)
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _given(out, (tokens, q_heads, dim), torch.bfloat16, dev, "out")
+    lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    need = lib.fp4q_attention_mxfp4_workspace_bytes(tokens, batch, q_heads, c.heads, dim, max_new, max_len)
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    else:
+        ws = _ws(ws, dev)
+    with _OnDevice(dev):
+        L.check(lib.fp4q_attention_mxfp4(
+            ctypes.byref(c), q.data_ptr(), q.stride(0), q.stride(1), tokens, q_heads, block_table.data_ptr(),
+            max(block_table.stride(0), width), width, batch, seq_lens.data_ptr(), _ptr(cu_q), max_new, max_len,
+            scale, int(bool(causal)), int(window), out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+            _stream(dev)))
+    if check:
+        _check_data(ws)
+    return (out, lse) if return_lse else out

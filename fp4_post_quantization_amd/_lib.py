@@ -1,4 +1,4 @@
-"""ctypes declarations of the fp4q C ABI (include/fp4q.h, include/fp4q_gemm.h)."""
+"""ctypes declarations of the fp4q C ABI (include/fp4q.h, include/fp4q_gemm.h, include/fp4q_kv.h)."""
 
 import ctypes
 import os
@@ -22,6 +22,9 @@ DATA_BAD_GLOBAL_SCALE = 0x4
 DATA_BAD_SCALE = 0x8
 DATA_BAD_HESSIAN = 0x10
 DATA_BAD_PERM = 0x20
+DATA_BAD_POSITION = 0x40
+DATA_BAD_SLOT = 0x80
+DATA_BAD_TABLE = 0x100
 
 EXPORTS = (
     "fp4q_version",
@@ -46,11 +49,39 @@ EXPORTS = (
     "fp4q_gemm_nvfp4",
 )
 
+# include/fp4q_kv.h
+KV_EXPORTS = (
+    "fp4q_rotate_heads",
+    "fp4q_kv_append_mxfp4",
+    "fp4q_kv_read_mxfp4",
+    "fp4q_attention_mxfp4",
+    "fp4q_attention_mxfp4_workspace_bytes",
+)
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _U32 = ctypes.c_uint32
 _SZ = ctypes.c_size_t
+
+_F64 = ctypes.c_double
+
+
+class KVCacheStruct(ctypes.Structure):
+    """fp4q_kv_cache_t"""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("pages", _I64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", _I64), ("head_stride", _I64), ("token_stride", _I64)]
+
+
+class HeadMapStruct(ctypes.Structure):
+    """fp4q_head_map_t"""
+    _fields_ = [("norm_weight", _P), ("eps", _F64), ("positions", _P), ("table", _P), ("table_positions", _I64),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("hadamard_n", ctypes.c_int32)]
+
+
+_CACHE = ctypes.POINTER(KVCacheStruct)
+_MAP = ctypes.POINTER(HeadMapStruct)
 
 _SIGNATURES = {
     "fp4q_version": (_I, []),
@@ -76,6 +107,12 @@ _SIGNATURES = {
     "fp4q_gemm_mxfp4": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, ctypes.c_float, _I, _P, _I64, _P, _SZ, _P]),
     "fp4q_gemm_mxfp4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "fp4q_gemm_nvfp4_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "fp4q_rotate_heads": (_I, [_P, _I, _I64, _I64, _I64, _I64, _I64, _MAP, _I, _P, _P, _SZ, _P]),
+    "fp4q_kv_append_mxfp4": (_I, [_CACHE, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _MAP, _I, _I, _P, _SZ, _P]),
+    "fp4q_kv_read_mxfp4": (_I, [_CACHE, _P, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "fp4q_attention_mxfp4": (_I, [_CACHE, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64,
+                                  ctypes.c_float, _I, _I64, _P, _P, _P, _SZ, _P]),
+    "fp4q_attention_mxfp4_workspace_bytes": (_SZ, [_I64] * 7),
     "fp4q_gemm_nvfp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _I64, _P, _SZ, _P]),
 }
 

@@ -7,9 +7,11 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfp4q.so")
-SOURCES = [os.path.join(PKG, "csrc", "fp4q.hip"), os.path.join(PKG, "csrc", "fp4q_gemm.hip")]
-HEADERS = [os.path.join(PKG, "csrc", "fp4q_device.h"), os.path.join(ROOT, "include", "fp4q.h"),
-           os.path.join(ROOT, "include", "fp4q_gemm.h")]
+SOURCES = [os.path.join(PKG, "csrc", name)
+           for name in ("fp4q.hip", "fp4q_gemm.hip", "fp4q_kv.hip", "fp4q_attn.hip")]
+HEADERS = [os.path.join(PKG, "csrc", "fp4q_device.h"), os.path.join(PKG, "csrc", "fp4q_kv_host.h"),
+           os.path.join(ROOT, "include", "fp4q.h"), os.path.join(ROOT, "include", "fp4q_gemm.h"),
+           os.path.join(ROOT, "include", "fp4q_kv.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

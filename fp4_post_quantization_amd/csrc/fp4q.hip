@@ -59,55 +59,6 @@ __constant__ E4M3Tables kE4M3 = make_e4m3_tables();
 
 // ============================================================ kernels ====
 
-// The dispatch ID of the running kernel: the index of its packet in the
-// hardware queue, the same in every workgroup of a launch and different for
-// every launch on the queue.
-extern "C" __device__ unsigned long long fp4q_dispatch_id() __asm("llvm.amdgcn.dispatch.id");
-
-// The status word of a call is a 64-bit slot at the start of the workspace:
-// its low half (byte 0) holds the FP4Q_DATA_* bits, its high half the low
-// 32 bits of the dispatch ID of the call's first kernel.  That kernel's
-// workgroups merge into the slot by compare-and-swap.  A slot with another
-// tag belongs to an earlier call, or is garbage, and is replaced; a slot
-// with this call's tag gets the bits ORed in.  So in whichever order the
-// workgroups arrive, the slot ends with this call's tag and exactly the
-// bits its kernels reported.  Workgroup 0 of the first kernel always merges
-// (with no bits if it has none), so a call without errors still replaces
-// the slot; nothing waits on anything.  The call's later kernels run after
-// the first on the stream and OR their bits into the low half.
-struct Status {
-  uint32_t *slot;
-  bool first;  // this kernel is the call's first: merge under its dispatch tag
-
-  __device__ void merge(uint32_t bits) const {
-    unsigned long long *p = reinterpret_cast<unsigned long long *>(slot);
-    const unsigned long long tag = (unsigned long long)(uint32_t)fp4q_dispatch_id() << 32;
-    unsigned long long old = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (;;) {
-      const unsigned long long keep = (old & 0xFFFFFFFF00000000ull) == tag ? (old & 0xFFFFFFFFull) : 0ull;
-      const unsigned long long want = tag | keep | bits;
-      if (want == old) return;
-      const unsigned long long seen = atomicCAS(p, old, want);
-      if (seen == old) return;
-      old = seen;
-    }
-  }
-  // an error found by any workgroup
-  __device__ void report(uint32_t bits) const {
-    if (first) merge(bits);
-    else atomicOr(slot, bits);
-  }
-  // at the start of a kernel: workgroup 0 of the call's first kernel takes the slot
-  __device__ void begin() const {
-    if (first && blockIdx.x == 0 && threadIdx.x == 0) merge(0u);
-  }
-  // at the end of a kernel whose lanes gathered their error bits in err: one report site for all
-  // of them (thread 0 of workgroup 0 reports even without errors, taking the slot for a first kernel)
-  __device__ void finish(uint32_t err) const {
-    if (__builtin_expect(err != 0u, 0) || (first && blockIdx.x == 0 && threadIdx.x == 0)) report(err);
-  }
-};
-
 // The only kernel of an empty call: takes the status slot for the call, or
 // adds to it (first = false), with no bits or those of validating a given
 // NVFP4 global scale, and optionally writes the global scale of an empty

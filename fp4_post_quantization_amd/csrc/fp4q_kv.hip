@@ -1,0 +1,507 @@
+// Heads of queries, keys and values on their way to and from an MXFP4
+// key/value cache (include/fp4q_kv.h): norm and rotation of heads, append
+// into page slots, and the decoded rows of slots.
+//
+// Work decomposition: a lane owns 8 contiguous elements of a head, a head
+// is head_dim / 8 adjacent lanes, so every load and store of a wave is
+// contiguous over its heads (16 bytes a lane for bfloat16) and one token of
+// one head is already work for 16 lanes.  All three kernels are bound by the
+// bytes they move; nothing is read twice from memory: the element a rotation
+// pairs with comes from the same cache lines, loaded again by the lane that
+// needs it.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "fp4q.h"
+#include "fp4q_device.h"
+#include "fp4q_kv.h"
+#include "fp4q_kv_host.h"
+
+namespace fp4q {
+namespace {
+
+constexpr int kChunk = 8;  // elements of a lane
+
+struct HeadMap {
+  const float *weight;
+  double eps;
+  const int64_t *positions;
+  const float *table;
+  int64_t n_positions;
+  int rotary, interleaved, hadamard;
+};
+
+__device__ __forceinline__ void load8(const uint16_t *p, float z[8]) {
+  const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    z[2 * k] = as_f(w[k] << 16);
+    z[2 * k + 1] = as_f(w[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float z[8]) {
+  const f32x4 *q = reinterpret_cast<const f32x4 *>(p);
+  const f32x4 a = q[0], b = q[1];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    z[k] = a[k];
+    z[4 + k] = b[k];
+  }
+}
+
+// bfloat16 nearest to f, ties to even (NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  const uint32_t u = as_u(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float z[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = bf16_bits(z[2 * k]) | (bf16_bits(z[2 * k + 1]) << 16);
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
+}
+__device__ __forceinline__ void store8(float *p, const float z[8]) {
+  f32x4 *q = reinterpret_cast<f32x4 *>(p);
+  __builtin_nontemporal_store(f32x4{z[0], z[1], z[2], z[3]}, q);
+  __builtin_nontemporal_store(f32x4{z[4], z[5], z[6], z[7]}, q + 1);
+}
+
+// One stage of the block Hadamard over lanes l and l ^ M.
+template <int M>
+__device__ __forceinline__ void hadamard_lanes(float z[8], int lane) {
+  const bool hi = lane & M;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float o = __shfl_xor(z[i], M);
+    z[i] = hi ? (o - z[i]) : (z[i] + o);
+  }
+}
+
+// fp4q_block_hadamard's stages on a lane's 8 elements: h = 1, 2, 4 inside
+// the lane, then lanes 1, 2, 4 and 8 apart.  n is the same in every lane.
+__device__ __forceinline__ void hadamard8(float z[8], int n, int lane) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & h) == 0) {
+        const float a = z[i], b = z[i + h];
+        z[i] = a + b;
+        z[i + h] = a - b;
+      }
+    }
+  }
+  hadamard_lanes<1>(z, lane);
+  if (n >= 32) hadamard_lanes<2>(z, lane);
+  if (n >= 64) hadamard_lanes<4>(z, lane);
+  if (n >= 128) hadamard_lanes<8>(z, lane);
+  const float c = n == 16 ? hadamard_scale<16>()
+                          : (n == 32 ? hadamard_scale<32>() : (n == 64 ? hadamard_scale<64>() : hadamard_scale<128>()));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = z[i] * c;
+}
+
+// The lane's 8 elements (chunk c) of the head at x after the map.  Every
+// lane of a head calls this together; active lanes have a head.  The sum of
+// squares is kept in float64, where the square of a float32 is exact and 256
+// of them lose at most 2^-45 of the sum, so r does not depend on the order
+// in which lanes add.
+template <typename T, int D>
+__device__ __forceinline__ void map_head(const T *x, int c, int lane, int64_t token, bool active, const HeadMap &m,
+                                         float z[8], uint32_t &err) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = 0.0f;
+  // the pair's other element, 8 elements at a time: chunk c + half / 8 or c - half / 8
+  const int half = m.rotary / 2, at = c * kChunk;
+  const bool turned = m.table != nullptr && at < m.rotary;
+  const bool first = at < half;
+  float p[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = 0.0f;
+  const int other = first ? at + half : at - half;
+  const bool paired = turned && !m.interleaved;
+  if (active) {
+    load8(x + at, z);
+    if (paired) load8(x + other, p);
+  }
+  float cs[8], sn[8];
+  if (active && turned) {
+    int64_t pos = m.positions[token];
+    if (pos < 0 || pos >= m.n_positions) {
+      err |= FP4Q_DATA_BAD_POSITION;
+      pos = 0;
+    }
+    const float *row = m.table + pos * m.rotary;
+    if (m.interleaved) {
+      const f32x4 a = *reinterpret_cast<const f32x4 *>(row + at / 2);
+      const f32x4 b = *reinterpret_cast<const f32x4 *>(row + half + at / 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = a[i];
+        sn[i] = b[i];
+      }
+    } else {
+      const int k = first ? at : at - half;
+      load8(row + k, cs);
+      load8(row + half + k, sn);
+    }
+  }
+  if (m.weight) {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)z[i] * (double)z[i];
+#pragma unroll
+    for (int d = 1; d < D / kChunk; d <<= 1) s += __shfl_xor(s, d);
+    const float r = (float)(1.0 / sqrt(s * (1.0 / D) + m.eps));
+    float w[8];
+    load8(m.weight + at, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = (z[i] * r) * w[i];
+    if (paired) {
+      load8(m.weight + other, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = (p[i] * r) * w[i];
+    }
+  }
+  if (active && turned) {
+    if (m.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = z[2 * i], b = z[2 * i + 1];
+        z[2 * i] = a * cs[i] - b * sn[i];
+        z[2 * i + 1] = b * cs[i] + a * sn[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = p[i] * sn[i];
+        z[i] = first ? z[i] * cs[i] - t : z[i] * cs[i] + t;
+      }
+    }
+  }
+  if (m.hadamard) hadamard8(z, m.hadamard, lane);
+}
+
+// -------------------------------------------------------- rotate_heads ----
+template <typename T, typename OutT, int D>
+__global__ __launch_bounds__(kThreads) void rotate_heads_kernel(const T *x, int units, int heads, int64_t st,
+                                                                 int64_t sh, HeadMap m, OutT *out,
+                                                                 uint32_t *status) {
+  constexpr int LPH = D / kChunk;
+  const int lane = threadIdx.x & 63, c = threadIdx.x % LPH;
+  const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
+  const bool active = u < units;
+  const int token = active ? (int)((uint32_t)u / (uint32_t)heads) : 0;
+  const int h = active ? (int)u - token * heads : 0;
+  uint32_t err = 0u;
+  float z[8];
+  map_head<T, D>(x + token * st + h * sh, c, lane, token, active, m, z, err);
+  if (active) store8(out + u * D + c * kChunk, z);
+  Status{status, true}.finish(err);
+}
+
+// ----------------------------------------------------------- kv_append ----
+struct CacheView {
+  uint8_t *codes[2], *scales[2];  // keys, values
+  int64_t rows;                   // pages * page_size: slot numbers below it are in the cache
+  int log_page;
+  int64_t page_stride, head_stride, token_stride;
+  // byte offset of a row's codes; its scales are at a sixteenth of it
+  __device__ __forceinline__ int64_t at(int64_t slot, int h) const {
+    const int64_t page = slot >> log_page, r = slot & ((1 << log_page) - 1);
+    return page * page_stride + h * head_stride + r * token_stride;
+  }
+};
+
+// Value of lane S of the caller's quad.
+template <int S>
+__device__ __forceinline__ float quad_bcast(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), S * 0x55, 0xF, 0xF, true));
+}
+
+// This lane's part of a block's loss chain, continued from acc.
+__device__ __forceinline__ float chain8(const float z[8], const float q[8], float V, float acc) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float e = fmaf(-q[i], V, z[i]);
+    acc = fmaf(e, e, acc);
+  }
+  return acc;
+}
+
+// fp4q_quantize_mxfp4 of a block of 32 spread over a quad: the base
+// exponent from the block's maximum, then the window's exponents in
+// ascending order with the loss as one chain in element order, handed from
+// lane to lane.  Returns the lane's 8 codes; E is the block's exponent.
+__device__ __forceinline__ uint32_t quantize_quad(const float z[8], int lo, int hi, int &E) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(z[i]));
+  a = fmaxf(a, xor_lane<1>(a));
+  a = fmaxf(a, xor_lane<2>(a));
+  const int eb = mx_base_exponent(a);
+  E = max(-127, eb + lo);
+  if (lo < hi) {
+    float best = __builtin_inff();
+    const int top = min(127, eb + hi);
+    for (int e = E; e <= top; ++e) {
+      const float down = pow2f(-e), V = pow2f(e);
+      float y[8], q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = z[i] * down;
+      fp4x8_to_f32(cvt_fp4x8(y), q);
+      float L = quad_bcast<0>(chain8(z, q, V, 0.0f));
+      L = quad_bcast<1>(chain8(z, q, V, L));
+      L = quad_bcast<2>(chain8(z, q, V, L));
+      L = quad_bcast<3>(chain8(z, q, V, L));
+      if (L < best) {
+        best = L;
+        E = e;
+      }
+    }
+  }
+  const float down = pow2f(-E);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = z[i] * down;
+  return cvt_fp4x8(y);
+}
+
+struct AppendArgs {
+  const void *src[2];  // keys, values
+  int64_t st[2], sh[2];
+  const int64_t *slots;
+  int units, heads;  // units = tokens * heads of each
+  HeadMap m;
+  int lo, hi;
+  CacheView cache;
+  uint32_t *status;
+};
+
+// blockIdx.y: keys or values.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
+  constexpr int LPH = D / kChunk;
+  const int kv = blockIdx.y;
+  const int lane = threadIdx.x & 63, c = threadIdx.x % LPH;
+  const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
+  uint32_t err = 0u;
+  bool active = u < a.units;
+  const int token = active ? (int)((uint32_t)u / (uint32_t)a.heads) : 0;
+  const int h = active ? (int)u - token * a.heads : 0;
+  int64_t slot = -1;
+  if (active) {
+    slot = a.slots[token];
+    if (slot >= a.cache.rows) {
+      err |= FP4Q_DATA_BAD_SLOT;
+      slot = -1;
+    }
+  }
+  active = slot >= 0;
+  const T *x = static_cast<const T *>(a.src[kv]) + token * a.st[kv] + h * a.sh[kv];
+  float z[8];
+  if (kv == 0) {
+    map_head<T, D>(x, c, lane, token, active, a.m, z, err);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = 0.0f;
+    if (active) load8(x + c * kChunk, z);
+  }
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) finite &= fabsf(z[i]) <= 3.402823466e38f;
+  if (!finite) err |= FP4Q_DATA_NONFINITE_INPUT;
+  int E;
+  const uint32_t codes = quantize_quad(z, a.lo, a.hi, E);
+  if (active) {
+    const int64_t row = a.cache.at(slot, h);
+    *reinterpret_cast<uint32_t *>(a.cache.codes[kv] + row + c * 4) = codes;
+    if ((c & 3) == 0) a.cache.scales[kv][row / 16 + c / 4] = (uint8_t)(E + 127);
+  }
+  const Status st{a.status, true};
+  if (__builtin_expect(err != 0u, 0)) st.report(err);
+  else if (blockIdx.x == 0 && kv == 0 && threadIdx.x == 0) st.merge(0u);
+}
+
+// ------------------------------------------------------------- kv_read ----
+template <typename OutT, int D>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, const int64_t *__restrict__ slots,
+                                                            int units, int heads, OutT *k_out, OutT *v_out,
+                                                            uint32_t *status) {
+  constexpr int LPH = D / kChunk;
+  const int kv = blockIdx.y;
+  OutT *out = kv ? v_out : k_out;
+  const int c = threadIdx.x % LPH;
+  const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
+  uint32_t err = 0u;
+  if (u < units) {
+    const int token = (int)((uint32_t)u / (uint32_t)heads), h = (int)u - token * heads;
+    int64_t slot = slots[token];
+    if (slot >= cache.rows) {
+      err |= FP4Q_DATA_BAD_SLOT;
+      slot = -1;
+    }
+    if (out) {
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = 0.0f;
+      if (slot >= 0) {
+        const int64_t row = cache.at(slot, h);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(cache.codes[kv] + row + c * 4);
+        const uint32_t b = cache.scales[kv][row / 16 + c / 4];
+        const float s = b == 255u ? __builtin_nanf("") : pow2f((int)b - 127);
+        fp4x8_to_f32(w, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = z[i] * s;
+      }
+      store8(out + u * D + c * kChunk, z);
+    }
+  }
+  const Status st{status, true};
+  if (__builtin_expect(err != 0u, 0)) st.report(err);
+  else if (blockIdx.x == 0 && kv == 0 && threadIdx.x == 0) st.merge(0u);
+}
+
+// The only kernel of a call without tokens: takes the status slot.
+__global__ __launch_bounds__(64) void kv_status_kernel(uint32_t *status) {
+  if (threadIdx.x == 0) Status{status, true}.merge(0u);
+}
+
+// ------------------------------------------------------------ dispatch ----
+template <typename F>
+void with_dim(int64_t d, F &&f) {
+  if (d == 64) f(std::integral_constant<int, 64>{});
+  else if (d == 128) f(std::integral_constant<int, 128>{});
+  else f(std::integral_constant<int, 256>{});
+}
+template <typename F>
+void with_type(fp4q_dtype_t t, F &&f) {
+  if (t == FP4Q_BF16) f((uint16_t *)nullptr);
+  else f((float *)nullptr);
+}
+
+fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
+
+HeadMap head_map(const fp4q_head_map_t &m) {
+  return HeadMap{m.norm_weight, m.eps, m.positions, m.rotary_dim ? m.table : nullptr, m.table_positions,
+                 m.rotary_dim, m.interleaved, m.hadamard_n};
+}
+
+CacheView view(const fp4q_kv_cache_t &c) {
+  return CacheView{{c.k_codes, c.v_codes}, {c.k_scales, c.v_scales}, c.pages * c.page_size, kv_log2(c.page_size),
+                   c.page_stride, c.head_stride, c.token_stride};
+}
+
+bool ws_ok(const void *ws, size_t bytes) { return ws && bytes >= kWorkspaceBytes && kv_aligned(ws, 8); }
+
+}  // namespace
+}  // namespace fp4q
+
+using namespace fp4q;
+
+extern "C" fp4q_status_t fp4q_rotate_heads(const void *x, fp4q_dtype_t dtype, int64_t tokens, int64_t heads,
+                                           int64_t head_dim, int64_t token_stride, int64_t head_stride,
+                                           const fp4q_head_map_t *map, fp4q_dtype_t out_dtype, void *out,
+                                           void *workspace, size_t workspace_bytes, void *stream) {
+  const bool empty = tokens == 0 || heads == 0;
+  if (!map || (!empty && (!x || !out))) return FP4Q_ERR_NULL;
+  if (!ws_ok(workspace, workspace_bytes)) return FP4Q_ERR_WORKSPACE;
+  fp4q_status_t st = kv_check_heads(dtype, tokens, heads, head_dim, token_stride, head_stride, x);
+  if (st != FP4Q_OK) return st;
+  if (out_dtype != FP4Q_F32 && out_dtype != FP4Q_BF16) return FP4Q_ERR_ARG;
+  if ((st = kv_check_map(*map, head_dim, empty)) != FP4Q_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t *status = (uint32_t *)((char *)workspace + kWsStatus);
+  if (empty) {
+    hipLaunchKernelGGL(kv_status_kernel, dim3(1), dim3(64), 0, s, status);
+    return hip_status();
+  }
+  if (!kv_aligned(out, 16)) return FP4Q_ERR_ALIGN;
+  const int units = (int)(tokens * heads);
+  const HeadMap m = head_map(*map);
+  with_dim(head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    constexpr int U = kThreads / (D / kChunk);
+    const dim3 grid((unsigned)(((int64_t)units + U - 1) / U));
+    with_type(dtype, [&](auto tp) {
+      using T = std::remove_pointer_t<decltype(tp)>;
+      with_type(out_dtype, [&](auto op) {
+        using O = std::remove_pointer_t<decltype(op)>;
+        hipLaunchKernelGGL((rotate_heads_kernel<T, O, D>), grid, dim3(kThreads), 0, s, (const T *)x, units, (int)heads,
+                           token_stride, head_stride, m, (O *)out, status);
+      });
+    });
+  });
+  return hip_status();
+}
+
+extern "C" fp4q_status_t fp4q_kv_append_mxfp4(const fp4q_kv_cache_t *cache, const void *k, int64_t k_token_stride,
+                                              int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                                              int64_t v_head_stride, fp4q_dtype_t dtype, int64_t tokens,
+                                              const int64_t *slots, const fp4q_head_map_t *map, int off_lo,
+                                              int off_hi, void *workspace, size_t workspace_bytes, void *stream) {
+  if (!cache || !map || (tokens != 0 && (!k || !v || !slots))) return FP4Q_ERR_NULL;
+  if (!ws_ok(workspace, workspace_bytes)) return FP4Q_ERR_WORKSPACE;
+  if (off_lo > 0 || off_hi < 0 || off_lo < -16 || off_hi > 16) return FP4Q_ERR_ARG;
+  fp4q_status_t st = kv_check_cache(*cache);
+  if (st != FP4Q_OK) return st;
+  if ((st = kv_check_heads(dtype, tokens, cache->heads, cache->head_dim, k_token_stride, k_head_stride, k)) != FP4Q_OK)
+    return st;
+  if ((st = kv_check_heads(dtype, tokens, cache->heads, cache->head_dim, v_token_stride, v_head_stride, v)) != FP4Q_OK)
+    return st;
+  if ((st = kv_check_map(*map, cache->head_dim, tokens == 0)) != FP4Q_OK) return st;
+  if (tokens && !kv_aligned(slots, 8)) return FP4Q_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t *status = (uint32_t *)((char *)workspace + kWsStatus);
+  if (tokens == 0) {
+    hipLaunchKernelGGL(kv_status_kernel, dim3(1), dim3(64), 0, s, status);
+    return hip_status();
+  }
+  const AppendArgs a{{k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, slots,
+                     (int)(tokens * cache->heads), cache->heads, head_map(*map), off_lo, off_hi, view(*cache),
+                     status};
+  with_dim(cache->head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    constexpr int U = kThreads / (D / kChunk);
+    const dim3 grid((unsigned)(((int64_t)a.units + U - 1) / U), 2);
+    with_type(dtype, [&](auto tp) {
+      using T = std::remove_pointer_t<decltype(tp)>;
+      hipLaunchKernelGGL((kv_append_kernel<T, D>), grid, dim3(kThreads), 0, s, a);
+    });
+  });
+  return hip_status();
+}
+
+extern "C" fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *slots, int64_t tokens,
+                                            fp4q_dtype_t out_dtype, void *k_out, void *v_out, void *workspace,
+                                            size_t workspace_bytes, void *stream) {
+  if (!cache || (tokens != 0 && (!slots || (!k_out && !v_out)))) return FP4Q_ERR_NULL;
+  if (!ws_ok(workspace, workspace_bytes)) return FP4Q_ERR_WORKSPACE;
+  if (out_dtype != FP4Q_F32 && out_dtype != FP4Q_BF16) return FP4Q_ERR_ARG;
+  fp4q_status_t st = kv_check_cache(*cache);
+  if (st != FP4Q_OK) return st;
+  if (tokens < 0 || tokens * cache->heads >= kKvMaxUnits) return FP4Q_ERR_SHAPE;
+  if (tokens && (!kv_aligned(slots, 8) || !kv_aligned(k_out, 16) || !kv_aligned(v_out, 16))) return FP4Q_ERR_ALIGN;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t *status = (uint32_t *)((char *)workspace + kWsStatus);
+  if (tokens == 0) {
+    hipLaunchKernelGGL(kv_status_kernel, dim3(1), dim3(64), 0, s, status);
+    return hip_status();
+  }
+  const int units = (int)(tokens * cache->heads);
+  const CacheView c = view(*cache);
+  with_dim(cache->head_dim, [&](auto dc) {
+    constexpr int D = decltype(dc)::value;
+    constexpr int U = kThreads / (D / kChunk);
+    const dim3 grid((unsigned)(((int64_t)units + U - 1) / U), 2);
+    with_type(out_dtype, [&](auto op) {
+      using O = std::remove_pointer_t<decltype(op)>;
+      hipLaunchKernelGGL((kv_read_kernel<O, D>), grid, dim3(kThreads), 0, s, c, slots, units, cache->heads,
+                         (O *)k_out, (O *)v_out, status);
+    });
+  });
+  return hip_status();
+}

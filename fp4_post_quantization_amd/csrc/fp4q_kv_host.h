@@ -1,0 +1,169 @@
+// Argument checks and index arithmetic of the key/value cache calls: plain
+// C++ without HIP, so that a host program can exercise them; the functions
+// marked FP4Q_HD are the ones the kernels run.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "fp4q.h"
+#include "fp4q_kv.h"
+
+#ifdef __HIPCC__
+#define FP4Q_HD __host__ __device__ __forceinline__
+#else
+#define FP4Q_HD inline
+#endif
+
+namespace fp4q {
+
+constexpr int64_t kKvMaxUnits = (int64_t)1 << 30;  // (token, head) pairs of a call
+
+inline bool kv_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+inline int kv_log2(int64_t n) {
+  int k = 0;
+  while (((int64_t)1 << k) < n) ++k;
+  return k;
+}
+
+inline bool kv_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
+
+inline fp4q_status_t kv_check_heads(fp4q_dtype_t dtype, int64_t tokens, int64_t heads, int64_t head_dim,
+                                    int64_t token_stride, int64_t head_stride, const void *x) {
+  if (dtype != FP4Q_F32 && dtype != FP4Q_BF16) return FP4Q_ERR_ARG;
+  if (tokens < 0 || heads < 0 || heads > 65536 || !kv_head_dim_ok(head_dim)) return FP4Q_ERR_SHAPE;
+  if (tokens == 0 || heads == 0) return FP4Q_OK;
+  if (tokens >= kKvMaxUnits || tokens * heads >= kKvMaxUnits) return FP4Q_ERR_SHAPE;
+  const int64_t limit = (int64_t)1 << 40;  // so that no byte offset passes 63 bits
+  if (token_stride < 0 || head_stride < 0 || token_stride > limit || head_stride > limit) return FP4Q_ERR_SHAPE;
+  const int64_t size = dtype == FP4Q_BF16 ? 2 : 4;
+  if (!kv_aligned(x, 16) || token_stride * size % 16 || head_stride * size % 16) return FP4Q_ERR_ALIGN;
+  return FP4Q_OK;
+}
+
+inline fp4q_status_t kv_check_map(const fp4q_head_map_t &m, int64_t head_dim, bool empty) {
+  if (m.hadamard_n != 0 && m.hadamard_n != 16 && m.hadamard_n != 32 && m.hadamard_n != 64 && m.hadamard_n != 128)
+    return FP4Q_ERR_ARG;
+  if (m.hadamard_n > head_dim) return FP4Q_ERR_SHAPE;
+  if (m.interleaved != 0 && m.interleaved != 1) return FP4Q_ERR_ARG;
+  if (m.norm_weight && !(m.eps >= 0.0 && m.eps <= 1.7e308)) return FP4Q_ERR_ARG;
+  if (m.norm_weight && !kv_aligned(m.norm_weight, 16)) return FP4Q_ERR_ALIGN;
+  if (m.rotary_dim < 0 || m.rotary_dim > head_dim || m.rotary_dim % 16) return FP4Q_ERR_SHAPE;
+  if (m.rotary_dim) {
+    if (!m.table || (!m.positions && !empty)) return FP4Q_ERR_NULL;
+    if (m.table_positions < 1 || m.table_positions > ((int64_t)1 << 40)) return FP4Q_ERR_SHAPE;
+    if (!kv_aligned(m.table, 16) || !kv_aligned(m.positions, 8)) return FP4Q_ERR_ALIGN;
+  } else if (m.table) {
+    return FP4Q_ERR_SHAPE;
+  }
+  return FP4Q_OK;
+}
+
+// Rows of row_bytes bytes at the three strides do not overlap: taken from
+// the smallest stride up, each is at least the extent of what it repeats.
+inline bool kv_rows_apart(int64_t row_bytes, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
+  int64_t n[3] = {n0, n1, n2}, s[3] = {s0, s1, s2};
+  __int128 extent = row_bytes;
+  for (int k = 0; k < 3; ++k) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) break;
+    if ((__int128)s[at] < extent) return false;
+    extent += (__int128)s[at] * (n[at] - 1);
+    n[at] = 1;
+  }
+  return extent < ((__int128)1 << 62);
+}
+
+inline fp4q_status_t kv_check_cache(const fp4q_kv_cache_t &c) {
+  if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales) return FP4Q_ERR_NULL;
+  if (!kv_head_dim_ok(c.head_dim) || c.heads < 1 || (int64_t)c.heads * c.head_dim > 65536) return FP4Q_ERR_SHAPE;
+  if (c.page_size < 16 || c.page_size > 1024 || (c.page_size & (c.page_size - 1))) return FP4Q_ERR_SHAPE;
+  if (c.pages < 1 || c.pages > 0x7FFFFFFF) return FP4Q_ERR_SHAPE;
+  if (c.pages * c.page_size >= ((int64_t)1 << 40) / c.heads) return FP4Q_ERR_SHAPE;
+  if (c.page_stride < 0 || c.head_stride < 0 || c.token_stride < 0 || c.token_stride > ((int64_t)1 << 26))
+    return FP4Q_ERR_SHAPE;
+  if (!kv_rows_apart(c.head_dim / 2, c.pages, c.page_stride, c.heads, c.head_stride, c.page_size, c.token_stride))
+    return FP4Q_ERR_SHAPE;
+  if (!kv_aligned(c.k_codes, 16) || !kv_aligned(c.v_codes, 16) || c.page_stride % 16 || c.head_stride % 16 ||
+      c.token_stride % 16)
+    return FP4Q_ERR_ALIGN;
+  return FP4Q_OK;
+}
+
+// ------------------------------------------------- attention's work list ----
+
+struct AttnShape {
+  int64_t tokens;       // rows of q
+  int batch, groups;    // sequences; query heads per cache head
+  int heads;            // cache heads
+  int max_new, max_len; // host bounds on a sequence's new tokens and length
+  int causal, window;
+};
+
+// One sequence as the kernels see it: its values cut to what the call's
+// bounds allow, so that nothing derived from it leaves the given tensors.
+struct AttnSeq {
+  int64_t first;  // its first row of q
+  int fresh;      // its rows of q
+  int len;        // cached tokens
+  bool bad;       // a value had to be cut
+};
+
+FP4Q_HD AttnSeq attn_seq(const AttnShape &a, int len, int64_t begin, int64_t end) {
+  AttnSeq s;
+  s.bad = false;
+  if (len < 0 || len > a.max_len) {
+    s.bad = true;
+    len = len < 0 ? 0 : a.max_len;
+  }
+  if (begin < 0 || begin > a.tokens || end < begin || end > a.tokens || end - begin > a.max_new) {
+    s.bad = true;
+    begin = begin < 0 ? 0 : (begin > a.tokens ? a.tokens : begin);
+    end = end > a.tokens ? a.tokens : end;
+    end = end < begin ? begin : (end - begin > a.max_new ? begin + a.max_new : end);
+  }
+  s.first = begin;
+  s.fresh = (int)(end - begin);
+  s.len = len;
+  return s;
+}
+
+// Keys [lo, hi) that row token i of a sequence sees (empty where hi <= lo).
+FP4Q_HD int attn_hi(const AttnShape &a, const AttnSeq &s, int i) {
+  const int64_t p = (int64_t)s.len - s.fresh + i + 1;
+  return a.causal && p < s.len ? (p < 0 ? 0 : (int)p) : s.len;
+}
+FP4Q_HD int attn_lo(const AttnShape &a, const AttnSeq &s, int i) {
+  if (!a.window) return 0;
+  const int64_t p = (int64_t)s.len - s.fresh + i + 1 - a.window;
+  return p < 0 ? 0 : (p > s.len ? s.len : (int)p);
+}
+
+// Row tiles of a sequence (rows_per_tile of its fresh * groups rows each) and
+// the key tiles of tile_len tokens that any of its rows can see: key tiles
+// lo .. lo + n - 1, at least one, so that every row tile is somebody's work.
+struct AttnWork {
+  int64_t row_tiles;
+  int lo, n;
+};
+FP4Q_HD AttnWork attn_work(const AttnShape &a, const AttnSeq &s, int rows_per_tile, int tile_len) {
+  AttnWork w;
+  w.row_tiles = ((int64_t)s.fresh * a.groups + rows_per_tile - 1) / rows_per_tile;
+  w.lo = attn_lo(a, s, 0) / tile_len;
+  const int hi = s.fresh ? attn_hi(a, s, s.fresh - 1) : 0;
+  w.n = (int)(((int64_t)hi + tile_len - 1) / tile_len) - w.lo;
+  if (w.n < 1) w.n = 1;
+  return w;
+}
+
+// Work of all sequences laid end to end, in key tiles, is cut into `spans`
+// equal spans; span i is [attn_cut(i), attn_cut(i + 1)).
+FP4Q_HD int64_t attn_cut(int64_t total, int64_t spans, int64_t i) {
+  const int64_t q = total / spans, r = total % spans;
+  return q * i + (i < r ? i : r);
+}
+
+}  // namespace fp4q

@@ -18,7 +18,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr size_t kAttnHeader = 256;  // workspace: status word, then the partial results
+constexpr size_t kAttnHeader = 256;  // workspace: status word; then the spans' Joins, then partial results
+
+// What a span leaves for the joining kernel: the unit that begins in it and
+// ends in a later one (rows 0: there is none).
+struct Join {
+  int64_t first;  // the sequence's first row of q
+  int64_t row0;   // the row tile's first (token, head) row
+  int last, rows, head, pad;
+};
 
 struct AttnArgs {
   AttnShape sh;
@@ -34,6 +42,7 @@ struct AttnArgs {
   float *lse;
   uint32_t *status;
   float *parts;
+  Join *joins;  // [spans]
   int spans;  // work items of the split form; 0: one workgroup per (sequence, row tile, head)
 };
 
@@ -63,12 +72,15 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
 
-// The sequences' work, scanned by one wave 64 sequences at a time.
+// The sequences' work, scanned by one wave 64 sequences at a time; the first
+// 64 are scanned once.
 template <int ROWS, int TT>
 struct WorkScan {
   const AttnArgs &a;
   int lane;
   bool split;
+  int64_t mine0, sum0;
+  __device__ WorkScan(const AttnArgs &args, int l, bool sp) : a(args), lane(l), split(sp) { sum0 = scan(0, mine0); }
   __device__ int64_t scan(int base, int64_t &mine) const {  // inclusive prefix of this group
     mine = work_of<ROWS, TT>(a, base + lane, split);
     int64_t s = mine;
@@ -84,16 +96,15 @@ struct WorkScan {
     return (int64_t)(((uint64_t)hi << 32) | lo);
   }
   __device__ int64_t total() const {
-    int64_t t = 0, mine;
-    for (int base = 0; base < a.sh.batch; base += 64) t += lane_value(scan(base, mine), 63);
+    int64_t t = lane_value(sum0, 63), mine;
+    for (int base = 64; base < a.sh.batch; base += 64) t += lane_value(scan(base, mine), 63);
     return t;
   }
   // The sequence that position pos of the work falls in, and the position
   // within it; false past the end.
   __device__ bool find(int64_t pos, int &b, int64_t &off) const {
-    int64_t run = 0, mine;
-    for (int base = 0; base < a.sh.batch; base += 64) {
-      const int64_t s = scan(base, mine);
+    int64_t run = 0, mine = mine0, s = sum0;
+    for (int base = 0;;) {
       const uint64_t hit = __ballot(pos < run + s);
       if (hit) {
         const int l = __builtin_ctzll(hit);
@@ -102,8 +113,10 @@ struct WorkScan {
         return true;
       }
       run += lane_value(s, 63);
+      base += 64;
+      if (base >= a.sh.batch) return false;
+      s = scan(base, mine);
     }
-    return false;
   }
 };
 
@@ -378,20 +391,23 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
   const LaneAt<D> at(lane, a.token_stride);
   const WorkScan<ROWS, TT> scan{a, lane, a.spans != 0};
 
-  int64_t pos, end;
+  int64_t pos, end, total = 0;
   int64_t span = blockIdx.x;
+  Join join{0, 0, 0, 0, 0, 0};
   if (a.spans) {
-    const int64_t total = uniform64(scan.total());
+    total = uniform64(scan.total());
     pos = attn_cut(total, a.spans, span);
     end = attn_cut(total, a.spans, span + 1);
   } else {
     pos = span;
     end = span + 1;
   }
-  const int64_t start = pos;
   int b = 0;
   int64_t off = 0;
-  if (pos >= end || !scan.find(pos, b, off)) return;
+  if (pos >= end || !scan.find(pos, b, off)) {
+    if (a.spans && threadIdx.x == 0) a.joins[span] = join;
+    return;
+  }
   b = uniform(b);
   off = uniform64(off);
 
@@ -405,8 +421,8 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
       if (++b >= a.sh.batch) break;
       continue;
     }
-    const int64_t unit = off / tiles;
-    const int rt = uniform((int)(unit / a.sh.heads)), h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
+    const int64_t unit = attn_div(off, tiles);
+    const int rt = uniform((int)attn_div(unit, a.sh.heads)), h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
     int t0 = 0, t1 = wk.n;  // this workgroup's key tiles of the unit
     if (a.spans) {
       t0 = (int)(off - unit * tiles);
@@ -417,7 +433,9 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
     const bool whole = t0 == 0 && t1 == wk.n;
     const int64_t r0 = (int64_t)rt * ROWS, rows = (int64_t)sq.fresh * a.sh.groups;
     const int live = uniform((int)(rows - r0 < ROWS ? rows - r0 : ROWS));
-    const int i0 = uniform((int)(r0 / a.sh.groups)), i1 = uniform((int)((r0 + live - 1) / a.sh.groups));
+    if (!whole && t0 == 0)
+      join = Join{sq.first, r0, (int)attn_span_of(total, a.spans, pos + wk.n - 1), live, h, 0};
+    const int i0 = uniform((int)attn_div(r0, a.sh.groups)), i1 = uniform((int)attn_div(r0 + live - 1, a.sh.groups));
     // keys that all rows of the tile see
     const int all_lo = uniform(attn_lo(a.sh, sq, i1)), all_hi = uniform(attn_hi(a.sh, sq, i0));
     // keys that any row of the sequence sees
@@ -430,7 +448,7 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
     for (int r = 0; r < NR; ++r) {
       const int64_t row = r0 + 16 * r + n;
       const bool on = row < rows;
-      const int i = on ? (int)(row / a.sh.groups) : i0;
+      const int i = on ? (int)attn_div(row, a.sh.groups) : i0;
       const int qh = h * a.sh.groups + (on ? (int)(row - (int64_t)i * a.sh.groups) : 0);
       load_query<D>(a.q + (sq.first + i) * a.q_st + qh * a.q_sh, on, g, q[r]);
       lo[r] = attn_lo(a.sh, sq, i);
@@ -531,7 +549,7 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
         if (whole) {
           const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
           const int64_t gr = r0 + 16 * r + row;
-          const int64_t i = gr / a.sh.groups;
+          const int64_t i = attn_div(gr, a.sh.groups);
           const int64_t head = (sq.first + i) * (a.sh.heads * a.sh.groups) + h * a.sh.groups + (gr - i * a.sh.groups);
           u32x4 w;
 #pragma unroll
@@ -556,15 +574,14 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
     pos += done;
     off += done;
   }
-  (void)start;
+  if (a.spans && threadIdx.x == 0) a.joins[span] = join;
   if (__builtin_expect(err != 0u, 0)) status.report(err);
 }
 
-// Joins the partial results of units that several spans share.  Workgroup
-// (w, row) looks whether a unit begins in span w and ends in a later one, and
-// joins that unit's row: span w's second slot, then the first slots of the
-// spans after it, in that order.
-template <int D, int ROWS, int TT>
+// Joins the partial results of units that several spans share: workgroup
+// (w, row) joins a row of the unit that begins in span w and ends in a later
+// one, from span w's second slot and the first slots of the spans after it.
+template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;  // elements of a lane
   __shared__ float so[4][D];
@@ -572,27 +589,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = wave_index();
   const int64_t span = blockIdx.x;
   const int row = blockIdx.y;
-  const WorkScan<ROWS, TT> scan{a, lane, true};
-  const int64_t total = uniform64(scan.total());
-  const int64_t start = attn_cut(total, a.spans, span), end = attn_cut(total, a.spans, span + 1);
-  if (start >= end) return;
-  int b = 0;
-  int64_t off = 0;
-  if (!scan.find(end - 1, b, off)) return;
-  b = uniform(b);
-  off = uniform64(off);
-  const AttnSeq sq = seq_of(a, b);
-  const AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
-  const int64_t unit = off / wk.n;
-  const int64_t begin = end - 1 - (off - unit * wk.n), stop = begin + wk.n;  // the unit's work
-  if (begin < start || stop <= end) return;
-  const int64_t rt = unit / a.sh.heads;
-  const int h = (int)(unit - rt * a.sh.heads);
-  const int64_t gr = rt * ROWS + row;
-  if (gr >= (int64_t)sq.fresh * a.sh.groups) return;
-  int64_t last = span + 1;  // the span that the unit ends in
-  while (attn_cut(total, a.spans, last + 1) < stop) ++last;
-
+  const Join j = a.joins[span];
+  if (row >= j.rows) return;
+  const int64_t last = j.last, gr = j.row0 + row;
   using P = Part<D, ROWS>;
   float m = kNegInf, l = 0.0f, o[PER];
 #pragma unroll
@@ -630,8 +629,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     y = fmaf(so[w][d + 1], f, y);
   }
   const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-  const int64_t i = gr / a.sh.groups;
-  const int64_t head = (sq.first + i) * (a.sh.heads * a.sh.groups) + h * a.sh.groups + (gr - i * a.sh.groups);
+  const int64_t i = attn_div(gr, a.sh.groups);
+  const int64_t head = (j.first + i) * (a.sh.heads * a.sh.groups) + j.head * a.sh.groups + (gr - i * a.sh.groups);
   reinterpret_cast<uint32_t *>(a.out)[(head * D + d) / 2] = pack_bf16(x * inv, y * inv);
   if (a.lse && d == 0) a.lse[head] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : (sum == 0.0f ? kNegInf : sum);
 }
@@ -684,8 +683,10 @@ void launch_rows(const AttnArgs &a, const Plan &p, hipStream_t s) {
   constexpr int NW = 4;
   if (p.spans) {
     hipLaunchKernelGGL((attn_rows_kernel<D, NR, NW>), dim3((unsigned)p.spans), dim3(64 * NW), 0, s, a);
-    hipLaunchKernelGGL((attn_join_kernel<D, 16 * NR, Geo<D>::TT>), dim3((unsigned)p.spans, 16 * NR), dim3(256), 0, s,
-                       a);
+    // no unit has more rows than a sequence
+    const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;
+    hipLaunchKernelGGL((attn_join_kernel<D, 16 * NR>), dim3((unsigned)p.spans, (unsigned)(rows < 16 * NR ? rows : 16 * NR)),
+                       dim3(256), 0, s, a);
   } else {
     hipLaunchKernelGGL((attn_rows_kernel<D, NR, NW>), dim3((unsigned)p.units), dim3(64 * NW), 0, s, a);
   }
@@ -699,7 +700,8 @@ using namespace fp4q;
 extern "C" size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads,
                                                        int64_t head_dim, int64_t max_new, int64_t max_len) {
   if (!sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
-  return kAttnHeader + 4 * (size_t)make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len).part_floats;
+  const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len);
+  return kAttnHeader + p.spans * sizeof(Join) + 4 * (size_t)p.part_floats;
 }
 
 extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, const void *q, int64_t q_token_stride,
@@ -762,7 +764,8 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   a.out = (uint16_t *)out;
   a.lse = lse;
   a.status = status;
-  a.parts = (float *)((char *)workspace + kAttnHeader);
+  a.joins = (Join *)((char *)workspace + kAttnHeader);
+  a.parts = (float *)(a.joins + p.spans);
   a.spans = p.spans;
   auto go = [&](auto dc) {
     constexpr int D = decltype(dc)::value;

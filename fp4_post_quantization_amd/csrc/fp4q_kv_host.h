@@ -159,11 +159,22 @@ FP4Q_HD AttnWork attn_work(const AttnShape &a, const AttnSeq &s, int rows_per_ti
   return w;
 }
 
+// Quotient of non-negative numbers, by the shorter division where both fit.
+FP4Q_HD int64_t attn_div(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
 // Work of all sequences laid end to end, in key tiles, is cut into `spans`
 // equal spans; span i is [attn_cut(i), attn_cut(i + 1)).
 FP4Q_HD int64_t attn_cut(int64_t total, int64_t spans, int64_t i) {
-  const int64_t q = total / spans, r = total % spans;
+  const int64_t q = attn_div(total, spans), r = total - q * spans;
   return q * i + (i < r ? i : r);
+}
+// The span that position pos (0 .. total - 1) lies in.
+FP4Q_HD int64_t attn_span_of(int64_t total, int64_t spans, int64_t pos) {
+  const int64_t q = attn_div(total, spans), r = total - q * spans;
+  const int64_t wide = r * (q + 1);
+  return pos < wide ? attn_div(pos, q + 1) : r + attn_div(pos - wide, q);
 }
 
 }  // namespace fp4q

@@ -196,6 +196,7 @@ extern "C" void keys(const int64_t *s, int64_t len, int64_t begin, int64_t end, 
   o[0] = attn_lo(a, q, (int)i); o[1] = attn_hi(a, q, (int)i);
 }
 extern "C" int64_t cut(int64_t total, int64_t spans, int64_t i) { return attn_cut(total, spans, i); }
+extern "C" int64_t span_of(int64_t total, int64_t spans, int64_t p) { return attn_span_of(total, spans, p); }
 """
 
 
@@ -210,7 +211,8 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(so))
     P, I = ctypes.c_void_p, ctypes.c_int64
     lib.seq.argtypes, lib.keys.argtypes = [P, I, I, I, I, I, P], [P, I, I, I, I, P]
-    lib.cut.argtypes, lib.cut.restype = [I, I, I], I
+    for f in (lib.cut, lib.span_of):
+        f.argtypes, f.restype = [I, I, I], I
     return lib
 
 
@@ -264,3 +266,6 @@ def test_spans_cover_the_work_once(host):
             sizes = {b - a for a, b in zip(cuts, cuts[1:])}
             assert min(sizes) >= 0 and max(sizes) - min(sizes) <= 1
             assert sorted(cuts) == cuts
+            for i, (a, b) in enumerate(zip(cuts, cuts[1:])):
+                for p in {a, b - 1} if b > a else ():
+                    assert host.span_of(total, spans, p) == i

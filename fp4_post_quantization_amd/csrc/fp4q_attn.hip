@@ -53,9 +53,27 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
+// v, without the compiler knowing that it does not change: what is derived
+// from it is computed where it is used instead of being kept in registers
+// throughout a loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// In a block that few iterations enter: keeps the compiler from running it
+// in all of them and selecting afterwards.
+__device__ __forceinline__ void not_speculated() { asm volatile(""); }
+
 __device__ __forceinline__ AttnSeq seq_of(const AttnArgs &a, int b) {
   const int64_t begin = a.cu ? a.cu[b] : b, end = a.cu ? a.cu[b + 1] : b + 1;
   return attn_seq(a.sh, a.lens[b], begin, end);
+}
+
+// The same for a sequence that is the same in every lane.
+__device__ __forceinline__ AttnSeq seq_of_uniform(const AttnArgs &a, int b) {
+  const int begin = a.cu ? uniform(a.cu[b]) : b, end = a.cu ? uniform(a.cu[b + 1]) : b + 1;
+  return attn_seq(a.sh, uniform(a.lens[b]), begin, end);
 }
 
 // Work of sequence b: (row tile, head) units times its key tiles (split
@@ -64,7 +82,7 @@ template <int ROWS, int TT>
 __device__ __forceinline__ int64_t work_of(const AttnArgs &a, int b, bool split) {
   if (b >= a.sh.batch) return 0;
   const AttnWork w = attn_work(a.sh, seq_of(a, b), ROWS, TT);
-  return w.row_tiles * a.sh.heads * (split ? w.n : 1);
+  return w.row_tiles * a.sh.heads * (split ? w.n + kUnitCost : 1);
 }
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
@@ -126,7 +144,7 @@ struct Geo {
   static constexpr int KW = D == 64 ? 2 : 4;     // dwords (8 elements) of a piece
   static constexpr int QS = KP * KW;             // 32-element steps of a score
   static constexpr int DT = D / 16;              // output tiles; lane c of 16 owns elements c DT .. c DT + DT - 1
-  static constexpr int TT = D == 256 ? 32 : 64;  // tokens of a key tile
+  static constexpr int TT = 32;                  // tokens of a key tile
   static constexpr int TG = TT / 16;
   using KT = std::conditional_t<D == 64, u32x2, u32x4>;
   using VT = std::conditional_t<D == 64, uint16_t, std::conditional_t<D == 128, uint32_t, u32x2>>;
@@ -153,7 +171,6 @@ struct KvTile {
 template <int D>
 struct LaneAt {
   uint32_t k, ks, v, vs;
-  uint32_t v_step, vs_step;  // from load j to j + 1
   __device__ LaneAt(int lane, int64_t token_stride) {
     const uint32_t m = lane & 15, g = lane >> 4, ts = (uint32_t)token_stride;
     const uint32_t kt = (m & 3) * 4 + (m >> 2);
@@ -161,8 +178,6 @@ struct LaneAt {
     ks = kt * (ts / 16) + (D == 64 ? g / 2 : g);
     v = g * ts + m * (D / 32);
     vs = g * (ts / 16) + m * Geo<D>::DT / 32;
-    v_step = 4 * ts;
-    vs_step = 4 * (ts / 16);
   }
 };
 
@@ -170,20 +185,22 @@ template <int D>
 __device__ __forceinline__ void load_tile(const AttnArgs &a, const LaneAt<D> &at, int64_t head_off, int token0,
                                           const int (&page)[Geo<D>::TG], KvTile<D> &t) {
   using G = Geo<D>;
+  // 32-bit offsets from uniform bases, opaque so that they are not widened to 64-bit registers outside the loop
+  const uint32_t k_at = opaque(at.k), ks_at = opaque(at.ks), v_at = opaque(at.v), vs_at = opaque(at.vs);
 #pragma unroll
   for (int tg = 0; tg < G::TG; ++tg) {
     const int r = (token0 + 16 * tg) & ((1 << a.log_page) - 1);
     const int64_t off = head_off + (int64_t)page[tg] * a.page_stride + r * a.token_stride;
-    const uint8_t *kc = a.kc + off, *vc = a.vc + off, *ks = a.ks + off / 16, *vs = a.vs + off / 16;
+    const uint8_t *kc = a.kc + off, *vc = a.vc + off, *ks = a.ks + (off >> 4), *vs = a.vs + (off >> 4);
 #pragma unroll
     for (int p = 0; p < G::KP; ++p) {
-      t.k[tg][p] = *reinterpret_cast<const typename G::KT *>(kc + at.k + p * 64);
-      t.ks[tg][p] = ks[at.ks + p * 4];
+      t.k[tg][p] = *reinterpret_cast<const typename G::KT *>(kc + (k_at + p * 64u));
+      t.ks[tg][p] = ks[ks_at + p * 4u];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      t.v[tg][j] = *reinterpret_cast<const typename G::VT *>(vc + at.v + j * at.v_step);
-      t.vs[tg][j] = vs[at.vs + j * at.vs_step];
+      t.v[tg][j] = *reinterpret_cast<const typename G::VT *>((vc + 4 * j * a.token_stride) + v_at);
+      t.vs[tg][j] = (vs + j * (a.token_stride >> 2))[vs_at];
     }
   }
 }
@@ -268,15 +285,24 @@ __device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> 
     for (int tg = 0; tg < G::TG; ++tg) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float v = s[r][tg][i] * a.scale_log2;
-        if (!full) {
-          const int tok = token0 + 16 * tg + 4 * i + g;
-          v = (tok >= lo[r]) & (tok < hi[r]) & ((groups_ok >> tg) & 1u) ? v : kNegInf;
-        }
-        s[r][tg][i] = v;
-        mx = fmaxf(mx, v);
+        s[r][tg][i] *= a.scale_log2;
       }
     }
+    if (!full) {
+      not_speculated();
+#pragma unroll
+      for (int tg = 0; tg < G::TG; ++tg) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = token0 + 16 * tg + 4 * i + g;
+          s[r][tg][i] = (tok >= lo[r]) & (tok < hi[r]) & ((groups_ok >> tg) & 1u) ? s[r][tg][i] : kNegInf;
+        }
+      }
+    }
+#pragma unroll
+    for (int tg = 0; tg < G::TG; ++tg)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[r][tg][i]);
     // the running maximum moves only when a score passes it by more than 2^8: until then the exponentials stay
     // below 2^8, and neither the sum nor the outputs need rescaling
     if (__ballot(mx > st[r].m + 8.0f)) {
@@ -312,10 +338,14 @@ __device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> 
       const int tg = 2 * h + j / 4;
       v[j] = t.v[tg][j & 3];
       vs[j] = as_f(t.vs[tg][j & 3] << 23);
-      if (!full) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
+    }
+    if (!full) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
+      not_speculated();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int tg = 2 * h + j / 4;
         const int tok = token0 + 16 * tg + 4 * (j & 3) + g;
-        const bool in = (tok >= keys_lo) & (tok < keys_hi) & ((groups_ok >> tg) & 1u);
-        if (!in) {
+        if (!((tok >= keys_lo) & (tok < keys_hi) & ((groups_ok >> tg) & 1u))) {
           v[j] = typename G::VT{};
           vs[j] = 1.0f;
         }
@@ -371,15 +401,18 @@ __device__ __forceinline__ float part_weight(float m, float top) {
   return m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
 }
 
+// Waves of a SIMD that the registers of a variant leave room for.
+constexpr int waves_per_simd(int dim, int nr) { return nr == 1 && dim <= 128 ? 2 : 1; }
+
 // Row r of a sequence's row tile: token i = r / groups, query head of group r % groups.
 template <int D, int NR, int NW>
-__global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kernel(AttnArgs a) {
   using G = Geo<D>;
   constexpr int ROWS = 16 * NR, TT = G::TT, TG = G::TG;
   constexpr int LD = D + 4;  // padded row of the merge buffer
   __shared__ __align__(16) float mo[NW][16][LD];
   __shared__ float mm[NW][16], ml[NW][16];
-  const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = wave_index();
   const Status status{a.status, true};
   if (blockIdx.x == 0 && wave == 0) {  // takes the status slot, and checks every sequence's length and rows
     bool bad = false;
@@ -393,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
 
   int64_t pos, end, total = 0;
   int64_t span = blockIdx.x;
-  Join join{0, 0, 0, 0, 0, 0};
+  bool joined = false;  // this span's Join is written
   if (a.spans) {
     total = uniform64(scan.total());
     pos = attn_cut(total, a.spans, span);
@@ -405,52 +438,56 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
   int b = 0;
   int64_t off = 0;
   if (pos >= end || !scan.find(pos, b, off)) {
-    if (a.spans && threadIdx.x == 0) a.joins[span] = join;
+    if (a.spans && threadIdx.x == 0) a.joins[span] = Join{0, 0, 0, 0, 0, 0};
     return;
   }
   b = uniform(b);
   off = uniform64(off);
 
   while (pos < end) {
-    AttnSeq sq = seq_of(a, b);
-    AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
-    const int64_t tiles = a.spans ? wk.n : 1;
+    const AttnSeq sq = seq_of_uniform(a, b);
+    const AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
+    const int64_t size = a.spans ? wk.n + kUnitCost : 1;  // of a unit
     const int64_t units = wk.row_tiles * a.sh.heads;
-    if (off >= units * tiles) {  // on to the next sequence that has rows
+    if (off >= units * size) {  // on to the next sequence that has rows
       off = 0;
       if (++b >= a.sh.batch) break;
       continue;
     }
-    const int64_t unit = attn_div(off, tiles);
+    const int64_t unit = attn_div(off, size);
     const int rt = uniform((int)attn_div(unit, a.sh.heads)), h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
-    int t0 = 0, t1 = wk.n;  // this workgroup's key tiles of the unit
-    if (a.spans) {
-      t0 = (int)(off - unit * tiles);
-      t1 = (int)(end - pos < tiles - t0 ? t0 + (end - pos) : tiles);
-    }
-    t0 = uniform(t0);
-    t1 = uniform(t1);
+    const int64_t from = off - unit * size, here = end - pos < size - from ? end - pos : size - from;
+    AttnPart part{0, wk.n};  // this workgroup's key tiles of the unit
+    if (a.spans) part = attn_part(from, from + here, wk.n);
+    pos += here;
+    off += here;
+    const int t0 = uniform(part.t0), t1 = uniform(part.t1);
+    if (t0 == t1) continue;
     const bool whole = t0 == 0 && t1 == wk.n;
     const int64_t r0 = (int64_t)rt * ROWS, rows = (int64_t)sq.fresh * a.sh.groups;
     const int live = uniform((int)(rows - r0 < ROWS ? rows - r0 : ROWS));
-    if (!whole && t0 == 0)
-      join = Join{sq.first, r0, (int)attn_span_of(total, a.spans, pos + wk.n - 1), live, h, 0};
+    if (!whole && t0 == 0) {
+      joined = true;
+      if (threadIdx.x == 0)
+        a.joins[span] = Join{sq.first, r0, (int)attn_span_of(total, a.spans, pos - here - from + size - 1), live, h, 0};
+    }
     const int i0 = uniform((int)attn_div(r0, a.sh.groups)), i1 = uniform((int)attn_div(r0 + live - 1, a.sh.groups));
     // keys that all rows of the tile see
     const int all_lo = uniform(attn_lo(a.sh, sq, i1)), all_hi = uniform(attn_hi(a.sh, sq, i0));
     // keys that any row of the sequence sees
     const int keys_lo = uniform(attn_lo(a.sh, sq, 0)), keys_hi = uniform(attn_hi(a.sh, sq, sq.fresh - 1));
 
+    const int ln = opaque(lane), ng = ln >> 4, nn = ln & 15;
     QFrag<D> q[NR];
     RowState<D> st[NR];
     int lo[NR], hi[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int64_t row = r0 + 16 * r + n;
+      const int64_t row = r0 + 16 * r + nn;
       const bool on = row < rows;
       const int i = on ? (int)attn_div(row, a.sh.groups) : i0;
       const int qh = h * a.sh.groups + (on ? (int)(row - (int64_t)i * a.sh.groups) : 0);
-      load_query<D>(a.q + (sq.first + i) * a.q_st + qh * a.q_sh, on, g, q[r]);
+      load_query<D>(a.q + (sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q[r]);
       lo[r] = attn_lo(a.sh, sq, i);
       hi[r] = attn_hi(a.sh, sq, i);
 #pragma unroll
@@ -467,10 +504,10 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
     // lane i holds the page of the i-th group of 16 tokens of a block of 64 groups; -1: none
     constexpr int BLOCK = 64 / TG;  // key tiles of it
     auto pages_of = [&](int tile) {
-      const int64_t tok = (int64_t)(wk.lo + tile) * TT + 16 * lane;
+      const int tok = (wk.lo + tile) * TT + 16 * lane;  // below 2^30 + 64 * 16
       int id = -1;
       if (tile < w1 && tok < keys_hi && tok + 15 >= keys_lo) {
-        id = row_table[tok >> a.log_page];
+        id = row_table[(uint32_t)(tok >> a.log_page)];
         if (id < 0 || id >= a.pages) {
           err |= FP4Q_DATA_BAD_TABLE;
           id = -1;
@@ -492,10 +529,10 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
     if (w0 < w1) {
       int first = w0;
       int ids = pages_of(first), ids_next = pages_of(first + BLOCK);
-      KvTile<D> cur, nxt;
-      uint32_t ok, ok_next = 0u;
-      fetch(w0, ids, first, cur, ok);
-      for (int tile = w0; tile < w1; ++tile) {
+      KvTile<D> even, odd;
+      uint32_t ok_even, ok_odd = 0u;
+      fetch(w0, ids, first, even, ok_even);
+      auto step = [&](int tile, const KvTile<D> &cur, uint32_t ok, KvTile<D> &nxt, uint32_t &ok_next) {
         if (tile + 1 < w1) {
           if (tile + 1 == first + BLOCK) {
             first += BLOCK;
@@ -507,30 +544,33 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
         const int token0 = (wk.lo + tile) * TT;
         const bool full = ok == (1u << TG) - 1u && token0 >= all_lo && token0 + TT <= all_hi;
         consume_tile<D, NR>(a, cur, q, lo, hi, token0, full, ok, keys_lo, keys_hi, lane, st);
-        cur = nxt;
-        ok = ok_next;
+      };
+      for (int tile = w0; tile < w1; tile += 2) {
+        step(tile, even, ok_even, odd, ok_odd);
+        if (tile + 1 < w1) step(tile + 1, odd, ok_odd, even, ok_even);
       }
     }
 
     // merge the waves, 16 rows at a time
+    const int mt = opaque((int)threadIdx.x), mn = mt & 15, mg = (mt >> 4) & 3;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       float l = st[r].l;
       l += xor16(l);
       l += xor32(l);
-      if (g == 0) {
-        mm[wave][n] = st[r].m;
-        ml[wave][n] = l;
+      if (mg == 0) {
+        mm[wave][mn] = st[r].m;
+        ml[wave][mn] = l;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int dt = 0; dt < G::DT; dt += 4)
-          *reinterpret_cast<f32x4 *>(&mo[wave][n][(4 * g + i) * G::DT + dt]) =
+          *reinterpret_cast<f32x4 *>(&mo[wave][mn][(4 * mg + i) * G::DT + dt]) =
               f32x4{st[r].o[dt][i], st[r].o[dt + 1][i], st[r].o[dt + 2][i], st[r].o[dt + 3][i]};
       __syncthreads();
       // 8 elements of a row a thread
-      for (int e = threadIdx.x; e < 16 * D / 8; e += 64 * NW) {
+      for (int e = mt; e < 16 * D / 8; e += 64 * NW) {
         const int row = e / (D / 8), d = e % (D / 8) * 8;
         if (16 * r + row >= live) continue;
         float top = mm[0][row];
@@ -570,11 +610,8 @@ __global__ __launch_bounds__(64 * NW, NW <= 4 && NR == 1 ? 2 : 1) void attn_rows
       }
       __syncthreads();
     }
-    const int64_t done = a.spans ? t1 - t0 : 1;
-    pos += done;
-    off += done;
   }
-  if (a.spans && threadIdx.x == 0) a.joins[span] = join;
+  if (a.spans && !joined && threadIdx.x == 0) a.joins[span] = Join{0, 0, 0, 0, 0, 0};
   if (__builtin_expect(err != 0u, 0)) status.report(err);
 }
 
@@ -640,8 +677,8 @@ __global__ __launch_bounds__(64) void attn_status_kernel(uint32_t *status) {
 }
 
 // ------------------------------------------------------------ dispatch ----
-constexpr int kSpans = 512;      // work items of the split form: two workgroups per CU
-constexpr int kDirectTiles = 16; // units of at most this many key tiles are not split
+constexpr int kCus = 256;
+constexpr int kDirectTiles = 32; // units of at most this many key tiles are not split
 
 struct Plan {
   int nr;         // row tiles of 16 a workgroup
@@ -654,16 +691,16 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
                int64_t max_len) {
   Plan p;
   const int64_t groups = q_heads / heads;
-  p.nr = max_new * groups <= 16 ? 1 : 2;
+  p.nr = max_new * groups <= 16 || head_dim == 256 ? 1 : 2;
   const int rows = 16 * p.nr;
-  const int64_t tile = head_dim == 256 ? 32 : 64;
+  const int64_t tile = 32;
   // a sequence's rows fill its tiles except the last one
   int64_t row_tiles = tokens * groups / rows + batch;
   const int64_t per_seq = (max_new * groups + rows - 1) / rows;
   if (row_tiles > batch * per_seq) row_tiles = batch * per_seq;
   p.units = row_tiles * heads;
   const bool direct = (max_len + tile - 1) / tile + 1 <= kDirectTiles;
-  p.spans = direct ? 0 : kSpans;
+  p.spans = direct ? 0 : kCus * waves_per_simd((int)head_dim, p.nr);  // as many workgroups as fit the chip at once
   p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * rows * (head_dim + 2);
   return p;
 }
@@ -769,7 +806,8 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   a.spans = p.spans;
   auto go = [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    if (p.nr == 1) launch_rows<D, 1>(a, p, s);
+    if constexpr (D == 256) launch_rows<D, 1>(a, p, s);
+    else if (p.nr == 1) launch_rows<D, 1>(a, p, s);
     else launch_rows<D, 2>(a, p, s);
   };
   if (cache->head_dim == 64) go(std::integral_constant<int, 64>{});

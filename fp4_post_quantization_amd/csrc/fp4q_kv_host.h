@@ -87,8 +87,10 @@ inline fp4q_status_t kv_check_cache(const fp4q_kv_cache_t &c) {
     return FP4Q_ERR_SHAPE;
   if (!kv_rows_apart(c.head_dim / 2, c.pages, c.page_stride, c.heads, c.head_stride, c.page_size, c.token_stride))
     return FP4Q_ERR_SHAPE;
-  if (!kv_aligned(c.k_codes, 16) || !kv_aligned(c.v_codes, 16) || c.page_stride % 16 || c.head_stride % 16 ||
-      c.token_stride % 16)
+  // a row's scales are read by whole dwords, or by halves of one that all lie alike in every page
+  const int64_t unit = c.head_dim / 2 < 64 ? c.head_dim / 2 : 64;
+  if (!kv_aligned(c.k_codes, 16) || !kv_aligned(c.v_codes, 16) || !kv_aligned(c.k_scales, unit / 16) ||
+      !kv_aligned(c.v_scales, unit / 16) || c.page_stride % 64 || c.head_stride % unit || c.token_stride % unit)
     return FP4Q_ERR_ALIGN;
   return FP4Q_OK;
 }
@@ -159,13 +161,29 @@ FP4Q_HD AttnWork attn_work(const AttnShape &a, const AttnSeq &s, int rows_per_ti
   return w;
 }
 
+// A unit of n key tiles takes n + kUnitCost of the work: besides its tiles it
+// costs a chain of dependent loads and a merge, about as long as that many
+// tiles take a workgroup.  Its first kUnitCost positions stand for them, so
+// the part of the unit within positions [from, to) is the tiles t0 .. t1 - 1.
+constexpr int kUnitCost = 8;
+struct AttnPart {
+  int t0, t1;
+};
+FP4Q_HD AttnPart attn_part(int64_t from, int64_t to, int n) {
+  AttnPart p;
+  from -= kUnitCost;
+  to -= kUnitCost;
+  p.t0 = from < 0 ? 0 : (from < n ? (int)from : n);
+  p.t1 = to < 0 ? 0 : (to < n ? (int)to : n);
+  return p;
+}
+
 // Quotient of non-negative numbers, by the shorter division where both fit.
 FP4Q_HD int64_t attn_div(int64_t a, int64_t b) {
   if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
   return a / b;
 }
-// Work of all sequences laid end to end, in key tiles, is cut into `spans`
-// equal spans; span i is [attn_cut(i), attn_cut(i + 1)).
+// Work of all sequences laid end to end is cut into `spans` equal spans; span i is [attn_cut(i), attn_cut(i + 1)).
 FP4Q_HD int64_t attn_cut(int64_t total, int64_t spans, int64_t i) {
   const int64_t q = attn_div(total, spans), r = total - q * spans;
   return q * i + (i < r ? i : r);

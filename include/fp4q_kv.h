@@ -46,8 +46,9 @@ extern "C" {
  *   codes of (p, h, r) start at p * page_stride + h * head_stride +
  *   r * token_stride (bytes), the same for keys and values; scales start at
  *   a sixteenth of that offset, so they lie in the same order as the codes.
- *   Strides are multiples of 16 and do not make rows overlap, the code
- *   pointers are 16-byte aligned, page_size is a power of two from 16 to
+ *   Strides are multiples of 64 (those of heads and rows of head_dim 64: of
+ *   32) and do not make rows overlap, the code pointers are 16-byte aligned
+ *   and the scale pointers 4-byte (head_dim 64: 2-byte), page_size is a power of two from 16 to
  *   1024, heads * head_dim at most 65536, and pages * page_size * heads below
  *   2^40.  Any byte may be in the rows that no token was written to. */
 typedef struct fp4q_kv_cache {

@@ -93,6 +93,8 @@ CACHE_FAULTS = [
     (dict(hs=64 * 32), "ERR_SHAPE"),                  # heads overlap
     (dict(ps=64 * 64), "ERR_SHAPE"),                  # pages overlap
     (dict(ts=72, hs=72 * 64, ps=72 * 128), "ERR_ALIGN"), (dict(kc=X + 4), "ERR_ALIGN"),
+    (dict(ts=80, hs=80 * 64, ps=80 * 128), "ERR_ALIGN"), (dict(ks=X + 2), "ERR_ALIGN"),
+    (dict(ps=64 * 2 * 64 + 32), "ERR_ALIGN"),
 ]
 
 
@@ -196,6 +198,10 @@ extern "C" void keys(const int64_t *s, int64_t len, int64_t begin, int64_t end, 
   o[0] = attn_lo(a, q, (int)i); o[1] = attn_hi(a, q, (int)i);
 }
 extern "C" int64_t cut(int64_t total, int64_t spans, int64_t i) { return attn_cut(total, spans, i); }
+extern "C" void part(int64_t from, int64_t to, int64_t n, int64_t *o) {
+  AttnPart p = attn_part(from, to, (int)n); o[0] = p.t0; o[1] = p.t1;
+}
+extern "C" int64_t unit_cost() { return kUnitCost; }
 extern "C" int64_t span_of(int64_t total, int64_t spans, int64_t p) { return attn_span_of(total, spans, p); }
 """
 
@@ -211,6 +217,7 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(so))
     P, I = ctypes.c_void_p, ctypes.c_int64
     lib.seq.argtypes, lib.keys.argtypes = [P, I, I, I, I, I, P], [P, I, I, I, I, P]
+    lib.part.argtypes, lib.unit_cost.restype = [I, I, I, P], I
     for f in (lib.cut, lib.span_of):
         f.argtypes, f.restype = [I, I, I], I
     return lib
@@ -269,3 +276,45 @@ def test_spans_cover_the_work_once(host):
             for i, (a, b) in enumerate(zip(cuts, cuts[1:])):
                 for p in {a, b - 1} if b > a else ():
                     assert host.span_of(total, spans, p) == i
+
+
+def test_units_of_spans_cover_every_tile_once_and_join(host):
+    """The walk of the attention kernel over its work: every key tile of every unit is taken by one span; the parts of
+    a unit that several spans share lie in the slots that the joining kernel reads, from the span that has its first
+    tile to the span that its work ends in."""
+    rng = np.random.default_rng(5)
+    cost, o = host.unit_cost(), np.zeros(2, dtype=np.int64)
+    for trial in range(60):
+        tiles = rng.integers(1, [2, 5, 40, 700][trial % 4] + 1, rng.integers(1, 60)).tolist()
+        spans = int(rng.choice([1, 2, 7, 64, 256]))
+        starts = np.concatenate([[0], np.cumsum([n + cost for n in tiles])])
+        total = int(starts[-1])
+        seen = [np.zeros(n, dtype=int) for n in tiles]
+        parts = {}   # slot -> unit, tiles
+        joins = {}
+        for s in range(spans):
+            pos, end = host.cut(total, spans, s), host.cut(total, spans, s + 1)
+            while pos < end:
+                u = int(np.searchsorted(starts, pos, side="right")) - 1
+                size, frm = tiles[u] + cost, pos - int(starts[u])
+                here = min(end - pos, size - frm)
+                host.part(frm, frm + here, tiles[u], o.ctypes.data)
+                t0, t1 = int(o[0]), int(o[1])
+                pos += here
+                if t0 == t1:
+                    continue
+                seen[u][t0:t1] += 1
+                if (t0, t1) != (0, tiles[u]):
+                    slot = 2 * s + (1 if t0 == 0 else 0)
+                    assert slot not in parts
+                    parts[slot] = (u, t1 - t0)
+                    if t0 == 0:
+                        assert s not in joins
+                        joins[s] = (u, host.span_of(total, spans, pos - here - frm + size - 1))
+        assert all((x == 1).all() for x in seen)
+        used = set()
+        for s, (u, last) in joins.items():
+            slots = [2 * s + 1] + [2 * k for k in range(s + 1, last + 1)]
+            assert sum(parts[k][1] for k in slots) == tiles[u] and all(parts[k][0] == u for k in slots)
+            used |= set(slots)
+        assert used == set(parts)

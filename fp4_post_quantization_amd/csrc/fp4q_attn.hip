@@ -13,6 +13,7 @@ namespace fp4q {
 namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -401,6 +402,119 @@ __device__ __forceinline__ float part_weight(float m, float top) {
   return m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
 }
 
+// A workgroup's part of a unit: key tiles lo + t0 .. lo + t1 - 1 of one
+// (sequence, row tile, head).
+struct Unit {
+  AttnSeq sq;
+  int64_t r0;            // first of the row tile's rows; row r is token r / groups, query head r % groups of the group
+  int b, h, live;        // sequence, head, rows
+  int lo, t0, t1;
+  int i0, i1;            // first and last token of the rows
+  int keys_lo, keys_hi;  // keys that any row of the sequence sees
+  bool whole;            // these are all key tiles of the unit
+};
+
+// The units of a workgroup, one after another: with a.spans those of its span
+// of the work, else the one with its number.
+template <int ROWS, int TT>
+struct Walk {
+  const AttnArgs &a;
+  int64_t pos, end, off, total;
+  int b;
+  bool joined;  // this span's Join is written
+
+  __device__ __forceinline__ Walk(const AttnArgs &args, int lane) : a(args), off(0), total(0), b(0), joined(false) {
+    const WorkScan<ROWS, TT> scan(a, lane, a.spans != 0);
+    pos = blockIdx.x;
+    end = pos + 1;
+    if (a.spans) {
+      total = uniform64(scan.total());
+      end = attn_cut(total, a.spans, pos + 1);
+      pos = attn_cut(total, a.spans, pos);
+    }
+    if (pos < end && !scan.find(pos, b, off)) end = pos;
+    b = uniform(b);
+    off = uniform64(off);
+  }
+
+  __device__ __forceinline__ bool next(Unit &u) {
+    while (pos < end) {
+      const AttnSeq sq = seq_of_uniform(a, b);
+      const AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
+      const int64_t size = a.spans ? wk.n + kUnitCost : 1;  // of a unit
+      if (off >= wk.row_tiles * a.sh.heads * size) {        // on to the next sequence that has rows
+        off = 0;
+        if (++b >= a.sh.batch) return false;
+        continue;
+      }
+      const int64_t unit = attn_div(off, size);
+      int rt = uniform((int)attn_div(unit, a.sh.heads));
+      const int h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
+      // causal: the last rows see the most keys; their workgroups start first
+      if (!a.spans) rt = (int)wk.row_tiles - 1 - rt;
+      const int64_t from = off - unit * size, here = end - pos < size - from ? end - pos : size - from;
+      AttnPart part{0, wk.n};
+      if (a.spans) part = attn_part(from, from + here, wk.n);
+      pos += here;
+      off += here;
+      u.t0 = uniform(part.t0);
+      u.t1 = uniform(part.t1);
+      if (u.t0 == u.t1) continue;
+      u.sq = sq;
+      u.b = b;
+      u.h = h;
+      u.lo = wk.lo;
+      u.whole = u.t0 == 0 && u.t1 == wk.n;
+      u.r0 = (int64_t)rt * ROWS;
+      const int64_t rows = (int64_t)sq.fresh * a.sh.groups;
+      u.live = uniform((int)(rows - u.r0 < ROWS ? rows - u.r0 : ROWS));
+      u.i0 = uniform((int)attn_div(u.r0, a.sh.groups));
+      u.i1 = uniform((int)attn_div(u.r0 + u.live - 1, a.sh.groups));
+      u.keys_lo = uniform(attn_lo(a.sh, sq, 0));
+      u.keys_hi = uniform(attn_hi(a.sh, sq, sq.fresh - 1));
+      if (!u.whole && u.t0 == 0) {
+        joined = true;
+        if (threadIdx.x == 0)
+          a.joins[blockIdx.x] =
+              Join{sq.first, u.r0, (int)attn_span_of(total, a.spans, pos - here - from + size - 1), u.live, u.h, 0};
+      }
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ void finish() const {
+    if (a.spans && !joined && threadIdx.x == 0) a.joins[blockIdx.x] = Join{0, 0, 0, 0, 0, 0};
+  }
+};
+
+// Position of row r of a unit among the rows of out and lse.
+__device__ __forceinline__ int64_t out_row(const AttnArgs &a, int64_t first, int h, int64_t r) {
+  const int64_t i = attn_div(r, a.sh.groups);
+  return (first + i) * (a.sh.heads * a.sh.groups) + h * a.sh.groups + (r - i * a.sh.groups);
+}
+__device__ __forceinline__ float row_factor(float sum) { return sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum); }
+__device__ __forceinline__ float row_lse(float m, float sum) {
+  return sum > 0.0f ? (m + log2f(sum)) * kLn2 : (sum == 0.0f ? kNegInf : sum);
+}
+
+// Taking the status slot, and checking every sequence's length and rows: the
+// first wave of the first workgroup.
+__device__ __forceinline__ void open_status(const AttnArgs &a, int lane, int wave) {
+  if (blockIdx.x != 0 || wave != 0) return;
+  bool bad = false;
+  for (int i = lane; i < a.sh.batch; i += 64) bad |= seq_of(a, i).bad;
+  const uint32_t bits = __ballot(bad) ? FP4Q_DATA_BAD_TABLE : 0u;
+  if (lane == 0) Status{a.status, true}.merge(bits);
+}
+
+// The page of token tok of a sequence, -1 where it is outside the cache.
+__device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_table, int tok, uint32_t &err) {
+  const int id = row_table[(uint32_t)(tok >> a.log_page)];
+  if (id >= 0 && id < a.pages) return id;
+  err |= FP4Q_DATA_BAD_TABLE;
+  return -1;
+}
+
 // Waves of a SIMD that the registers of a variant leave room for.
 constexpr int waves_per_simd(int dim, int nr) { return nr == 1 && dim <= 128 ? 2 : 1; }
 
@@ -413,83 +527,28 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
   __shared__ __align__(16) float mo[NW][16][LD];
   __shared__ float mm[NW][16], ml[NW][16];
   const int lane = threadIdx.x & 63, wave = wave_index();
-  const Status status{a.status, true};
-  if (blockIdx.x == 0 && wave == 0) {  // takes the status slot, and checks every sequence's length and rows
-    bool bad = false;
-    for (int i = lane; i < a.sh.batch; i += 64) bad |= seq_of(a, i).bad;
-    const uint32_t bits = __ballot(bad) ? FP4Q_DATA_BAD_TABLE : 0u;
-    if (lane == 0) status.merge(bits);
-  }
+  open_status(a, lane, wave);
   uint32_t err = 0u;
   const LaneAt<D> at(lane, a.token_stride);
-  const WorkScan<ROWS, TT> scan{a, lane, a.spans != 0};
-
-  int64_t pos, end, total = 0;
-  int64_t span = blockIdx.x;
-  bool joined = false;  // this span's Join is written
-  if (a.spans) {
-    total = uniform64(scan.total());
-    pos = attn_cut(total, a.spans, span);
-    end = attn_cut(total, a.spans, span + 1);
-  } else {
-    pos = span;
-    end = span + 1;
-  }
-  int b = 0;
-  int64_t off = 0;
-  if (pos >= end || !scan.find(pos, b, off)) {
-    if (a.spans && threadIdx.x == 0) a.joins[span] = Join{0, 0, 0, 0, 0, 0};
-    return;
-  }
-  b = uniform(b);
-  off = uniform64(off);
-
-  while (pos < end) {
-    const AttnSeq sq = seq_of_uniform(a, b);
-    const AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
-    const int64_t size = a.spans ? wk.n + kUnitCost : 1;  // of a unit
-    const int64_t units = wk.row_tiles * a.sh.heads;
-    if (off >= units * size) {  // on to the next sequence that has rows
-      off = 0;
-      if (++b >= a.sh.batch) break;
-      continue;
-    }
-    const int64_t unit = attn_div(off, size);
-    const int rt = uniform((int)attn_div(unit, a.sh.heads)), h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
-    const int64_t from = off - unit * size, here = end - pos < size - from ? end - pos : size - from;
-    AttnPart part{0, wk.n};  // this workgroup's key tiles of the unit
-    if (a.spans) part = attn_part(from, from + here, wk.n);
-    pos += here;
-    off += here;
-    const int t0 = uniform(part.t0), t1 = uniform(part.t1);
-    if (t0 == t1) continue;
-    const bool whole = t0 == 0 && t1 == wk.n;
-    const int64_t r0 = (int64_t)rt * ROWS, rows = (int64_t)sq.fresh * a.sh.groups;
-    const int live = uniform((int)(rows - r0 < ROWS ? rows - r0 : ROWS));
-    if (!whole && t0 == 0) {
-      joined = true;
-      if (threadIdx.x == 0)
-        a.joins[span] = Join{sq.first, r0, (int)attn_span_of(total, a.spans, pos - here - from + size - 1), live, h, 0};
-    }
-    const int i0 = uniform((int)attn_div(r0, a.sh.groups)), i1 = uniform((int)attn_div(r0 + live - 1, a.sh.groups));
+  Walk<ROWS, TT> walk(a, lane);
+  Unit u;
+  while (walk.next(u)) {
+    const int t0 = u.t0, t1 = u.t1;
     // keys that all rows of the tile see
-    const int all_lo = uniform(attn_lo(a.sh, sq, i1)), all_hi = uniform(attn_hi(a.sh, sq, i0));
-    // keys that any row of the sequence sees
-    const int keys_lo = uniform(attn_lo(a.sh, sq, 0)), keys_hi = uniform(attn_hi(a.sh, sq, sq.fresh - 1));
-
+    const int all_lo = uniform(attn_lo(a.sh, u.sq, u.i1)), all_hi = uniform(attn_hi(a.sh, u.sq, u.i0));
     const int ln = opaque(lane), ng = ln >> 4, nn = ln & 15;
     QFrag<D> q[NR];
     RowState<D> st[NR];
     int lo[NR], hi[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const int64_t row = r0 + 16 * r + nn;
-      const bool on = row < rows;
-      const int i = on ? (int)attn_div(row, a.sh.groups) : i0;
-      const int qh = h * a.sh.groups + (on ? (int)(row - (int64_t)i * a.sh.groups) : 0);
-      load_query<D>(a.q + (sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q[r]);
-      lo[r] = attn_lo(a.sh, sq, i);
-      hi[r] = attn_hi(a.sh, sq, i);
+      const bool on = 16 * r + nn < u.live;
+      const int64_t row = u.r0 + (on ? 16 * r + nn : 0);
+      const int i = (int)attn_div(row, a.sh.groups);
+      const int qh = u.h * a.sh.groups + (int)(row - (int64_t)i * a.sh.groups);
+      load_query<D>(a.q + (u.sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q[r]);
+      lo[r] = attn_lo(a.sh, u.sq, i);
+      hi[r] = attn_hi(a.sh, u.sq, i);
 #pragma unroll
       for (int dt = 0; dt < G::DT; ++dt) st[r].o[dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       st[r].m = kNegInf;
@@ -499,20 +558,14 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
     // the workgroup's tiles, a contiguous part for each wave
     const int nt = t1 - t0;
     const int w0 = t0 + (int)((int64_t)nt * wave / NW), w1 = t0 + (int)((int64_t)nt * (wave + 1) / NW);
-    const int64_t head_off = h * a.head_stride;
-    const int32_t *row_table = a.table + b * a.table_stride;
+    const int64_t head_off = u.h * a.head_stride;
+    const int32_t *row_table = a.table + u.b * a.table_stride;
     // lane i holds the page of the i-th group of 16 tokens of a block of 64 groups; -1: none
     constexpr int BLOCK = 64 / TG;  // key tiles of it
     auto pages_of = [&](int tile) {
-      const int tok = (wk.lo + tile) * TT + 16 * lane;  // below 2^30 + 64 * 16
+      const int tok = (u.lo + tile) * TT + 16 * lane;  // below 2^30 + 64 * 16
       int id = -1;
-      if (tile < w1 && tok < keys_hi && tok + 15 >= keys_lo) {
-        id = row_table[(uint32_t)(tok >> a.log_page)];
-        if (id < 0 || id >= a.pages) {
-          err |= FP4Q_DATA_BAD_TABLE;
-          id = -1;
-        }
-      }
+      if (tile < w1 && tok < u.keys_hi && tok + 15 >= u.keys_lo) id = page_of(a, row_table, tok, err);
       return id;
     };
     auto fetch = [&](int tile, int ids, int first, KvTile<D> &t, uint32_t &ok) {
@@ -524,7 +577,7 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
         ok |= id >= 0 ? 1u << tg : 0u;
         page[tg] = id < 0 ? 0 : id;
       }
-      load_tile<D>(a, at, head_off, (wk.lo + tile) * TT, page, t);
+      load_tile<D>(a, at, head_off, (u.lo + tile) * TT, page, t);
     };
     if (w0 < w1) {
       int first = w0;
@@ -541,9 +594,9 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
           }
           fetch(tile + 1, ids, first, nxt, ok_next);
         }
-        const int token0 = (wk.lo + tile) * TT;
+        const int token0 = (u.lo + tile) * TT;
         const bool full = ok == (1u << TG) - 1u && token0 >= all_lo && token0 + TT <= all_hi;
-        consume_tile<D, NR>(a, cur, q, lo, hi, token0, full, ok, keys_lo, keys_hi, lane, st);
+        consume_tile<D, NR>(a, cur, q, lo, hi, token0, full, ok, u.keys_lo, u.keys_hi, lane, st);
       };
       for (int tile = w0; tile < w1; tile += 2) {
         step(tile, even, ok_even, odd, ok_odd);
@@ -572,7 +625,7 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
       // 8 elements of a row a thread
       for (int e = mt; e < 16 * D / 8; e += 64 * NW) {
         const int row = e / (D / 8), d = e % (D / 8) * 8;
-        if (16 * r + row >= live) continue;
+        if (16 * r + row >= u.live) continue;
         float top = mm[0][row];
 #pragma unroll
         for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w][row]);
@@ -586,19 +639,17 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[k] = fmaf(mo[w][row][d + k], f, o[k]);
         }
-        if (whole) {
-          const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-          const int64_t gr = r0 + 16 * r + row;
-          const int64_t i = attn_div(gr, a.sh.groups);
-          const int64_t head = (sq.first + i) * (a.sh.heads * a.sh.groups) + h * a.sh.groups + (gr - i * a.sh.groups);
+        if (u.whole) {
+          const float inv = row_factor(sum);
+          const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + 16 * r + row);
           u32x4 w;
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
           *reinterpret_cast<u32x4 *>(a.out + head * D + d) = w;
-          if (a.lse && d == 0) a.lse[head] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : (sum == 0.0f ? kNegInf : sum);
+          if (a.lse && d == 0) a.lse[head] = row_lse(top, sum);
         } else {
           using P = Part<D, ROWS>;
-          const int64_t slot = 2 * span + (t0 == 0 ? 1 : 0);
+          const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);
           float *po = P::o(a.parts, slot) + (16 * r + row) * D + d;
           *reinterpret_cast<f32x4 *>(po) = f32x4{o[0], o[1], o[2], o[3]};
           *reinterpret_cast<f32x4 *>(po + 4) = f32x4{o[4], o[5], o[6], o[7]};
@@ -611,13 +662,312 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
       __syncthreads();
     }
   }
-  if (a.spans && !joined && threadIdx.x == 0) a.joins[span] = Join{0, 0, 0, 0, 0, 0};
-  if (__builtin_expect(err != 0u, 0)) status.report(err);
+  walk.finish();
+  if (__builtin_expect(err != 0u, 0)) Status{a.status, true}.report(err);
 }
 
-// Joins the partial results of units that several spans share: workgroup
-// (w, row) joins a row of the unit that begins in span w and ends in a later
-// one, from span w's second slot and the first slots of the spans after it.
+// ------------------------------------------------------------ prompts ----
+// Many rows: a workgroup of NW waves takes 32 NW rows, a wave 32 of them, and
+// the workgroup's waves share the key tiles (64 tokens) through LDS.  Scores
+// and outputs run on v_mfma_f32_32x32x16_bf16 in the transposed form, S^T =
+// K Q^T and O^T += V^T P^T: a lane's score registers are one query row's, so
+// the softmax needs one exchange, and they are P^T's operand as they lie.
+//  * Keys stay FP4 in LDS (a quarter of the reads); a lane decodes its own
+//    operand.  Key tile row m is token 16 (m / 16) + 8 (m / 4 % 2) + 4 (m / 8
+//    % 2) + m % 4, so that score register i of lane half h is token 16 (i / 8)
+//    + 8 h + i % 8: eight consecutive tokens for each step of the second
+//    product.
+//  * Values are decoded once for all waves and written transposed, [element]
+//    [token] bfloat16, 8 tokens (16 bytes) an operand.  Operand row m is
+//    element 16 (m / 4 % 2) + 4 (m / 8) + m % 4 of 32, so that a lane ends with
+//    16 consecutive elements of its row.
+// 16-byte pieces of both are swizzled so that 16 lanes that read or write
+// together fall on different banks.
+template <int D>
+struct PromptGeo {
+  static constexpr int TT = 64;
+  static constexpr int RB = D / 2;    // code bytes of a row
+  static constexpr int GR = D / 32;   // its pieces of 16 bytes, one scale block each
+  static constexpr int HG = GR / 2;   // pieces of a lane half
+  static constexpr int DT = D / 32;   // output tiles
+  static constexpr int ITEMS = 2 * D; // staging work: (row, piece) of keys, and (4 tokens, 8 elements) of values
+  // bytes of a buffer: keys, key scales, values
+  static constexpr int KS = TT * RB, V = KS + TT * GR, BUF = V + D * TT * 2;
+  static __device__ int key_piece(int row, int piece) { return piece ^ ((row / (8 / HG)) & (GR - 1)); }
+  static __device__ int value_swizzle(int d) {
+    return (((d >> 1) & 3) ^ (((d >> 3) & 1) | ((d >> 4) & 2))) | ((d >> 2) & 4);
+  }
+};
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_kernel(AttnArgs a) {
+  using G = PromptGeo<D>;
+  constexpr int TT = G::TT, M = 32 * NW, THREADS = 64 * NW;
+  constexpr int PT = (G::ITEMS + THREADS - 1) / THREADS;  // staging items of a thread
+  __shared__ __align__(16) uint8_t smem[2 * G::BUF];
+  const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 31, hh = lane >> 5;
+  open_status(a, lane, wave);
+  uint32_t err = 0u;
+  const float c = fmaxf(fabsf(a.scale_log2), 1e-30f);  // the sign of the scale goes into the queries
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+  const float slack = 8.0f / c;
+  // the lane's places in a buffer
+  const int kt = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+  const int vd = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
+  const int v_piece = hh ^ G::value_swizzle(vd);
+
+  Walk<M, TT> walk(a, lane);
+  Unit u;
+  while (walk.next(u)) {
+    // key tiles that the row tile's own rows see, and those of the wave's rows
+    const int see_lo = attn_lo(a.sh, u.sq, u.i0) / TT, see_hi = (attn_hi(a.sh, u.sq, u.i1) + TT - 1) / TT;
+    const int tb = uniform(max(u.lo + u.t0, see_lo)), te = uniform(min(u.lo + u.t1, see_hi));
+    const int w_rows = u.live - 32 * wave;  // of the wave: 32 or fewer, none where it is not positive
+    const int j0 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave : 0), a.sh.groups));
+    const int j1 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave + min(w_rows, 32) - 1 : 0), a.sh.groups));
+    const int some_lo = uniform(attn_lo(a.sh, u.sq, j0)), some_hi = uniform(w_rows > 0 ? attn_hi(a.sh, u.sq, j1) : 0);
+    const int all_lo = uniform(attn_lo(a.sh, u.sq, j1)), all_hi = uniform(attn_hi(a.sh, u.sq, j0));
+
+    const bool on = n < w_rows;
+    const int64_t row = u.r0 + (on ? 32 * wave + n : 0);
+    const int i = (int)attn_div(row, a.sh.groups);
+    const int lo = attn_lo(a.sh, u.sq, i), hi = attn_hi(a.sh, u.sq, i);
+    u32x4 q[G::HG * 4];
+    {
+      const uint16_t *qp = a.q + (u.sq.first + i) * a.q_st + (u.h * a.sh.groups + (row - (int64_t)i * a.sh.groups)) * a.q_sh;
+#pragma unroll
+      for (int x = 0; x < G::HG * 4; ++x) {
+        q[x] = u32x4{0u, 0u, 0u, 0u};
+        if (on) q[x] = *reinterpret_cast<const u32x4 *>(qp + hh * (D / 2) + 8 * x);
+        q[x] ^= flip;
+      }
+    }
+    f32x16 o[G::DT];
+#pragma unroll
+    for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[dt][x] = 0.0f;
+    float m = kNegInf, l = 0.0f;
+
+    const int64_t head_off = u.h * a.head_stride;
+    const int32_t *row_table = a.table + u.b * a.table_stride;
+    auto pages_of = [&](int tile) {  // lane i: the page of the i-th group of 16 tokens from the tile on; -1: none
+      const int tok = tile * TT + 16 * lane;
+      int id = -1;
+      if (tile < te && tok < u.keys_hi && tok + 15 >= u.keys_lo) id = page_of(a, row_table, tok, err);
+      return id;
+    };
+
+    // a tile's bytes on their way from memory to LDS
+    u32x4 kr[PT];
+    uint32_t kb[PT], vr[PT][4], vb[PT][4], ok_groups = 0u, ok_next = 0u;
+    auto fetch = [&](int tile, int ids, int first) {
+      const uint64_t bad = __ballot(ids < 0);
+      ok_next = ~(uint32_t)(bad >> (4 * (tile - first))) & 15u;
+#pragma unroll
+      for (int x = 0; x < PT; ++x) {
+        const int item = opaque((int)threadIdx.x) + x * THREADS;
+        if (G::ITEMS % THREADS == 0 || item < G::ITEMS) {
+          const int kr_row = item / G::GR, piece = item % G::GR;
+          const int kid = __shfl(ids, 4 * (tile - first) + kr_row / 16);
+          const int mask = (1 << a.log_page) - 1;
+          const int64_t ko = head_off + (int64_t)max(kid, 0) * a.page_stride +
+                             ((tile * TT + kr_row) & mask) * a.token_stride;
+          kr[x] = *reinterpret_cast<const u32x4 *>(a.kc + ko + piece * 16);
+          kb[x] = a.ks[(ko >> 4) + piece];
+          const int e8 = item % (D / 8), t4 = item / (D / 8);
+          const int vid = __shfl(ids, 4 * (tile - first) + t4 / 4);
+          const int64_t vo = head_off + (int64_t)max(vid, 0) * a.page_stride +
+                             ((tile * TT + 4 * t4) & mask) * a.token_stride;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            vr[x][j] = *reinterpret_cast<const uint32_t *>(a.vc + vo + j * a.token_stride + e8 * 4);
+            vb[x][j] = a.vs[((vo + j * a.token_stride) >> 4) + e8 / 4];
+          }
+        }
+      }
+    };
+    auto store = [&](int tile, uint8_t *buf) {
+      const bool inside = ok_next == 15u && tile * TT >= u.keys_lo && tile * TT + TT <= u.keys_hi;
+#pragma unroll
+      for (int x = 0; x < PT; ++x) {
+        const int item = opaque((int)threadIdx.x) + x * THREADS;
+        if (G::ITEMS % THREADS == 0 || item < G::ITEMS) {
+          const int kr_row = item / G::GR, piece = item % G::GR;
+          *reinterpret_cast<u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16) = kr[x];
+          buf[G::KS + item] = (uint8_t)kb[x];
+          const int e8 = item % (D / 8), t4 = item / (D / 8);
+          float sc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[j] = as_f(vb[x][j] << 23);
+          if (!inside) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
+            not_speculated();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int tok = tile * TT + 4 * t4 + j;
+              if (!((tok >= u.keys_lo) & (tok < u.keys_hi) & ((ok_next >> (t4 / 4)) & 1u))) {
+                vr[x][j] = 0u;
+                sc[j] = 1.0f;
+              }
+            }
+          }
+          uint8_t *vp = buf + G::V + e8 * 8 * (TT * 2);
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) {  // elements 2 e2 and 2 e2 + 1 of the item's 8
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[j] = e2 == 0   ? fp4x2_to_bf16<0>(vr[x][j], sc[j])
+                     : e2 == 1 ? fp4x2_to_bf16<1>(vr[x][j], sc[j])
+                     : e2 == 2 ? fp4x2_to_bf16<2>(vr[x][j], sc[j])
+                               : fp4x2_to_bf16<3>(vr[x][j], sc[j]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const int e = 2 * e2 + p;
+              const uint32_t sel = p ? 0x07060302u : 0x05040100u;
+              const u32x2 w = {__builtin_amdgcn_perm(y[1], y[0], sel), __builtin_amdgcn_perm(y[3], y[2], sel)};
+              const int at = ((t4 >> 1) ^ G::value_swizzle(e8 * 8 + e)) * 16 + (t4 & 1) * 8;
+              *reinterpret_cast<u32x2 *>(vp + e * (TT * 2) + at) = w;
+            }
+          }
+        }
+      }
+    };
+
+    auto consume = [&](int tile, const uint8_t *buf) {
+      const int token0 = tile * TT;
+      f32x16 s[2];
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) s[sub][x] = 0.0f;
+        const int kr_row = 32 * sub + kt;
+#pragma unroll
+        for (int p = 0; p < G::HG; ++p) {
+          const int piece = hh * G::HG + p;
+          const u32x4 kc = *reinterpret_cast<const u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16);
+          const float ks = as_f((uint32_t)buf[G::KS + kr_row * G::GR + piece] << 23);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                fp4x8_to_bf16(kc[w], ks), __builtin_bit_cast(bf16x8, q[4 * p + w]), s[sub], 0, 0, 0);
+        }
+      }
+      if (!(ok_groups == 15u && token0 >= all_lo && token0 + TT <= all_hi)) {
+        not_speculated();
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int tok = token0 + 32 * sub + 16 * (x / 8) + 8 * hh + x % 8;
+            s[sub][x] = (tok >= lo) & (tok < hi) & ((ok_groups >> (2 * sub + x / 8)) & 1u) ? s[sub][x] : kNegInf;
+          }
+      }
+      float mx = kNegInf;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) mx = fmaxf(mx, s[sub][x]);
+      // the running maximum moves only when a score passes it by more than 2^8 (see consume_tile)
+      if (__ballot(mx > m + slack)) {
+        mx = fmaxf(mx, xor32(mx));
+        const float top = fmaxf(m, mx);
+        const float shrink = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
+        m = top;
+        l *= shrink;
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[dt][x] *= shrink;
+      }
+      const float ref = m == kNegInf ? 0.0f : m * c;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          s[sub][x] = __builtin_amdgcn_exp2f(fmaf(s[sub][x], c, -ref));
+          l += s[sub][x];
+        }
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {  // 16 tokens each
+        u32x4 pw;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[st / 2][8 * (st & 1) + 2 * x], s[st / 2][8 * (st & 1) + 2 * x + 1]);
+        const bf16x8 pv = __builtin_bit_cast(bf16x8, pw);
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt) {
+          // the swizzle of element vd + 32 dt is vd's with bit 1 flipped where dt is odd
+          const int at = (v_piece ^ ((2 * st) ^ (2 * (dt & 1)))) * 16;
+          const u32x4 vv = *reinterpret_cast<const u32x4 *>(buf + G::V + (vd + 32 * dt) * (TT * 2) + at);
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv), pv, o[dt], 0, 0, 0);
+        }
+      }
+    };
+
+    if (tb < te) {
+      int first = tb;
+      int ids = pages_of(first), ids_next = pages_of(first + 16);
+      fetch(tb, ids, first);
+      store(tb, smem);
+      __syncthreads();
+      for (int tile = tb; tile < te; ++tile) {
+        uint8_t *cur = smem + ((tile - tb) & 1) * G::BUF, *nxt = smem + ((tile - tb + 1) & 1) * G::BUF;
+        ok_groups = ok_next;
+        if (tile + 1 < te) {
+          if (tile + 1 == first + 16) {
+            first += 16;
+            ids = ids_next;
+            ids_next = pages_of(first + 16);
+          }
+          fetch(tile + 1, ids, first);
+        }
+        if (tile * TT < some_hi && tile * TT + TT > some_lo) consume(tile, cur);
+        if (tile + 1 < te) store(tile + 1, nxt);
+        __syncthreads();
+      }
+    }
+
+    l += xor32(l);
+    const float top = m == kNegInf ? kNegInf : m * c;
+    if (on) {
+      if (u.whole) {
+        const float inv = row_factor(l);
+        const int64_t head = out_row(a, u.sq.first, u.h, row);
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt) {
+          u32x4 w[2];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = pack_bf16(o[dt][2 * x] * inv, o[dt][2 * x + 1] * inv);
+          u32x4 *p = reinterpret_cast<u32x4 *>(a.out + head * D + dt * 32 + hh * 16);
+          p[0] = w[0];
+          p[1] = w[1];
+        }
+        if (a.lse && hh == 0) a.lse[head] = row_lse(top, l);
+      } else {
+        using P = Part<D, M>;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (u.t0 == 0 ? 1 : 0);
+        const int pr = 32 * wave + n;
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<f32x4 *>(P::o(a.parts, slot) + pr * D + dt * 32 + hh * 16 + 4 * x) =
+                f32x4{o[dt][4 * x], o[dt][4 * x + 1], o[dt][4 * x + 2], o[dt][4 * x + 3]};
+        if (hh == 0) {
+          P::m(a.parts, slot)[pr] = top;
+          P::l(a.parts, slot)[pr] = l;
+        }
+      }
+    }
+  }
+  walk.finish();
+  if (__builtin_expect(err != 0u, 0)) Status{a.status, true}.report(err);
+}
+
+// Joins the partial results of units that several spans share: workgroups
+// (w, y) join the rows y, y + gridDim.y, ... of the unit that begins in span w
+// and ends in a later one, from span w's second slot and the first slots of
+// the spans after it.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int PER = D / 64;  // elements of a lane
@@ -625,51 +975,52 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   __shared__ float sm[4], sl[4];
   const int lane = threadIdx.x & 63, wave = wave_index();
   const int64_t span = blockIdx.x;
-  const int row = blockIdx.y;
   const Join j = a.joins[span];
-  if (row >= j.rows) return;
-  const int64_t last = j.last, gr = j.row0 + row;
-  using P = Part<D, ROWS>;
-  float m = kNegInf, l = 0.0f, o[PER];
+  const int64_t last = j.last;
+  for (int row = blockIdx.y; row < j.rows; row += gridDim.y) {
+    using P = Part<D, ROWS>;
+    float m = kNegInf, l = 0.0f, o[PER];
 #pragma unroll
-  for (int k = 0; k < PER; ++k) o[k] = 0.0f;
-  for (int64_t s = span + wave; s <= last; s += 4) {
-    const int64_t slot = 2 * s + (s == span ? 1 : 0);
-    const float pm = P::m(a.parts, slot)[row], pl = P::l(a.parts, slot)[row];
-    const float *po = P::o(a.parts, slot) + row * D + lane * PER;
-    float v[PER];
+    for (int k = 0; k < PER; ++k) o[k] = 0.0f;
+    for (int64_t s = span + wave; s <= last; s += 4) {
+      const int64_t slot = 2 * s + (s == span ? 1 : 0);
+      const float pm = P::m(a.parts, slot)[row], pl = P::l(a.parts, slot)[row];
+      const float *po = P::o(a.parts, slot) + row * D + lane * PER;
+      float v[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) v[k] = po[k];
-    const float top = fmaxf(m, pm);
-    const float f0 = part_weight(m, top), f1 = part_weight(pm, top);
-    m = top;
-    l = l * f0 + pl * f1;
+      for (int k = 0; k < PER; ++k) v[k] = po[k];
+      const float top = fmaxf(m, pm);
+      const float f0 = part_weight(m, top), f1 = part_weight(pm, top);
+      m = top;
+      l = l * f0 + pl * f1;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) o[k] = o[k] * f0 + v[k] * f1;
+      for (int k = 0; k < PER; ++k) o[k] = o[k] * f0 + v[k] * f1;
+    }
+    if (lane == 0) {
+      sm[wave] = m;
+      sl[wave] = l;
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) so[wave][lane * PER + k] = o[k];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+      float sum = 0.0f, x = 0.0f, y = 0.0f;
+      const int d = 2 * threadIdx.x;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = part_weight(sm[w], top);
+        sum = fmaf(sl[w], f, sum);
+        x = fmaf(so[w][d], f, x);
+        y = fmaf(so[w][d + 1], f, y);
+      }
+      const float inv = row_factor(sum);
+      const int64_t head = out_row(a, j.first, j.head, j.row0 + row);
+      reinterpret_cast<uint32_t *>(a.out)[(head * D + d) / 2] = pack_bf16(x * inv, y * inv);
+      if (a.lse && d == 0) a.lse[head] = row_lse(top, sum);
+    }
+    __syncthreads();
   }
-  if (lane == 0) {
-    sm[wave] = m;
-    sl[wave] = l;
-  }
-#pragma unroll
-  for (int k = 0; k < PER; ++k) so[wave][lane * PER + k] = o[k];
-  __syncthreads();
-  if (threadIdx.x >= D / 2) return;
-  float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float sum = 0.0f, x = 0.0f, y = 0.0f;
-  const int d = 2 * threadIdx.x;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = part_weight(sm[w], top);
-    sum = fmaf(sl[w], f, sum);
-    x = fmaf(so[w][d], f, x);
-    y = fmaf(so[w][d + 1], f, y);
-  }
-  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-  const int64_t i = attn_div(gr, a.sh.groups);
-  const int64_t head = (j.first + i) * (a.sh.heads * a.sh.groups) + j.head * a.sh.groups + (gr - i * a.sh.groups);
-  reinterpret_cast<uint32_t *>(a.out)[(head * D + d) / 2] = pack_bf16(x * inv, y * inv);
-  if (a.lse && d == 0) a.lse[head] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : (sum == 0.0f ? kNegInf : sum);
 }
 
 __global__ __launch_bounds__(64) void attn_status_kernel(uint32_t *status) {
@@ -681,7 +1032,7 @@ constexpr int kCus = 256;
 constexpr int kDirectTiles = 32; // units of at most this many key tiles are not split
 
 struct Plan {
-  int nr;         // row tiles of 16 a workgroup
+  int rows;       // of a row tile: 16 or 32 (attn_rows_kernel), 128 (attn_prompt_kernel)
   int64_t units;  // upper bound of (sequence, row tile, head) units
   int spans;
   int64_t part_floats;
@@ -691,17 +1042,17 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
                int64_t max_len) {
   Plan p;
   const int64_t groups = q_heads / heads;
-  p.nr = max_new * groups <= 16 || head_dim == 256 ? 1 : 2;
-  const int rows = 16 * p.nr;
-  const int64_t tile = 32;
+  p.rows = max_new * groups > 64 ? 128 : (max_new * groups <= 16 || head_dim == 256 ? 16 : 32);
+  const int64_t tile = p.rows == 128 ? 64 : 32;
   // a sequence's rows fill its tiles except the last one
-  int64_t row_tiles = tokens * groups / rows + batch;
-  const int64_t per_seq = (max_new * groups + rows - 1) / rows;
+  int64_t row_tiles = tokens * groups / p.rows + batch;
+  const int64_t per_seq = (max_new * groups + p.rows - 1) / p.rows;
   if (row_tiles > batch * per_seq) row_tiles = batch * per_seq;
   p.units = row_tiles * heads;
-  const bool direct = (max_len + tile - 1) / tile + 1 <= kDirectTiles;
-  p.spans = direct ? 0 : kCus * waves_per_simd((int)head_dim, p.nr);  // as many workgroups as fit the chip at once
-  p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * rows * (head_dim + 2);
+  const int64_t fit = kCus * (p.rows == 128 ? (head_dim == 256 ? 1 : 2) : waves_per_simd((int)head_dim, p.rows / 16));
+  const bool direct = (max_len + tile - 1) / tile + 1 <= kDirectTiles || (p.rows == 128 && p.units >= fit);
+  p.spans = direct ? 0 : (int)fit;  // as many workgroups as fit the chip at once
+  p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * p.rows * (head_dim + 2);
   return p;
 }
 
@@ -715,18 +1066,15 @@ bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int
 
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
 
-template <int D, int NR>
-void launch_rows(const AttnArgs &a, const Plan &p, hipStream_t s) {
-  constexpr int NW = 4;
-  if (p.spans) {
-    hipLaunchKernelGGL((attn_rows_kernel<D, NR, NW>), dim3((unsigned)p.spans), dim3(64 * NW), 0, s, a);
-    // no unit has more rows than a sequence
-    const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;
-    hipLaunchKernelGGL((attn_join_kernel<D, 16 * NR>), dim3((unsigned)p.spans, (unsigned)(rows < 16 * NR ? rows : 16 * NR)),
-                       dim3(256), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((attn_rows_kernel<D, NR, NW>), dim3((unsigned)p.units), dim3(64 * NW), 0, s, a);
-  }
+template <int D, int ROWS>
+void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.spans ? p.spans : p.units));
+  if constexpr (ROWS == 128) hipLaunchKernelGGL((attn_prompt_kernel<D, 4>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attn_rows_kernel<D, ROWS / 16, 4>), grid, dim3(256), 0, s, a);
+  if (!p.spans) return;
+  const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
+  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),
+                     dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -806,9 +1154,9 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   a.spans = p.spans;
   auto go = [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    if constexpr (D == 256) launch_rows<D, 1>(a, p, s);
-    else if (p.nr == 1) launch_rows<D, 1>(a, p, s);
-    else launch_rows<D, 2>(a, p, s);
+    if (p.rows == 128) launch<D, 128>(a, p, s);
+    else if (p.rows == 16) launch<D, 16>(a, p, s);
+    else if constexpr (D != 256) launch<D, 32>(a, p, s);
   };
   if (cache->head_dim == 64) go(std::integral_constant<int, 64>{});
   else if (cache->head_dim == 128) go(std::integral_constant<int, 128>{});

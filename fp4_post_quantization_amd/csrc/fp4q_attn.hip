@@ -699,6 +699,32 @@ struct PromptGeo {
   }
 };
 
+// Where a thread's staging items lie: offsets from their group of 16 tokens
+// in memory, and in a buffer.  Item x of thread t is number t + x threads:
+// piece item % GR of key row item / GR, and elements 8 (item % (D / 8)) .. of
+// the four tokens from 4 (item / (D / 8)) on.
+template <int D>
+struct StageAt {
+  using G = PromptGeo<D>;
+  uint32_t k, ks, v, vs;
+  uint32_t to_k, to_ks, to_v, v_piece;
+  __device__ StageAt(int tid, int64_t token_stride) {
+    const uint32_t ts = (uint32_t)token_stride;
+    // within the wave's rows, or the lane's group of 16 where the wave has two
+    const int in = tid % (64 < 16 * G::GR ? 64 : 16 * G::GR);
+    k = in / G::GR * ts + in % G::GR * 16;
+    ks = in / G::GR * (ts / 16) + in % G::GR;
+    const int e8 = tid % (D / 8), t4 = tid / (D / 8), iv = tid % (64 < 4 * (D / 8) ? 64 : 4 * (D / 8));
+    v = 4 * (iv / (D / 8)) * ts + e8 * 4;
+    vs = 4 * (iv / (D / 8)) * (ts / 16) + e8 / 4;
+    const int row = tid / G::GR;
+    to_k = row * G::RB + G::key_piece(row, tid % G::GR) * 16;
+    to_ks = G::KS + tid;
+    to_v = G::V + e8 * 8 * (G::TT * 2) + (t4 & 1) * 8;
+    v_piece = (t4 >> 1) ^ G::value_swizzle(e8 * 8);  // of the item's first element; (e / 2) flips its low bits
+  }
+};
+
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_kernel(AttnArgs a) {
   using G = PromptGeo<D>;
@@ -715,6 +741,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
   const int kt = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
   const int vd = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
   const int v_piece = hh ^ G::value_swizzle(vd);
+  const StageAt<D> at(threadIdx.x, a.token_stride);
 
   Walk<M, TT> walk(a, lane);
   Unit u;
@@ -764,71 +791,74 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
     auto fetch = [&](int tile, int ids, int first) {
       const uint64_t bad = __ballot(ids < 0);
       ok_next = ~(uint32_t)(bad >> (4 * (tile - first))) & 15u;
+      if (G::ITEMS < THREADS && 64 * wave >= G::ITEMS) return;
 #pragma unroll
       for (int x = 0; x < PT; ++x) {
-        const int item = opaque((int)threadIdx.x) + x * THREADS;
-        if (G::ITEMS % THREADS == 0 || item < G::ITEMS) {
-          const int kr_row = item / G::GR, piece = item % G::GR;
-          const int kid = __shfl(ids, 4 * (tile - first) + kr_row / 16);
-          const int mask = (1 << a.log_page) - 1;
-          const int64_t ko = head_off + (int64_t)max(kid, 0) * a.page_stride +
-                             ((tile * TT + kr_row) & mask) * a.token_stride;
-          kr[x] = *reinterpret_cast<const u32x4 *>(a.kc + ko + piece * 16);
-          kb[x] = a.ks[(ko >> 4) + piece];
-          const int e8 = item % (D / 8), t4 = item / (D / 8);
-          const int vid = __shfl(ids, 4 * (tile - first) + t4 / 4);
-          const int64_t vo = head_off + (int64_t)max(vid, 0) * a.page_stride +
-                             ((tile * TT + 4 * t4) & mask) * a.token_stride;
+        // the wave's 64 items of keys are 64 / GR rows, those of values as many tokens: part of one group of 16
+        // tokens, or (head_dim 64) two groups
+        auto group_off = [&](int g) {
+          const int id = __builtin_amdgcn_readlane(ids, 4 * (tile - first) + g);
+          return head_off + (int64_t)max(id, 0) * a.page_stride +
+                 ((tile * TT + 16 * g) & ((1 << a.log_page) - 1)) * a.token_stride;
+        };
+        const int row0 = (x * THREADS + 64 * wave) / G::GR;
+        int64_t off = group_off(row0 / 16) + (row0 % 16) * a.token_stride;
+        if constexpr (D == 64) {
+          const int64_t other = group_off(row0 / 16 + 1);
+          off = lane < 32 ? off : other;
+        }
+        const uint8_t *kc = a.kc + off, *ks = a.ks + (off >> 4), *vc = a.vc + off, *vs = a.vs + (off >> 4);
+        const uint32_t k_at = opaque(at.k), ks_at = opaque(at.ks), v_at = opaque(at.v), vs_at = opaque(at.vs);
+        kr[x] = *reinterpret_cast<const u32x4 *>(kc + k_at);
+        kb[x] = ks[ks_at];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            vr[x][j] = *reinterpret_cast<const uint32_t *>(a.vc + vo + j * a.token_stride + e8 * 4);
-            vb[x][j] = a.vs[((vo + j * a.token_stride) >> 4) + e8 / 4];
-          }
+        for (int j = 0; j < 4; ++j) {
+          vr[x][j] = *reinterpret_cast<const uint32_t *>((vc + j * a.token_stride) + v_at);
+          vb[x][j] = (vs + j * (a.token_stride >> 4))[vs_at];
         }
       }
     };
     auto store = [&](int tile, uint8_t *buf) {
+      if (G::ITEMS < THREADS && 64 * wave >= G::ITEMS) return;
       const bool inside = ok_next == 15u && tile * TT >= u.keys_lo && tile * TT + TT <= u.keys_hi;
 #pragma unroll
       for (int x = 0; x < PT; ++x) {
-        const int item = opaque((int)threadIdx.x) + x * THREADS;
-        if (G::ITEMS % THREADS == 0 || item < G::ITEMS) {
-          const int kr_row = item / G::GR, piece = item % G::GR;
-          *reinterpret_cast<u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16) = kr[x];
-          buf[G::KS + item] = (uint8_t)kb[x];
-          const int e8 = item % (D / 8), t4 = item / (D / 8);
-          float sc[4];
+        *reinterpret_cast<u32x4 *>(buf + at.to_k + x * (THREADS * 16)) = kr[x];
+        buf[at.to_ks + x * THREADS] = (uint8_t)kb[x];
+        float sc[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[j] = as_f(vb[x][j] << 23);
-          if (!inside) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
-            not_speculated();
+        for (int j = 0; j < 4; ++j) sc[j] = as_f(vb[x][j] << 23);
+        constexpr int T4X = THREADS / (D / 8);  // groups of 4 tokens from one x to the next
+        if (!inside) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
+          not_speculated();
+          const int t4 = x * T4X + threadIdx.x / (D / 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int tok = tile * TT + 4 * t4 + j;
-              if (!((tok >= u.keys_lo) & (tok < u.keys_hi) & ((ok_next >> (t4 / 4)) & 1u))) {
-                vr[x][j] = 0u;
-                sc[j] = 1.0f;
-              }
+          for (int j = 0; j < 4; ++j) {
+            const int tok = tile * TT + 4 * t4 + j;
+            if (!((tok >= u.keys_lo) & (tok < u.keys_hi) & ((ok_next >> (t4 / 4)) & 1u))) {
+              vr[x][j] = 0u;
+              sc[j] = 1.0f;
             }
           }
-          uint8_t *vp = buf + G::V + e8 * 8 * (TT * 2);
+        }
 #pragma unroll
-          for (int e2 = 0; e2 < 4; ++e2) {  // elements 2 e2 and 2 e2 + 1 of the item's 8
-            uint32_t y[4];
+        for (int e2 = 0; e2 < 4; ++e2) {  // elements 2 e2 and 2 e2 + 1 of the item's 8
+          uint32_t y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[j] = e2 == 0   ? fp4x2_to_bf16<0>(vr[x][j], sc[j])
-                     : e2 == 1 ? fp4x2_to_bf16<1>(vr[x][j], sc[j])
-                     : e2 == 2 ? fp4x2_to_bf16<2>(vr[x][j], sc[j])
-                               : fp4x2_to_bf16<3>(vr[x][j], sc[j]);
+          for (int j = 0; j < 4; ++j)
+            y[j] = e2 == 0   ? fp4x2_to_bf16<0>(vr[x][j], sc[j])
+                   : e2 == 1 ? fp4x2_to_bf16<1>(vr[x][j], sc[j])
+                   : e2 == 2 ? fp4x2_to_bf16<2>(vr[x][j], sc[j])
+                             : fp4x2_to_bf16<3>(vr[x][j], sc[j]);
+          // pieces of 8 tokens; from one x to the next the piece moves by a power of two that the swizzle leaves
+          // alone when it is added by an exclusive or
+          const uint32_t piece = at.v_piece ^ (uint32_t)((x * T4X / 2) ^ e2);
+          uint8_t *vp = buf + at.to_v + piece * 16;
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const int e = 2 * e2 + p;
-              const uint32_t sel = p ? 0x07060302u : 0x05040100u;
-              const u32x2 w = {__builtin_amdgcn_perm(y[1], y[0], sel), __builtin_amdgcn_perm(y[3], y[2], sel)};
-              const int at = ((t4 >> 1) ^ G::value_swizzle(e8 * 8 + e)) * 16 + (t4 & 1) * 8;
-              *reinterpret_cast<u32x2 *>(vp + e * (TT * 2) + at) = w;
-            }
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t sel = p ? 0x07060302u : 0x05040100u;
+            *reinterpret_cast<u32x2 *>(vp + (2 * e2 + p) * (TT * 2)) =
+                u32x2{__builtin_amdgcn_perm(y[1], y[0], sel), __builtin_amdgcn_perm(y[3], y[2], sel)};
           }
         }
       }

@@ -730,7 +730,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
   using G = PromptGeo<D>;
   constexpr int TT = G::TT, M = 32 * NW, THREADS = 64 * NW;
   constexpr int PT = (G::ITEMS + THREADS - 1) / THREADS;  // staging items of a thread
-  __shared__ __align__(16) uint8_t smem[2 * G::BUF];
+  __shared__ __align__(16) uint8_t smem[3 * G::BUF];
   const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 31, hh = lane >> 5;
   open_status(a, lane, wave);
   uint32_t err = 0u;
@@ -746,13 +746,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
   Walk<M, TT> walk(a, lane);
   Unit u;
   while (walk.next(u)) {
-    // key tiles that the row tile's own rows see, and those of the wave's rows
+    // key tiles that the row tile's own rows see
     const int see_lo = attn_lo(a.sh, u.sq, u.i0) / TT, see_hi = (attn_hi(a.sh, u.sq, u.i1) + TT - 1) / TT;
     const int tb = uniform(max(u.lo + u.t0, see_lo)), te = uniform(min(u.lo + u.t1, see_hi));
     const int w_rows = u.live - 32 * wave;  // of the wave: 32 or fewer, none where it is not positive
     const int j0 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave : 0), a.sh.groups));
     const int j1 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave + min(w_rows, 32) - 1 : 0), a.sh.groups));
-    const int some_lo = uniform(attn_lo(a.sh, u.sq, j0)), some_hi = uniform(w_rows > 0 ? attn_hi(a.sh, u.sq, j1) : 0);
     const int all_lo = uniform(attn_lo(a.sh, u.sq, j1)), all_hi = uniform(attn_hi(a.sh, u.sq, j0));
 
     const bool on = n < w_rows;
@@ -787,7 +786,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
 
     // a tile's bytes on their way from memory to LDS
     u32x4 kr[PT];
-    uint32_t kb[PT], vr[PT][4], vb[PT][4], ok_groups = 0u, ok_next = 0u;
+    uint32_t kb[PT], vr[PT][4], vb[PT][4], ok_next = 0u;
     auto fetch = [&](int tile, int ids, int first) {
       const uint64_t bad = __ballot(ids < 0);
       ok_next = ~(uint32_t)(bad >> (4 * (tile - first))) & 15u;
@@ -818,9 +817,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
         }
       }
     };
-    auto store = [&](int tile, uint8_t *buf) {
+    auto store = [&](int tile, uint8_t *buf, uint32_t ok) {
       if (G::ITEMS < THREADS && 64 * wave >= G::ITEMS) return;
-      const bool inside = ok_next == 15u && tile * TT >= u.keys_lo && tile * TT + TT <= u.keys_hi;
+      const bool inside = ok == 15u && tile * TT >= u.keys_lo && tile * TT + TT <= u.keys_hi;
 #pragma unroll
       for (int x = 0; x < PT; ++x) {
         *reinterpret_cast<u32x4 *>(buf + at.to_k + x * (THREADS * 16)) = kr[x];
@@ -835,7 +834,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int tok = tile * TT + 4 * t4 + j;
-            if (!((tok >= u.keys_lo) & (tok < u.keys_hi) & ((ok_next >> (t4 / 4)) & 1u))) {
+            if (!((tok >= u.keys_lo) & (tok < u.keys_hi) & ((ok >> (t4 / 4)) & 1u))) {
               vr[x][j] = 0u;
               sc[j] = 1.0f;
             }
@@ -864,40 +863,35 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       }
     };
 
-    auto consume = [&](int tile, const uint8_t *buf) {
-      const int token0 = tile * TT;
-      f32x16 s[2];
+    // scores of 32 tokens of a tile
+    auto scores = [&](const uint8_t *buf, int sub, f32x16 &s) {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
+      for (int x = 0; x < 16; ++x) s[x] = 0.0f;
+      const int kr_row = 32 * sub + kt;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) s[sub][x] = 0.0f;
-        const int kr_row = 32 * sub + kt;
+      for (int p = 0; p < G::HG; ++p) {
+        const int piece = hh * G::HG + p;
+        const u32x4 kc = *reinterpret_cast<const u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16);
+        const float ks = as_f((uint32_t)buf[G::KS + kr_row * G::GR + piece] << 23);
 #pragma unroll
-        for (int p = 0; p < G::HG; ++p) {
-          const int piece = hh * G::HG + p;
-          const u32x4 kc = *reinterpret_cast<const u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16);
-          const float ks = as_f((uint32_t)buf[G::KS + kr_row * G::GR + piece] << 23);
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            s[sub] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                fp4x8_to_bf16(kc[w], ks), __builtin_bit_cast(bf16x8, q[4 * p + w]), s[sub], 0, 0, 0);
-        }
+        for (int w = 0; w < 4; ++w)
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp4x8_to_bf16(kc[w], ks), __builtin_bit_cast(bf16x8, q[4 * p + w]),
+                                                      s, 0, 0, 0);
       }
-      if (!(ok_groups == 15u && token0 >= all_lo && token0 + TT <= all_hi)) {
+    };
+    // masks them and keeps the running maximum
+    auto settle = [&](int token0, uint32_t ok, f32x16 &s) {
+      if (!(ok == 3u && token0 >= all_lo && token0 + 32 <= all_hi)) {
         not_speculated();
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int tok = token0 + 32 * sub + 16 * (x / 8) + 8 * hh + x % 8;
-            s[sub][x] = (tok >= lo) & (tok < hi) & ((ok_groups >> (2 * sub + x / 8)) & 1u) ? s[sub][x] : kNegInf;
-          }
+        for (int x = 0; x < 16; ++x) {
+          const int tok = token0 + 16 * (x / 8) + 8 * hh + x % 8;
+          s[x] = (tok >= lo) & (tok < hi) & ((ok >> (x / 8)) & 1u) ? s[x] : kNegInf;
+        }
       }
-      float mx = kNegInf;
+      float mx = s[0];
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) mx = fmaxf(mx, s[sub][x]);
+      for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[x]);
       // the running maximum moves only when a score passes it by more than 2^8 (see consume_tile)
       if (__ballot(mx > m + slack)) {
         mx = fmaxf(mx, xor32(mx));
@@ -910,24 +904,25 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
 #pragma unroll
           for (int x = 0; x < 16; ++x) o[dt][x] *= shrink;
       }
+    };
+    // their part of the output
+    auto outputs = [&](const uint8_t *buf, int sub, f32x16 &s) {
       const float ref = m == kNegInf ? 0.0f : m * c;
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          s[sub][x] = __builtin_amdgcn_exp2f(fmaf(s[sub][x], c, -ref));
-          l += s[sub][x];
-        }
-#pragma unroll
-      for (int st = 0; st < 4; ++st) {  // 16 tokens each
+      for (int st = 0; st < 2; ++st) {  // 16 tokens each
         u32x4 pw;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[st / 2][8 * (st & 1) + 2 * x], s[st / 2][8 * (st & 1) + 2 * x + 1]);
+        for (int x = 0; x < 8; ++x) {
+          s[8 * st + x] = __builtin_amdgcn_exp2f(fmaf(s[8 * st + x], c, -ref));
+          l += s[8 * st + x];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[8 * st + 2 * x], s[8 * st + 2 * x + 1]);
         const bf16x8 pv = __builtin_bit_cast(bf16x8, pw);
 #pragma unroll
         for (int dt = 0; dt < G::DT; ++dt) {
           // the swizzle of element vd + 32 dt is vd's with bit 1 flipped where dt is odd
-          const int at = (v_piece ^ ((2 * st) ^ (2 * (dt & 1)))) * 16;
+          const int at = (v_piece ^ ((2 * (2 * sub + st)) ^ (2 * (dt & 1)))) * 16;
           const u32x4 vv = *reinterpret_cast<const u32x4 *>(buf + G::V + (vd + 32 * dt) * (TT * 2) + at);
           o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv), pv, o[dt], 0, 0, 0);
         }
@@ -937,24 +932,40 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
     if (tb < te) {
       int first = tb;
       int ids = pages_of(first), ids_next = pages_of(first + 16);
-      fetch(tb, ids, first);
-      store(tb, smem);
-      __syncthreads();
-      for (int tile = tb; tile < te; ++tile) {
-        uint8_t *cur = smem + ((tile - tb) & 1) * G::BUF, *nxt = smem + ((tile - tb + 1) & 1) * G::BUF;
-        ok_groups = ok_next;
-        if (tile + 1 < te) {
-          if (tile + 1 == first + 16) {
-            first += 16;
-            ids = ids_next;
-            ids_next = pages_of(first + 16);
-          }
-          fetch(tile + 1, ids, first);
+      auto fetch_next = [&](int tile) {
+        if (tile == first + 16) {
+          first += 16;
+          ids = ids_next;
+          ids_next = pages_of(first + 16);
         }
-        if (tile * TT < some_hi && tile * TT + TT > some_lo) consume(tile, cur);
-        if (tile + 1 < te) store(tile + 1, nxt);
+        fetch(tile, ids, first);
+      };
+      // Three buffers: while a tile's scores of 32 tokens turn into probabilities and outputs, the matrix cores run
+      // the scores of the next 32, which for a tile's second half are the next tile's first.
+      fetch(tb, ids, first);
+      uint32_t ok_cur = ok_next;
+      store(tb, smem, ok_cur);
+      if (tb + 1 < te) fetch_next(tb + 1);
+      __syncthreads();
+      f32x16 s0, s1;
+      scores(smem, 0, s0);
+      int at_cur = 0, at_nxt = G::BUF;
+      for (int tile = tb; tile < te; ++tile) {
+        const uint32_t ok_tile = ok_next;
+        if (tile + 1 < te) store(tile + 1, smem + at_nxt, ok_tile);
+        if (tile + 2 < te) fetch_next(tile + 2);
+        settle(tile * TT, ok_cur & 3u, s0);
+        scores(smem + at_cur, 1, s1);
+        outputs(smem + at_cur, 0, s0);
         __syncthreads();
+        settle(tile * TT + 32, ok_cur >> 2, s1);
+        scores(smem + at_nxt, 0, s0);  // past the last tile: of whatever is there, not used
+        outputs(smem + at_cur, 1, s1);
+        ok_cur = ok_tile;
+        at_cur = at_nxt;
+        at_nxt = at_nxt == 2 * G::BUF ? 0 : at_nxt + G::BUF;
       }
+      __syncthreads();  // the buffers are free for the next unit
     }
 
     l += xor32(l);

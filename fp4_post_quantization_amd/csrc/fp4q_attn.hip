@@ -863,20 +863,37 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       }
     };
 
-    // scores of 32 tokens of a tile
-    auto scores = [&](const uint8_t *buf, int sub, f32x16 &s) {
-#pragma unroll
-      for (int x = 0; x < 16; ++x) s[x] = 0.0f;
+    // key operands of 32 tokens of a tile, still FP4
+    u32x4 kc[G::HG];
+    float ks[G::HG];
+    auto load_keys = [&](const uint8_t *buf, int sub) {
       const int kr_row = 32 * sub + kt;
 #pragma unroll
       for (int p = 0; p < G::HG; ++p) {
         const int piece = hh * G::HG + p;
-        const u32x4 kc = *reinterpret_cast<const u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16);
-        const float ks = as_f((uint32_t)buf[G::KS + kr_row * G::GR + piece] << 23);
+        kc[p] = *reinterpret_cast<const u32x4 *>(buf + kr_row * G::RB + G::key_piece(kr_row, piece) * 16);
+        ks[p] = as_f((uint32_t)buf[G::KS + kr_row * G::GR + piece] << 23);
+      }
+    };
+    // their scores
+    auto scores = [&](f32x16 &s) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) s[x] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < G::HG; ++p)
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp4x8_to_bf16(kc[w], ks), __builtin_bit_cast(bf16x8, q[4 * p + w]),
-                                                      s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp4x8_to_bf16(kc[p][w], ks[p]),
+                                                      __builtin_bit_cast(bf16x8, q[4 * p + w]), s, 0, 0, 0);
+    };
+    // value operands of 16 tokens of a tile
+    u32x4 vv[G::DT];
+    auto load_values = [&](const uint8_t *buf, int st) {
+#pragma unroll
+      for (int dt = 0; dt < G::DT; ++dt) {
+        // the swizzle of element vd + 32 dt is vd's with bit 1 flipped where dt is odd
+        const int piece = v_piece ^ (2 * st) ^ (2 * (dt & 1));
+        vv[dt] = *reinterpret_cast<const u32x4 *>(buf + G::V + (vd + 32 * dt) * (TT * 2) + piece * 16);
       }
     };
     // masks them and keeps the running maximum
@@ -905,7 +922,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
           for (int x = 0; x < 16; ++x) o[dt][x] *= shrink;
       }
     };
-    // their part of the output
+    // their part of the output; the first 16 tokens' value operands are loaded
     auto outputs = [&](const uint8_t *buf, int sub, f32x16 &s) {
       const float ref = m == kNegInf ? 0.0f : m * c;
 #pragma unroll
@@ -919,13 +936,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
 #pragma unroll
         for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[8 * st + 2 * x], s[8 * st + 2 * x + 1]);
         const bf16x8 pv = __builtin_bit_cast(bf16x8, pw);
+        if (st == 1) load_values(buf, 2 * sub + 1);
 #pragma unroll
-        for (int dt = 0; dt < G::DT; ++dt) {
-          // the swizzle of element vd + 32 dt is vd's with bit 1 flipped where dt is odd
-          const int at = (v_piece ^ ((2 * (2 * sub + st)) ^ (2 * (dt & 1)))) * 16;
-          const u32x4 vv = *reinterpret_cast<const u32x4 *>(buf + G::V + (vd + 32 * dt) * (TT * 2) + at);
-          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv), pv, o[dt], 0, 0, 0);
-        }
+        for (int dt = 0; dt < G::DT; ++dt)
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv[dt]), pv, o[dt], 0, 0, 0);
       }
     };
 
@@ -948,18 +962,23 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       if (tb + 1 < te) fetch_next(tb + 1);
       __syncthreads();
       f32x16 s0, s1;
-      scores(smem, 0, s0);
+      load_keys(smem, 0);
+      scores(s0);
       int at_cur = 0, at_nxt = G::BUF;
       for (int tile = tb; tile < te; ++tile) {
         const uint32_t ok_tile = ok_next;
         if (tile + 1 < te) store(tile + 1, smem + at_nxt, ok_tile);
         if (tile + 2 < te) fetch_next(tile + 2);
+        load_keys(smem + at_cur, 1);
+        load_values(smem + at_cur, 0);
         settle(tile * TT, ok_cur & 3u, s0);
-        scores(smem + at_cur, 1, s1);
+        scores(s1);
         outputs(smem + at_cur, 0, s0);
         __syncthreads();
+        load_keys(smem + at_nxt, 0);  // past the last tile: whatever is there, not used
+        load_values(smem + at_cur, 2);
         settle(tile * TT + 32, ok_cur >> 2, s1);
-        scores(smem + at_nxt, 0, s0);  // past the last tile: of whatever is there, not used
+        scores(s0);
         outputs(smem + at_cur, 1, s1);
         ok_cur = ok_tile;
         at_cur = at_nxt;

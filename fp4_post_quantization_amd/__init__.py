@@ -18,8 +18,6 @@ HIP kernels.  There is no CPU fallback; a missing library raises.
     attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, ...)
 """
 
-import ctypes
-import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -681,6 +679,29 @@ def kv_cache_mxfp4(pages, heads, page_size, head_dim, device=None):
 
 
 def _cache_struct(cache):
+    """The cache as the library takes it (fp4q_kv_cache_t, packed), its heads,
+    page size and head_dim, and its device."""
+    kc, ks, vc, vs = cache
+    dev = kc.get_device()
+    shape, st = kc.shape, kc.stride()
+    if len(shape) == 4 and dev >= 0:
+        pages, heads, page, half = shape
+        s0, s1, s2, s3 = st
+        sub, sst = (pages, heads, page, half >> 4), (s0 >> 4, s1 >> 4, s2 >> 4, 1)
+        u8 = torch.uint8
+        if (s3 == 1 and vc.shape == shape and ks.shape == sub and vs.shape == sub and vc.stride() == st
+                and ks.stride() == sst and vs.stride() == sst and kc.dtype is u8 and ks.dtype is u8
+                and vc.dtype is u8 and vs.dtype is u8 and vc.get_device() == dev and ks.get_device() == dev
+                and vs.get_device() == dev):
+            packed = L.KV_CACHE_PACK(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page, heads,
+                                     2 * half, s0, s1, s2)
+            return packed, heads, page, 2 * half, kc.device
+    return _checked_cache_struct(cache)
+
+
+def _checked_cache_struct(cache):
+    """_cache_struct with a message for what is wrong, and for the strides of
+    axes of one entry, which do not matter."""
     kc, ks, vc, vs = cache
     dev = kc.device
     if dev.type != "cuda":
@@ -695,65 +716,67 @@ def _cache_struct(cache):
                                    ("v_codes", vc, kc.shape, (st[0], st[1], st[2], 1)), ("v_scales", vs, sub, sst)):
         if t.dtype != torch.uint8 or t.device != dev or t.shape != shape:
             raise ValueError(f"cache.{name} must be a uint8 tensor of shape {tuple(shape)} on {dev}")
-        if t.stride() != stride and any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), stride)):
+        if any(n > 1 and a != b for n, a, b in zip(t.shape, t.stride(), stride)):
             raise ValueError(f"cache.{name} must have strides {stride}: a dense last axis, codes and scales of keys "
                              "and values in one order")
-    return L.KVCacheStruct(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page, heads, 2 * half,
-                           st[0], st[1], st[2]), dev
+    packed = L.KV_CACHE_PACK(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page, heads,
+                             2 * half, st[0], st[1], st[2])
+    return packed, heads, page, 2 * half, dev
 
 
 def _heads(t, name, device=None):
     """A [tokens, heads, head_dim] device tensor with a dense last axis."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
+    if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} is on {t.device}, must be on {device or 'a GPU'}")
     return t if t.stride(2) == 1 else t.contiguous()
 
 
-def _index(t, shape, dtype, device, name):
-    """An index vector the library reads in place."""
-    return t if t is None else _given(t, shape, dtype, device, name)
+def _index(t, n, dtype, device, name):
+    """A dense index vector of n entries, which the library reads in place."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.size(0) == n and t.device == device
+            and (n < 2 or t.stride(0) == 1)):
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},) on {device}")
 
 
 def _head_map(tokens, dim, device, positions, table, interleaved, norm_weight, eps, hadamard_n):
-    """fp4q_head_map_t and the tensors it points into."""
+    """fp4q_head_map_t, packed, and the norm's weights as the library reads
+    them (which the caller keeps until the call is made)."""
     if (positions is None) != (table is None):
         raise ValueError("positions and table go together")
-    rot = n_pos = 0
+    rot = n_pos = pos_ptr = table_ptr = w_ptr = 0
     if table is not None:
         if table.dim() != 2 or table.dtype != torch.float32 or table.device != device or not table.is_contiguous():
             raise ValueError(f"table must be a contiguous float32 [positions, rotary_dim] tensor on {device}")
         n_pos, rot = table.shape
-        if rot == 0:
-            raise ValueError("table must have rotary_dim columns")
-        _index(positions, (tokens,), torch.int64, device, "positions")
+        if rot == 0 or n_pos == 0:
+            raise ValueError("table must have rows of rotary_dim columns")
+        table_ptr, pos_ptr = table.data_ptr(), _index(positions, tokens, torch.int64, device, "positions")
     w = norm_weight
     if w is not None:
-        w = w.to(device=device, dtype=torch.float32).contiguous()
+        if w.dtype is not torch.float32 or w.device != device or not w.is_contiguous():
+            w = w.to(device=device, dtype=torch.float32).contiguous()
         if w.shape != (dim,):
             raise ValueError("norm_weight must have head_dim entries")
-        if w.data_ptr() % 16:
+        w_ptr = w.data_ptr()
+        if w_ptr % 16:
             w = w.clone()
-    m = L.HeadMapStruct(_ptr(w), float(eps), _ptr(positions), _ptr(table), n_pos, rot, int(bool(interleaved)),
-                        int(hadamard_n))
-    return m, w
+            w_ptr = w.data_ptr()
+    return L.HEAD_MAP_PACK(w_ptr, eps, pos_ptr, table_ptr, n_pos, rot, bool(interleaved), hadamard_n), w
 
 
-class _OnDevice:
-    """Makes a tensor's device current for a launch; free where it is already."""
+_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __init__(self, device):
-        self.index = device.index
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _launch(device, call, *args):
+    """call(*args, stream) with the tensors' device current, on its current
+    stream."""
+    if _GET_DEVICE() == device.index:
+        return L.check(call(*args, _stream(device)))
+    with torch.cuda.device(device):
+        return L.check(call(*args, _stream(device)))
 
 
 def rotate_heads(x, positions=None, table=None, *, interleaved=False, norm_weight=None, eps=1e-6, hadamard_n=0,
@@ -777,14 +800,13 @@ def rotate_heads(x, positions=None, table=None, *, interleaved=False, norm_weigh
     dev = x.device
     m, keep = _head_map(tokens, dim, dev, positions, table, interleaved, norm_weight, eps, hadamard_n)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=out_dtype or x.dtype, device=dev)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     else:
         _given(out, (tokens, heads, dim), out_dtype or out.dtype, dev, "out")
-    with _OnDevice(dev):
-        ws = _ws(ws, dev)
-        L.check(lib.fp4q_rotate_heads(x.data_ptr(), _dtype_code(x), tokens, heads, dim, x.stride(0), x.stride(1),
-                                      ctypes.byref(m), _dtype_code(out), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                      _stream(dev)))
+    ws = _ws(ws, dev)
+    st, sh, _ = x.stride()
+    _launch(dev, lib.fp4q_rotate_heads, x.data_ptr(), _dtype_code(x), tokens, heads, dim, st, sh, m, _dtype_code(out),
+            out.data_ptr(), ws.data_ptr(), ws.numel())
     if check:
         _check_data(ws)
     return out
@@ -800,23 +822,20 @@ def kv_append_mxfp4(cache, k, v, slots, positions=None, table=None, *, interleav
     the others of a call must be distinct.  With hadamard_n the queries need
     the same rotation."""
     lib = L.load()
-    c, dev = _cache_struct(cache)
+    c, c_heads, _, c_dim, dev = _cache_struct(cache)
     k, v = _heads(k, "k", dev), _heads(v, "v", dev)
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and type")
     tokens, heads, dim = k.shape
-    if heads != c.heads or dim != c.head_dim:
-        raise ValueError(f"k must be [tokens, {c.heads}, {c.head_dim}]")
-    _index(slots, (tokens,), torch.int64, dev, "slots")
-    if slots is None:
-        raise ValueError("slots is required")
+    if heads != c_heads or dim != c_dim:
+        raise ValueError(f"k must be [tokens, {c_heads}, {c_dim}]")
+    slots_ptr = _index(slots, tokens, torch.int64, dev, "slots")
     m, keep = _head_map(tokens, dim, dev, positions, table, interleaved, norm_weight, eps, hadamard_n)
-    with _OnDevice(dev):
-        ws = _ws(ws, dev)
-        L.check(lib.fp4q_kv_append_mxfp4(ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-                                         v.stride(0), v.stride(1), _dtype_code(k), tokens, slots.data_ptr(),
-                                         ctypes.byref(m), int(window[0]), int(window[1]), ws.data_ptr(), ws.numel(),
-                                         _stream(dev)))
+    ws = _ws(ws, dev)
+    k0, k1, _ = k.stride()
+    v0, v1, _ = v.stride()
+    _launch(dev, lib.fp4q_kv_append_mxfp4, c, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, _dtype_code(k), tokens,
+            slots_ptr, m, int(window[0]), int(window[1]), ws.data_ptr(), ws.numel())
     if check:
         _check_data(ws)
 
@@ -826,21 +845,22 @@ def kv_read_mxfp4(cache, slots, *, out_dtype=torch.bfloat16, out=None, ws=None, 
     slot gives zeros): (k, v), each [tokens, heads, head_dim] in bfloat16 or
     float32.  out: a pair of dense tensors to write into."""
     lib = L.load()
-    c, dev = _cache_struct(cache)
+    c, heads, _, dim, dev = _cache_struct(cache)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D int64 tensor")
-    _index(slots, slots.shape, torch.int64, dev, "slots")
-    shape = (slots.numel(), c.heads, c.head_dim)
+    tokens = slots.size(0)
+    slots_ptr = _index(slots, tokens, torch.int64, dev, "slots")
+    shape = (tokens, heads, dim)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+        k = torch.empty(shape, dtype=out_dtype, device=dev)
+        v = torch.empty_like(k)
     else:
+        k, v = out
         for t in out:
-            _given(t, shape, out[0].dtype, dev, "out")
-    k, v = out
-    with _OnDevice(dev):
-        ws = _ws(ws, dev)
-        L.check(lib.fp4q_kv_read_mxfp4(ctypes.byref(c), slots.data_ptr(), shape[0], _dtype_code(k), k.data_ptr(),
-                                       v.data_ptr(), ws.data_ptr(), ws.numel(), _stream(dev)))
+            _given(t, shape, k.dtype, dev, "out")
+    ws = _ws(ws, dev)
+    _launch(dev, lib.fp4q_kv_read_mxfp4, c, slots_ptr, tokens, _dtype_code(k), k.data_ptr(), v.data_ptr(),
+            ws.data_ptr(), ws.numel())
     if check:
         _check_data(ws)
     return k, v
@@ -870,42 +890,45 @@ def attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, *, max_new=None,
     calls that may overlap need one each.  check: synchronize and raise on
     data errors."""
     lib = L.load()
-    c, dev = _cache_struct(cache)
+    c, kv_heads, page, c_dim, dev = _cache_struct(cache)
     q = _heads(q, "q", dev)
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be bfloat16, got {q.dtype}")
     tokens, q_heads, dim = q.shape
-    if dim != c.head_dim or q_heads % c.heads:
-        raise ValueError(f"q must be [tokens, a multiple of {c.heads}, {c.head_dim}]")
-    if (not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.dtype != torch.int32
+    if dim != c_dim or q_heads % kv_heads:
+        raise ValueError(f"q must be [tokens, a multiple of {kv_heads}, {c_dim}]")
+    if (not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.dtype is not torch.int32
             or block_table.device != dev or (block_table.stride(1) != 1 and block_table.size(1) > 1)
             or (block_table.size(0) > 1 and block_table.stride(0) < block_table.size(1))):
         raise ValueError(f"block_table must be a row-major int32 [batch, pages] tensor on {dev}")
     batch, width = block_table.shape
-    _given(seq_lens, (batch,), torch.int32, dev, "seq_lens")
+    lens_ptr = _index(seq_lens, batch, torch.int32, dev, "seq_lens")
+    cu_ptr = None
     if cu_q is not None:
-        _given(cu_q, (batch + 1,), torch.int32, dev, "cu_q")
+        cu_ptr = _index(cu_q, batch + 1, torch.int32, dev, "cu_q")
+        max_new = tokens if max_new is None else min(int(max_new), tokens)
     elif tokens != batch:
         raise ValueError("without cu_q there is one row of q for each sequence")
-    max_new = min(tokens, tokens if cu_q is not None else 1) if max_new is None else min(int(max_new), tokens)
-    max_len = width * c.page_size if max_len is None else min(int(max_len), width * c.page_size)
-    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    else:
+        max_new = min(tokens, 1 if max_new is None else int(max_new))
+    room = width * page
+    max_len = room if max_len is None else min(int(max_len), room)
+    window = int(window)
     if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _given(out, (tokens, q_heads, dim), torch.bfloat16, dev, "out")
     lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=dev) if return_lse else None
-    need = lib.fp4q_attention_mxfp4_workspace_bytes(tokens, batch, q_heads, c.heads, dim, max_new, max_len)
     if ws is None:
+        need = lib.fp4q_attention_mxfp4_workspace_bytes(tokens, batch, q_heads, kv_heads, dim, max_new, max_len, window)
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
         ws = _ws(ws, dev)
-    with _OnDevice(dev):
-        L.check(lib.fp4q_attention_mxfp4(
-            ctypes.byref(c), q.data_ptr(), q.stride(0), q.stride(1), tokens, q_heads, block_table.data_ptr(),
-            max(block_table.stride(0), width), width, batch, seq_lens.data_ptr(), _ptr(cu_q), max_new, max_len,
-            scale, int(bool(causal)), int(window), out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-            _stream(dev)))
+    q0, q1, _ = q.stride()
+    _launch(dev, lib.fp4q_attention_mxfp4, c, q.data_ptr(), q0, q1, tokens, q_heads, block_table.data_ptr(),
+            max(block_table.stride(0), width), width, batch, lens_ptr, cu_ptr, max_new, max_len,
+            dim ** -0.5 if scale is None else scale, bool(causal), window, out.data_ptr(), _ptr(lse), ws.data_ptr(),
+            ws.numel())
     if check:
         _check_data(ws)
     return (out, lse) if return_lse else out

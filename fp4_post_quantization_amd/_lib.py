@@ -2,6 +2,7 @@
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # the in-tree build; FP4Q_LIBRARY names another build of the same sources (e.g. the host-sanitized
@@ -80,8 +81,12 @@ class HeadMapStruct(ctypes.Structure):
                 ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("hadamard_n", ctypes.c_int32)]
 
 
-_CACHE = ctypes.POINTER(KVCacheStruct)
-_MAP = ctypes.POINTER(HeadMapStruct)
+# The same structs packed to bytes, which a call takes as well: building a
+# ctypes struct costs several times more host time.
+KV_CACHE_PACK = struct.Struct("4Qq3i3q").pack
+HEAD_MAP_PACK = struct.Struct("Qd2Qq3i0q").pack
+
+_CACHE = _MAP = _P  # host pointers: bytes or byref(struct)
 
 _SIGNATURES = {
     "fp4q_version": (_I, []),
@@ -112,7 +117,7 @@ _SIGNATURES = {
     "fp4q_kv_read_mxfp4": (_I, [_CACHE, _P, _I64, _I, _P, _P, _P, _SZ, _P]),
     "fp4q_attention_mxfp4": (_I, [_CACHE, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64,
                                   ctypes.c_float, _I, _I64, _P, _P, _P, _SZ, _P]),
-    "fp4q_attention_mxfp4_workspace_bytes": (_SZ, [_I64] * 7),
+    "fp4q_attention_mxfp4_workspace_bytes": (_SZ, [_I64] * 8),
     "fp4q_gemm_nvfp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _I64, _P, _SZ, _P]),
 }
 

@@ -77,13 +77,12 @@ __device__ __forceinline__ AttnSeq seq_of_uniform(const AttnArgs &a, int b) {
   return attn_seq(a.sh, uniform(a.lens[b]), begin, end);
 }
 
-// Work of sequence b: (row tile, head) units times its key tiles (split
+// Work of a sequence: (row tile, head) units times what each costs (split
 // form), or the units alone.
 template <int ROWS, int TT>
-__device__ __forceinline__ int64_t work_of(const AttnArgs &a, int b, bool split) {
-  if (b >= a.sh.batch) return 0;
-  const AttnWork w = attn_work(a.sh, seq_of(a, b), ROWS, TT);
-  return w.row_tiles * a.sh.heads * (split ? w.n + kUnitCost : 1);
+__device__ __forceinline__ int64_t work_of(const AttnArgs &a, const AttnSeq &sq) {
+  const AttnWork w = attn_work(a.sh, sq, ROWS, TT);
+  return w.row_tiles * a.sh.heads * (a.spans ? w.n + kUnitCost : 1);
 }
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
@@ -92,23 +91,29 @@ __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
 }
 
 // The sequences' work, scanned by one wave 64 sequences at a time; the first
-// 64 are scanned once.
+// 64 are loaded and scanned once, lane i keeping sequence i.
 template <int ROWS, int TT>
 struct WorkScan {
   const AttnArgs &a;
   int lane;
-  bool split;
+  AttnSeq seq0;
   int64_t mine0, sum0;
-  __device__ WorkScan(const AttnArgs &args, int l, bool sp) : a(args), lane(l), split(sp) { sum0 = scan(0, mine0); }
-  __device__ int64_t scan(int base, int64_t &mine) const {  // inclusive prefix of this group
-    mine = work_of<ROWS, TT>(a, base + lane, split);
-    int64_t s = mine;
+  __device__ WorkScan(const AttnArgs &args, int l) : a(args), lane(l), seq0{0, 0, 0, false} {
+    if (lane < a.sh.batch) seq0 = seq_of(a, lane);
+    mine0 = lane < a.sh.batch ? work_of<ROWS, TT>(a, seq0) : 0;
+    sum0 = prefix(mine0);
+  }
+  __device__ int64_t prefix(int64_t s) const {  // inclusive
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t o = shfl_up64(s, d);
       if (lane >= d) s += o;
     }
     return s;
+  }
+  __device__ int64_t scan(int base, int64_t &mine) const {
+    mine = base + lane < a.sh.batch ? work_of<ROWS, TT>(a, seq_of(a, base + lane)) : 0;
+    return prefix(mine);
   }
   static __device__ int64_t lane_value(int64_t v, int l) {
     const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
@@ -136,6 +141,15 @@ struct WorkScan {
       if (base >= a.sh.batch) return false;
       s = scan(base, mine);
     }
+  }
+  __device__ __forceinline__ AttnSeq seq(int b) const {  // of a sequence that is the same in every lane
+    if (b >= 64) return seq_of_uniform(a, b);
+    AttnSeq s;
+    s.first = __builtin_amdgcn_readlane((int)seq0.first, b);  // below 2^30
+    s.fresh = __builtin_amdgcn_readlane(seq0.fresh, b);
+    s.len = __builtin_amdgcn_readlane(seq0.len, b);
+    s.bad = false;
+    return s;
   }
 };
 
@@ -419,18 +433,20 @@ struct Unit {
 template <int ROWS, int TT>
 struct Walk {
   const AttnArgs &a;
+  WorkScan<ROWS, TT> scan;
   int64_t pos, end, off, total;
-  int b;
+  int b, spans;
   bool joined;  // this span's Join is written
 
-  __device__ __forceinline__ Walk(const AttnArgs &args, int lane) : a(args), off(0), total(0), b(0), joined(false) {
-    const WorkScan<ROWS, TT> scan(a, lane, a.spans != 0);
-    pos = blockIdx.x;
+  __device__ __forceinline__ Walk(const AttnArgs &args, int lane, int index)
+      : a(args), scan(args, lane), off(0), total(0), b(0), spans(0), joined(false) {
+    pos = index;
     end = pos + 1;
     if (a.spans) {
       total = uniform64(scan.total());
-      end = attn_cut(total, a.spans, pos + 1);
-      pos = attn_cut(total, a.spans, pos);
+      spans = attn_spans(total, a.spans);
+      end = index < spans ? attn_cut(total, spans, pos + 1) : 0;
+      pos = index < spans ? attn_cut(total, spans, pos) : 0;
     }
     if (pos < end && !scan.find(pos, b, off)) end = pos;
     b = uniform(b);
@@ -439,7 +455,7 @@ struct Walk {
 
   __device__ __forceinline__ bool next(Unit &u) {
     while (pos < end) {
-      const AttnSeq sq = seq_of_uniform(a, b);
+      const AttnSeq sq = scan.seq(b);
       const AttnWork wk = attn_work(a.sh, sq, ROWS, TT);
       const int64_t size = a.spans ? wk.n + kUnitCost : 1;  // of a unit
       if (off >= wk.row_tiles * a.sh.heads * size) {        // on to the next sequence that has rows
@@ -475,15 +491,15 @@ struct Walk {
       if (!u.whole && u.t0 == 0) {
         joined = true;
         if (threadIdx.x == 0)
-          a.joins[blockIdx.x] =
-              Join{sq.first, u.r0, (int)attn_span_of(total, a.spans, pos - here - from + size - 1), u.live, u.h, 0};
+          a.joins[blockIdx.x - 1] =
+              Join{sq.first, u.r0, (int)attn_span_of(total, spans, pos - here - from + size - 1), u.live, u.h, 0};
       }
       return true;
     }
     return false;
   }
   __device__ __forceinline__ void finish() const {
-    if (a.spans && !joined && threadIdx.x == 0) a.joins[blockIdx.x] = Join{0, 0, 0, 0, 0, 0};
+    if (a.spans && !joined && threadIdx.x == 0) a.joins[blockIdx.x - 1] = Join{0, 0, 0, 0, 0, 0};
   }
 };
 
@@ -497,14 +513,18 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
   return sum > 0.0f ? (m + log2f(sum)) * kLn2 : (sum == 0.0f ? kNegInf : sum);
 }
 
-// Taking the status slot, and checking every sequence's length and rows: the
-// first wave of the first workgroup.
-__device__ __forceinline__ void open_status(const AttnArgs &a, int lane, int wave) {
-  if (blockIdx.x != 0 || wave != 0) return;
-  bool bad = false;
-  for (int i = lane; i < a.sh.batch; i += 64) bad |= seq_of(a, i).bad;
-  const uint32_t bits = __ballot(bad) ? FP4Q_DATA_BAD_TABLE : 0u;
-  if (lane == 0) Status{a.status, true}.merge(bits);
+// The first workgroup of a call takes the status slot and checks every
+// sequence's length and rows; it has no other work, so that nobody's work
+// waits for the slot's atomics.
+__device__ __forceinline__ bool is_status_group(const AttnArgs &a, int lane, int wave) {
+  if (blockIdx.x != 0) return false;
+  if (wave == 0) {
+    bool bad = false;
+    for (int i = lane; i < a.sh.batch; i += 64) bad |= seq_of(a, i).bad;
+    const uint32_t bits = __ballot(bad) ? FP4Q_DATA_BAD_TABLE : 0u;
+    if (lane == 0) Status{a.status, true}.merge(bits);
+  }
+  return true;
 }
 
 // The page of token tok of a sequence, -1 where it is outside the cache.
@@ -515,22 +535,19 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_tab
   return -1;
 }
 
-// Waves of a SIMD that the registers of a variant leave room for.
-constexpr int waves_per_simd(int dim, int nr) { return nr == 1 && dim <= 128 ? 2 : 1; }
-
 // Row r of a sequence's row tile: token i = r / groups, query head of group r % groups.
-template <int D, int NR, int NW>
-__global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kernel(AttnArgs a) {
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
   using G = Geo<D>;
-  constexpr int ROWS = 16 * NR, TT = G::TT, TG = G::TG;
+  constexpr int NR = 1, ROWS = 16 * NR, TT = G::TT, TG = G::TG;
   constexpr int LD = D + 4;  // padded row of the merge buffer
   __shared__ __align__(16) float mo[NW][16][LD];
   __shared__ float mm[NW][16], ml[NW][16];
   const int lane = threadIdx.x & 63, wave = wave_index();
-  open_status(a, lane, wave);
+  if (is_status_group(a, lane, wave)) return;
   uint32_t err = 0u;
   const LaneAt<D> at(lane, a.token_stride);
-  Walk<ROWS, TT> walk(a, lane);
+  Walk<ROWS, TT> walk(a, lane, (int)blockIdx.x - 1);
   Unit u;
   while (walk.next(u)) {
     const int t0 = u.t0, t1 = u.t1;
@@ -649,7 +666,7 @@ __global__ __launch_bounds__(64 * NW, waves_per_simd(D, NR)) void attn_rows_kern
           if (a.lse && d == 0) a.lse[head] = row_lse(top, sum);
         } else {
           using P = Part<D, ROWS>;
-          const int64_t slot = 2 * (int64_t)blockIdx.x + (t0 == 0 ? 1 : 0);
+          const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (t0 == 0 ? 1 : 0);
           float *po = P::o(a.parts, slot) + (16 * r + row) * D + d;
           *reinterpret_cast<f32x4 *>(po) = f32x4{o[0], o[1], o[2], o[3]};
           *reinterpret_cast<f32x4 *>(po + 4) = f32x4{o[4], o[5], o[6], o[7]};
@@ -726,13 +743,13 @@ struct StageAt {
 };
 
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnArgs a) {
   using G = PromptGeo<D>;
-  constexpr int TT = G::TT, M = 32 * NW, THREADS = 64 * NW;
+  constexpr int TT = G::TT, NR = 1, W = 32 * NR, M = W * NW, THREADS = 64 * NW;
   constexpr int PT = (G::ITEMS + THREADS - 1) / THREADS;  // staging items of a thread
   __shared__ __align__(16) uint8_t smem[3 * G::BUF];
   const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 31, hh = lane >> 5;
-  open_status(a, lane, wave);
+  if (is_status_group(a, lane, wave)) return;
   uint32_t err = 0u;
   const float c = fmaxf(fabsf(a.scale_log2), 1e-30f);  // the sign of the scale goes into the queries
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
@@ -743,37 +760,42 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
   const int v_piece = hh ^ G::value_swizzle(vd);
   const StageAt<D> at(threadIdx.x, a.token_stride);
 
-  Walk<M, TT> walk(a, lane);
+  Walk<M, TT> walk(a, lane, (int)blockIdx.x - 1);
   Unit u;
   while (walk.next(u)) {
     // key tiles that the row tile's own rows see
     const int see_lo = attn_lo(a.sh, u.sq, u.i0) / TT, see_hi = (attn_hi(a.sh, u.sq, u.i1) + TT - 1) / TT;
     const int tb = uniform(max(u.lo + u.t0, see_lo)), te = uniform(min(u.lo + u.t1, see_hi));
-    const int w_rows = u.live - 32 * wave;  // of the wave: 32 or fewer, none where it is not positive
-    const int j0 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave : 0), a.sh.groups));
-    const int j1 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? 32 * wave + min(w_rows, 32) - 1 : 0), a.sh.groups));
+    const int w_rows = u.live - W * wave;  // of the wave: W or fewer, none where it is not positive
+    const int j0 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? W * wave : 0), a.sh.groups));
+    const int j1 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? W * wave + min(w_rows, W) - 1 : 0), a.sh.groups));
     const int all_lo = uniform(attn_lo(a.sh, u.sq, j1)), all_hi = uniform(attn_hi(a.sh, u.sq, j0));
 
-    const bool on = n < w_rows;
-    const int64_t row = u.r0 + (on ? 32 * wave + n : 0);
-    const int i = (int)attn_div(row, a.sh.groups);
-    const int lo = attn_lo(a.sh, u.sq, i), hi = attn_hi(a.sh, u.sq, i);
-    u32x4 q[G::HG * 4];
-    {
+    u32x4 q[NR][G::HG * 4];
+    f32x16 o[NR][G::DT];
+    float m[NR], l[NR];
+    int lo[NR], hi[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const bool on = 32 * r + n < w_rows;
+      const int64_t row = u.r0 + (on ? W * wave + 32 * r + n : 0);
+      const int i = (int)attn_div(row, a.sh.groups);
+      lo[r] = attn_lo(a.sh, u.sq, i);
+      hi[r] = attn_hi(a.sh, u.sq, i);
       const uint16_t *qp = a.q + (u.sq.first + i) * a.q_st + (u.h * a.sh.groups + (row - (int64_t)i * a.sh.groups)) * a.q_sh;
 #pragma unroll
       for (int x = 0; x < G::HG * 4; ++x) {
-        q[x] = u32x4{0u, 0u, 0u, 0u};
-        if (on) q[x] = *reinterpret_cast<const u32x4 *>(qp + hh * (D / 2) + 8 * x);
-        q[x] ^= flip;
+        q[r][x] = u32x4{0u, 0u, 0u, 0u};
+        if (on) q[r][x] = *reinterpret_cast<const u32x4 *>(qp + hh * (D / 2) + 8 * x);
+        q[r][x] ^= flip;
       }
+#pragma unroll
+      for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[r][dt][x] = 0.0f;
+      m[r] = kNegInf;
+      l[r] = 0.0f;
     }
-    f32x16 o[G::DT];
-#pragma unroll
-    for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[dt][x] = 0.0f;
-    float m = kNegInf, l = 0.0f;
 
     const int64_t head_off = u.h * a.head_stride;
     const int32_t *row_table = a.table + u.b * a.table_stride;
@@ -876,15 +898,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       }
     };
     // their scores
-    auto scores = [&](f32x16 &s) {
+    auto scores = [&](f32x16 (&s)[NR]) {
 #pragma unroll
-      for (int x = 0; x < 16; ++x) s[x] = 0.0f;
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) s[r][x] = 0.0f;
 #pragma unroll
       for (int p = 0; p < G::HG; ++p)
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp4x8_to_bf16(kc[p][w], ks[p]),
-                                                      __builtin_bit_cast(bf16x8, q[4 * p + w]), s, 0, 0, 0);
+        for (int w = 0; w < 4; ++w) {
+          const bf16x8 kv = fp4x8_to_bf16(kc[p][w], ks[p]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv, __builtin_bit_cast(bf16x8, q[r][4 * p + w]), s[r], 0, 0, 0);
+        }
     };
     // value operands of 16 tokens of a tile
     u32x4 vv[G::DT];
@@ -897,49 +924,68 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       }
     };
     // masks them and keeps the running maximum
-    auto settle = [&](int token0, uint32_t ok, f32x16 &s) {
+    auto settle = [&](int token0, uint32_t ok, f32x16 (&s)[NR]) {
       if (!(ok == 3u && token0 >= all_lo && token0 + 32 <= all_hi)) {
         not_speculated();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int tok = token0 + 16 * (x / 8) + 8 * hh + x % 8;
-          s[x] = (tok >= lo) & (tok < hi) & ((ok >> (x / 8)) & 1u) ? s[x] : kNegInf;
-        }
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int tok = token0 + 16 * (x / 8) + 8 * hh + x % 8;
+            s[r][x] = (tok >= lo[r]) & (tok < hi[r]) & ((ok >> (x / 8)) & 1u) ? s[r][x] : kNegInf;
+          }
       }
-      float mx = s[0];
+      float mx[NR];
+      bool far = false;
 #pragma unroll
-      for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[x]);
+      for (int r = 0; r < NR; ++r) {
+        mx[r] = s[r][0];
+#pragma unroll
+        for (int x = 1; x < 16; ++x) mx[r] = fmaxf(mx[r], s[r][x]);
+        far |= mx[r] > m[r] + slack;
+      }
       // the running maximum moves only when a score passes it by more than 2^8 (see consume_tile)
-      if (__ballot(mx > m + slack)) {
-        mx = fmaxf(mx, xor32(mx));
-        const float top = fmaxf(m, mx);
-        const float shrink = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
-        m = top;
-        l *= shrink;
+      if (__ballot(far)) {
 #pragma unroll
-        for (int dt = 0; dt < G::DT; ++dt)
+        for (int r = 0; r < NR; ++r) {
+          const float top = fmaxf(m[r], fmaxf(mx[r], xor32(mx[r])));
+          const float shrink = m[r] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m[r] - top) * c);
+          m[r] = top;
+          l[r] *= shrink;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[dt][x] *= shrink;
+          for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[r][dt][x] *= shrink;
+        }
       }
     };
     // their part of the output; the first 16 tokens' value operands are loaded
-    auto outputs = [&](const uint8_t *buf, int sub, f32x16 &s) {
-      const float ref = m == kNegInf ? 0.0f : m * c;
+    auto outputs = [&](const uint8_t *buf, int sub, f32x16 (&s)[NR]) {
+      float ref[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) ref[r] = m[r] == kNegInf ? 0.0f : m[r] * c;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {  // 16 tokens each
-        u32x4 pw;
+        bf16x8 pv[NR];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          s[8 * st + x] = __builtin_amdgcn_exp2f(fmaf(s[8 * st + x], c, -ref));
-          l += s[8 * st + x];
+        for (int r = 0; r < NR; ++r) {
+          u32x4 pw;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            s[r][8 * st + x] = __builtin_amdgcn_exp2f(fmaf(s[r][8 * st + x], c, -ref[r]));
+            l[r] += s[r][8 * st + x];
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[r][8 * st + 2 * x], s[r][8 * st + 2 * x + 1]);
+          pv[r] = __builtin_bit_cast(bf16x8, pw);
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[8 * st + 2 * x], s[8 * st + 2 * x + 1]);
-        const bf16x8 pv = __builtin_bit_cast(bf16x8, pw);
         if (st == 1) load_values(buf, 2 * sub + 1);
 #pragma unroll
         for (int dt = 0; dt < G::DT; ++dt)
-          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv[dt]), pv, o[dt], 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            o[r][dt] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv[dt]), pv[r], o[r][dt], 0, 0, 0);
       }
     };
 
@@ -961,7 +1007,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       store(tb, smem, ok_cur);
       if (tb + 1 < te) fetch_next(tb + 1);
       __syncthreads();
-      f32x16 s0, s1;
+      f32x16 s0[NR], s1[NR];
       load_keys(smem, 0);
       scores(s0);
       int at_cur = 0, at_nxt = G::BUF;
@@ -987,35 +1033,37 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 8 / NW) void attn_prompt_ke
       __syncthreads();  // the buffers are free for the next unit
     }
 
-    l += xor32(l);
-    const float top = m == kNegInf ? kNegInf : m * c;
-    if (on) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float sum = l[r] + xor32(l[r]);
+      const float top = m[r] == kNegInf ? kNegInf : m[r] * c;
+      const int pr = W * wave + 32 * r + n;  // row of the tile
+      if (pr >= u.live) continue;
       if (u.whole) {
-        const float inv = row_factor(l);
-        const int64_t head = out_row(a, u.sq.first, u.h, row);
+        const float inv = row_factor(sum);
+        const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + pr);
 #pragma unroll
         for (int dt = 0; dt < G::DT; ++dt) {
           u32x4 w[2];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = pack_bf16(o[dt][2 * x] * inv, o[dt][2 * x + 1] * inv);
+          for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = pack_bf16(o[r][dt][2 * x] * inv, o[r][dt][2 * x + 1] * inv);
           u32x4 *p = reinterpret_cast<u32x4 *>(a.out + head * D + dt * 32 + hh * 16);
           p[0] = w[0];
           p[1] = w[1];
         }
-        if (a.lse && hh == 0) a.lse[head] = row_lse(top, l);
+        if (a.lse && hh == 0) a.lse[head] = row_lse(top, sum);
       } else {
         using P = Part<D, M>;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (u.t0 == 0 ? 1 : 0);
-        const int pr = 32 * wave + n;
+        const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (u.t0 == 0 ? 1 : 0);
 #pragma unroll
         for (int dt = 0; dt < G::DT; ++dt)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             *reinterpret_cast<f32x4 *>(P::o(a.parts, slot) + pr * D + dt * 32 + hh * 16 + 4 * x) =
-                f32x4{o[dt][4 * x], o[dt][4 * x + 1], o[dt][4 * x + 2], o[dt][4 * x + 3]};
+                f32x4{o[r][dt][4 * x], o[r][dt][4 * x + 1], o[r][dt][4 * x + 2], o[r][dt][4 * x + 3]};
         if (hh == 0) {
           P::m(a.parts, slot)[pr] = top;
-          P::l(a.parts, slot)[pr] = l;
+          P::l(a.parts, slot)[pr] = sum;
         }
       }
     }
@@ -1089,29 +1137,40 @@ __global__ __launch_bounds__(64) void attn_status_kernel(uint32_t *status) {
 
 // ------------------------------------------------------------ dispatch ----
 constexpr int kCus = 256;
-constexpr int kDirectTiles = 32; // units of at most this many key tiles are not split
 
 struct Plan {
-  int rows;       // of a row tile: 16 or 32 (attn_rows_kernel), 128 (attn_prompt_kernel)
+  int rows;       // of a row tile: 16 (attn_rows_kernel), 128 or 256 (attn_prompt_kernel)
   int64_t units;  // upper bound of (sequence, row tile, head) units
   int spans;
   int64_t part_floats;
 };
 
 Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_new,
-               int64_t max_len) {
+               int64_t max_len, int64_t window) {
+  const int64_t groups = q_heads / heads, seq_rows = max_new * groups;
+  const int64_t keys = window && window + max_new < max_len ? window + max_new : max_len;  // of a row tile, at most
+  auto units_of = [&](int64_t rows) {  // a sequence's rows fill its row tiles except the last one
+    const int64_t tiles = tokens * groups / rows + batch, most = batch * ((seq_rows + rows - 1) / rows);
+    return (tiles < most ? tiles : most) * heads;
+  };
   Plan p;
-  const int64_t groups = q_heads / heads;
-  p.rows = max_new * groups > 64 ? 128 : (max_new * groups <= 16 || head_dim == 256 ? 16 : 32);
-  const int64_t tile = p.rows == 128 ? 64 : 32;
-  // a sequence's rows fill its tiles except the last one
-  int64_t row_tiles = tokens * groups / p.rows + batch;
-  const int64_t per_seq = (max_new * groups + p.rows - 1) / p.rows;
-  if (row_tiles > batch * per_seq) row_tiles = batch * per_seq;
-  p.units = row_tiles * heads;
-  const int64_t fit = kCus * (p.rows == 128 ? (head_dim == 256 ? 1 : 2) : waves_per_simd((int)head_dim, p.rows / 16));
-  const bool direct = (max_len + tile - 1) / tile + 1 <= kDirectTiles || (p.rows == 128 && p.units >= fit);
-  p.spans = direct ? 0 : (int)fit;  // as many workgroups as fit the chip at once
+  // A row tile of 128 costs a fifth of eight of 16 for each key, but it has to be filled, and there have to be
+  // enough of them for half the CUs, or keys enough to be split.  Measured (32 heads on 8, 128 wide; one sequence
+  // unless said): 80 rows a head on 8192 keys, two sequences: 37 us with 16, 52 with 128; 512 rows on 16384 keys
+  // 103 and 85; 2048 rows on 512 keys 34 (with 32) and 25; five sequences of up to 951 rows behind a window of 1000
+  // (12 heads on 4 of 64) 20 and 37.  256 rows share the staging of a key tile among twice the waves where there
+  // are still two workgroups for each CU: 16384 rows a head on 8192 keys 505 us with 128, 470 with 256; 8192 rows on
+  // 2048 keys 65 and 71.
+  p.rows = 16;
+  if (seq_rows > 96 && (units_of(128) >= kCus / 2 || keys > 4096))
+    p.rows = head_dim != 256 && units_of(256) >= 2 * kCus ? 256 : 128;
+  p.units = units_of(p.rows);
+  const int64_t fit = kCus * (head_dim == 256 || p.rows == 256 ? 1 : 2);  // workgroups on the chip at once
+  // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
+  // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
+  const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
+  const bool direct = tiles <= 34 || (p.units >= fit && (p.rows != 16 || tiles <= 66));
+  p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
   p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * p.rows * (head_dim + 2);
   return p;
 }
@@ -1128,9 +1187,11 @@ fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : 
 
 template <int D, int ROWS>
 void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.spans ? p.spans : p.units));
-  if constexpr (ROWS == 128) hipLaunchKernelGGL((attn_prompt_kernel<D, 4>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((attn_rows_kernel<D, ROWS / 16, 4>), grid, dim3(256), 0, s, a);
+  const dim3 grid((unsigned)(p.spans ? p.spans : p.units) + 1);
+  if constexpr (ROWS >= 128)
+    hipLaunchKernelGGL((attn_prompt_kernel<D, ROWS / 32>), grid, dim3(2 * ROWS), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_rows_kernel<D, 4>), grid, dim3(256), 0, s, a);
   if (!p.spans) return;
   const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
   hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),
@@ -1143,9 +1204,10 @@ void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
 using namespace fp4q;
 
 extern "C" size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads,
-                                                       int64_t head_dim, int64_t max_new, int64_t max_len) {
-  if (!sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
-  const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len);
+                                                       int64_t head_dim, int64_t max_new, int64_t max_len,
+                                                       int64_t window) {
+  if (window < 0 || !sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
+  const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len, window);
   return kAttnHeader + p.spans * sizeof(Join) + 4 * (size_t)p.part_floats;
 }
 
@@ -1172,8 +1234,8 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   if (!empty && (!kv_aligned(out, 16) || !kv_aligned(lse, 4) || !kv_aligned(block_table, 4) ||
                  !kv_aligned(seq_lens, 4) || !kv_aligned(cu_q, 4)))
     return FP4Q_ERR_ALIGN;
-  const size_t need =
-      fp4q_attention_mxfp4_workspace_bytes(tokens, batch, q_heads, cache->heads, cache->head_dim, max_new, max_len);
+  const size_t need = fp4q_attention_mxfp4_workspace_bytes(tokens, batch, q_heads, cache->heads, cache->head_dim,
+                                                           max_new, max_len, window);
   if (!workspace || workspace_bytes < need || !kv_aligned(workspace, 16)) return FP4Q_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   uint32_t *status = (uint32_t *)workspace;
@@ -1181,7 +1243,7 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
     hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, s, status);
     return hip_status();
   }
-  const Plan p = make_plan(tokens, batch, q_heads, cache->heads, cache->head_dim, max_new, max_len);
+  const Plan p = make_plan(tokens, batch, q_heads, cache->heads, cache->head_dim, max_new, max_len, window);
   if (p.units == 0) {  // no sequence has a row
     hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, s, status);
     return hip_status();
@@ -1214,9 +1276,9 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   a.spans = p.spans;
   auto go = [&](auto dc) {
     constexpr int D = decltype(dc)::value;
-    if (p.rows == 128) launch<D, 128>(a, p, s);
-    else if (p.rows == 16) launch<D, 16>(a, p, s);
-    else if constexpr (D != 256) launch<D, 32>(a, p, s);
+    if (p.rows == 16) launch<D, 16>(a, p, s);
+    else if (p.rows == 128) launch<D, 128>(a, p, s);
+    else if constexpr (D != 256) launch<D, 256>(a, p, s);
   };
   if (cache->head_dim == 64) go(std::integral_constant<int, 64>{});
   else if (cache->head_dim == 128) go(std::integral_constant<int, 128>{});

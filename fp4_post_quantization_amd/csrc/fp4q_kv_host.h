@@ -188,6 +188,12 @@ FP4Q_HD int64_t attn_cut(int64_t total, int64_t spans, int64_t i) {
   const int64_t q = attn_div(total, spans), r = total - q * spans;
   return q * i + (i < r ? i : r);
 }
+// The spans that `total` positions of work are worth: none has fewer than a
+// unit's cost and four key tiles, one for each wave.
+FP4Q_HD int attn_spans(int64_t total, int spans) {
+  const int64_t most = attn_div(total, kUnitCost + 4);
+  return most < 1 ? 1 : (most < spans ? (int)most : spans);
+}
 // The span that position pos (0 .. total - 1) lies in.
 FP4Q_HD int64_t attn_span_of(int64_t total, int64_t spans, int64_t pos) {
   const int64_t q = attn_div(total, spans), r = total - q * spans;

@@ -187,7 +187,7 @@ fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, const void *q, 
 /* Workspace of such a call: a header, and the partial results of sequences
  * that several workgroups share.  0 for invalid sizes. */
 size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads,
-                                            int64_t head_dim, int64_t max_new, int64_t max_len);
+                                            int64_t head_dim, int64_t max_new, int64_t max_len, int64_t window);
 
 #ifdef __cplusplus
 }

@@ -504,7 +504,7 @@ def test_step_in_a_captured_graph_and_on_two_streams():
     w = torch.ones(dim, device=DEV)
     qkv = _heads(rng, batch, heads + 2 * kv, dim, torch.bfloat16).to(DEV)
     out = torch.empty(batch, heads, dim, dtype=torch.bfloat16, device=DEV)
-    need = fq._lib.load().fp4q_attention_mxfp4_workspace_bytes(batch, batch, heads, kv, dim, 1, width * page)
+    need = fq._lib.load().fp4q_attention_mxfp4_workspace_bytes(batch, batch, heads, kv, dim, 1, width * page, 0)
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
     st = torch.empty(8192, dtype=torch.uint8, device=DEV)
     side = torch.cuda.Stream()

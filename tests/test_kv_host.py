@@ -156,13 +156,22 @@ def test_attention_refusals(kw, want):
 def test_attention_workspace_of_invalid_sizes_is_zero():
     L, lib = _lib()
     f = lib.fp4q_attention_mxfp4_workspace_bytes
-    assert f(8, 8, 8, 2, 128, 1, 4096) >= 256
-    for bad in ((-1, 8, 8, 2, 128, 1, 64), (8, 8, 7, 2, 128, 1, 64), (8, 8, 8, 2, 80, 1, 64), (8, 8, 8, 0, 128, 1, 64),
-                (8, 8, 8, 2, 128, 9, 64), (8, 8, 8, 2, 128, 1, 1 << 31)):
+    assert f(8, 8, 8, 2, 128, 1, 4096, 0) >= 256
+    for bad in ((-1, 8, 8, 2, 128, 1, 64, 0), (8, 8, 7, 2, 128, 1, 64, 0), (8, 8, 8, 2, 80, 1, 64, 0),
+                (8, 8, 8, 0, 128, 1, 64, 0), (8, 8, 8, 2, 128, 9, 64, 0), (8, 8, 8, 2, 128, 1, 1 << 31, 0),
+                (8, 8, 8, 2, 128, 1, 64, -1)):
         assert f(*bad) == 0
 
 
 # ------------------------------------------------- the binding's checks ----
+def test_packed_structs_are_the_ctypes_ones():
+    L, _ = _lib()
+    args = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11)
+    assert L.KV_CACHE_PACK(*args) == bytes(L.KVCacheStruct(*args))
+    args = (1, 0.5, 3, 4, 5, 6, 1, 8)
+    assert L.HEAD_MAP_PACK(*args) == bytes(L.HeadMapStruct(*args))
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     import fp4_post_quantization_amd as fq
     x = torch.zeros(2, 3, 64)
@@ -202,6 +211,7 @@ extern "C" void part(int64_t from, int64_t to, int64_t n, int64_t *o) {
   AttnPart p = attn_part(from, to, (int)n); o[0] = p.t0; o[1] = p.t1;
 }
 extern "C" int64_t unit_cost() { return kUnitCost; }
+extern "C" int64_t worth(int64_t total, int64_t spans) { return attn_spans(total, (int)spans); }
 extern "C" int64_t span_of(int64_t total, int64_t spans, int64_t p) { return attn_span_of(total, spans, p); }
 """
 
@@ -218,6 +228,7 @@ def host(tmp_path_factory):
     P, I = ctypes.c_void_p, ctypes.c_int64
     lib.seq.argtypes, lib.keys.argtypes = [P, I, I, I, I, I, P], [P, I, I, I, I, P]
     lib.part.argtypes, lib.unit_cost.restype = [I, I, I, P], I
+    lib.worth.argtypes, lib.worth.restype = [I, I], I
     for f in (lib.cut, lib.span_of):
         f.argtypes, f.restype = [I, I, I], I
     return lib
@@ -289,6 +300,7 @@ def test_units_of_spans_cover_every_tile_once_and_join(host):
         spans = int(rng.choice([1, 2, 7, 64, 256]))
         starts = np.concatenate([[0], np.cumsum([n + cost for n in tiles])])
         total = int(starts[-1])
+        spans = host.worth(total, spans)
         seen = [np.zeros(n, dtype=int) for n in tiles]
         parts = {}   # slot -> unit, tiles
         joins = {}

@@ -31,6 +31,7 @@ struct Join {
 
 struct AttnArgs {
   AttnShape sh;
+  Divider by_groups, by_heads;
   const uint16_t *q;
   int64_t q_st, q_sh;
   const uint8_t *kc, *ks, *vc, *vs;
@@ -85,9 +86,29 @@ __device__ __forceinline__ int64_t work_of(const AttnArgs &a, const AttnSeq &sq)
   return w.row_tiles * a.sh.heads * (a.spans ? w.n + kUnitCost : 1);
 }
 
+__device__ __forceinline__ int64_t lane_value(int64_t v, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   const int lo = __shfl_up((int)(uint32_t)v, d), hi = __shfl_up((int)(v >> 32), d);
   return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// Inclusive prefix sums over the lanes of a wave: within the rows of 16 by
+// shifts of 1, 2, 4 and 8 (lanes from outside a row count as 0), then row 0's
+// and row 2's last lanes into rows 1 and 3, and lane 31 into rows 2 and 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
+}
+__device__ __forceinline__ uint32_t dpp_prefix(uint32_t v) {
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  return dpp_add<0x143, 0xC>(v);
 }
 
 // The sequences' work, scanned by one wave 64 sequences at a time; the first
@@ -104,6 +125,7 @@ struct WorkScan {
     sum0 = prefix(mine0);
   }
   __device__ int64_t prefix(int64_t s) const {  // inclusive
+    if (__ballot((uint64_t)s >> 25) == 0) return dpp_prefix((uint32_t)s);  // their sum fits 31 bits
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t o = shfl_up64(s, d);
@@ -114,10 +136,6 @@ struct WorkScan {
   __device__ int64_t scan(int base, int64_t &mine) const {
     mine = base + lane < a.sh.batch ? work_of<ROWS, TT>(a, seq_of(a, base + lane)) : 0;
     return prefix(mine);
-  }
-  static __device__ int64_t lane_value(int64_t v, int l) {
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, l), hi = __builtin_amdgcn_readlane((int)(v >> 32), l);
-    return (int64_t)(((uint64_t)hi << 32) | lo);
   }
   __device__ int64_t total() const {
     int64_t t = lane_value(sum0, 63), mine;
@@ -196,17 +214,18 @@ struct LaneAt {
   }
 };
 
+// off[tg]: byte offset of the first code row of the tile's 16-token group tg.
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &a, const LaneAt<D> &at, int64_t head_off, int token0,
-                                          const int (&page)[Geo<D>::TG], KvTile<D> &t) {
+__device__ __forceinline__ void load_tile(const AttnArgs &a, const LaneAt<D> &at, const int64_t (&off)[Geo<D>::TG],
+                                          KvTile<D> &t) {
   using G = Geo<D>;
   // 32-bit offsets from uniform bases, opaque so that they are not widened to 64-bit registers outside the loop
   const uint32_t k_at = opaque(at.k), ks_at = opaque(at.ks), v_at = opaque(at.v), vs_at = opaque(at.vs);
+  const uint32_t v_step = 4 * (uint32_t)a.token_stride, vs_step = v_step >> 4;
 #pragma unroll
   for (int tg = 0; tg < G::TG; ++tg) {
-    const int r = (token0 + 16 * tg) & ((1 << a.log_page) - 1);
-    const int64_t off = head_off + (int64_t)page[tg] * a.page_stride + r * a.token_stride;
-    const uint8_t *kc = a.kc + off, *vc = a.vc + off, *ks = a.ks + (off >> 4), *vs = a.vs + (off >> 4);
+    const uint8_t *kc = a.kc + off[tg], *vc = a.vc + off[tg];
+    const uint8_t *ks = a.ks + (off[tg] >> 4), *vs = a.vs + (off[tg] >> 4);
 #pragma unroll
     for (int p = 0; p < G::KP; ++p) {
       t.k[tg][p] = *reinterpret_cast<const typename G::KT *>(kc + (k_at + p * 64u));
@@ -214,8 +233,8 @@ __device__ __forceinline__ void load_tile(const AttnArgs &a, const LaneAt<D> &at
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      t.v[tg][j] = *reinterpret_cast<const typename G::VT *>((vc + 4 * j * a.token_stride) + v_at);
-      t.vs[tg][j] = (vs + j * (a.token_stride >> 2))[vs_at];
+      t.v[tg][j] = *reinterpret_cast<const typename G::VT *>(vc + (v_at + j * v_step));
+      t.vs[tg][j] = vs[vs_at + j * vs_step];
     }
   }
 }
@@ -463,9 +482,9 @@ struct Walk {
         if (++b >= a.sh.batch) return false;
         continue;
       }
-      const int64_t unit = attn_div(off, size);
-      int rt = uniform((int)attn_div(unit, a.sh.heads));
-      const int h = uniform((int)(unit - (int64_t)rt * a.sh.heads));
+      const int64_t unit = a.spans ? attn_div(off, size) : off;  // below 2^30 rows of 2^16 heads / 16
+      int rt = uniform((int)divide((uint32_t)unit, a.by_heads));
+      const int h = uniform((int)unit - rt * a.sh.heads);
       // causal: the last rows see the most keys; their workgroups start first
       if (!a.spans) rt = (int)wk.row_tiles - 1 - rt;
       const int64_t from = off - unit * size, here = end - pos < size - from ? end - pos : size - from;
@@ -484,8 +503,8 @@ struct Walk {
       u.r0 = (int64_t)rt * ROWS;
       const int64_t rows = (int64_t)sq.fresh * a.sh.groups;
       u.live = uniform((int)(rows - u.r0 < ROWS ? rows - u.r0 : ROWS));
-      u.i0 = uniform((int)attn_div(u.r0, a.sh.groups));
-      u.i1 = uniform((int)attn_div(u.r0 + u.live - 1, a.sh.groups));
+      u.i0 = uniform((int)divide((uint32_t)u.r0, a.by_groups));
+      u.i1 = uniform((int)divide((uint32_t)(u.r0 + u.live - 1), a.by_groups));
       u.keys_lo = uniform(attn_lo(a.sh, sq, 0));
       u.keys_hi = uniform(attn_hi(a.sh, sq, sq.fresh - 1));
       if (!u.whole && u.t0 == 0) {
@@ -505,7 +524,7 @@ struct Walk {
 
 // Position of row r of a unit among the rows of out and lse.
 __device__ __forceinline__ int64_t out_row(const AttnArgs &a, int64_t first, int h, int64_t r) {
-  const int64_t i = attn_div(r, a.sh.groups);
+  const int64_t i = divide((uint32_t)r, a.by_groups);
   return (first + i) * (a.sh.heads * a.sh.groups) + h * a.sh.groups + (r - i * a.sh.groups);
 }
 __device__ __forceinline__ float row_factor(float sum) { return sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum); }
@@ -561,7 +580,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
     for (int r = 0; r < NR; ++r) {
       const bool on = 16 * r + nn < u.live;
       const int64_t row = u.r0 + (on ? 16 * r + nn : 0);
-      const int i = (int)attn_div(row, a.sh.groups);
+      const int i = (int)divide((uint32_t)row, a.by_groups);
       const int qh = u.h * a.sh.groups + (int)(row - (int64_t)i * a.sh.groups);
       load_query<D>(a.q + (u.sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q[r]);
       lo[r] = attn_lo(a.sh, u.sq, i);
@@ -577,39 +596,40 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
     const int w0 = t0 + (int)((int64_t)nt * wave / NW), w1 = t0 + (int)((int64_t)nt * (wave + 1) / NW);
     const int64_t head_off = u.h * a.head_stride;
     const int32_t *row_table = a.table + u.b * a.table_stride;
-    // lane i holds the page of the i-th group of 16 tokens of a block of 64 groups; -1: none
+    // lane i holds the offset of the i-th group of 16 tokens of a block of 64 groups, and valid its bit: whether
+    // the group has a page (else the offset is that of page 0, whose bytes are masked)
     constexpr int BLOCK = 64 / TG;  // key tiles of it
-    auto pages_of = [&](int tile) {
+    auto groups_of = [&](int tile, uint64_t &valid) {
       const int tok = (u.lo + tile) * TT + 16 * lane;  // below 2^30 + 64 * 16
       int id = -1;
       if (tile < w1 && tok < u.keys_hi && tok + 15 >= u.keys_lo) id = page_of(a, row_table, tok, err);
-      return id;
+      valid = __ballot(id >= 0);
+      return head_off + (int64_t)max(id, 0) * a.page_stride +
+             (int64_t)(tok & ((1 << a.log_page) - 1)) * a.token_stride;
     };
-    auto fetch = [&](int tile, int ids, int first, KvTile<D> &t, uint32_t &ok) {
-      int page[TG];
-      ok = 0u;
+    auto fetch = [&](int i, int64_t offs, uint64_t valid, KvTile<D> &t, uint32_t &ok) {  // tile i of a block
+      int64_t off[TG];
 #pragma unroll
-      for (int tg = 0; tg < TG; ++tg) {
-        const int id = __builtin_amdgcn_readlane(ids, (tile - first) * TG + tg);
-        ok |= id >= 0 ? 1u << tg : 0u;
-        page[tg] = id < 0 ? 0 : id;
-      }
-      load_tile<D>(a, at, head_off, (u.lo + tile) * TT, page, t);
+      for (int tg = 0; tg < TG; ++tg) off[tg] = lane_value(offs, i * TG + tg);
+      ok = (uint32_t)(valid >> (i * TG)) & ((1u << TG) - 1u);
+      load_tile<D>(a, at, off, t);
     };
     if (w0 < w1) {
       int first = w0;
-      int ids = pages_of(first), ids_next = pages_of(first + BLOCK);
+      uint64_t valid, valid_next;
+      int64_t offs = groups_of(first, valid), offs_next = groups_of(first + BLOCK, valid_next);
       KvTile<D> even, odd;
       uint32_t ok_even, ok_odd = 0u;
-      fetch(w0, ids, first, even, ok_even);
+      fetch(0, offs, valid, even, ok_even);
       auto step = [&](int tile, const KvTile<D> &cur, uint32_t ok, KvTile<D> &nxt, uint32_t &ok_next) {
         if (tile + 1 < w1) {
           if (tile + 1 == first + BLOCK) {
             first += BLOCK;
-            ids = ids_next;
-            ids_next = pages_of(first + BLOCK);
+            offs = offs_next;
+            valid = valid_next;
+            offs_next = groups_of(first + BLOCK, valid_next);
           }
-          fetch(tile + 1, ids, first, nxt, ok_next);
+          fetch(tile + 1 - first, offs, valid, nxt, ok_next);
         }
         const int token0 = (u.lo + tile) * TT;
         const bool full = ok == (1u << TG) - 1u && token0 >= all_lo && token0 + TT <= all_hi;
@@ -767,8 +787,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     const int see_lo = attn_lo(a.sh, u.sq, u.i0) / TT, see_hi = (attn_hi(a.sh, u.sq, u.i1) + TT - 1) / TT;
     const int tb = uniform(max(u.lo + u.t0, see_lo)), te = uniform(min(u.lo + u.t1, see_hi));
     const int w_rows = u.live - W * wave;  // of the wave: W or fewer, none where it is not positive
-    const int j0 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? W * wave : 0), a.sh.groups));
-    const int j1 = uniform((int)attn_div(u.r0 + (w_rows > 0 ? W * wave + min(w_rows, W) - 1 : 0), a.sh.groups));
+    const int j0 = uniform((int)divide((uint32_t)(u.r0 + (w_rows > 0 ? W * wave : 0)), a.by_groups));
+    const int j1 = uniform((int)divide((uint32_t)(u.r0 + (w_rows > 0 ? W * wave + min(w_rows, W) - 1 : 0)), a.by_groups));
     const int all_lo = uniform(attn_lo(a.sh, u.sq, j1)), all_hi = uniform(attn_hi(a.sh, u.sq, j0));
 
     u32x4 q[NR][G::HG * 4];
@@ -779,7 +799,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     for (int r = 0; r < NR; ++r) {
       const bool on = 32 * r + n < w_rows;
       const int64_t row = u.r0 + (on ? W * wave + 32 * r + n : 0);
-      const int i = (int)attn_div(row, a.sh.groups);
+      const int i = (int)divide((uint32_t)row, a.by_groups);
       lo[r] = attn_lo(a.sh, u.sq, i);
       hi[r] = attn_hi(a.sh, u.sq, i);
       const uint16_t *qp = a.q + (u.sq.first + i) * a.q_st + (u.h * a.sh.groups + (row - (int64_t)i * a.sh.groups)) * a.q_sh;
@@ -1251,6 +1271,8 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   AttnArgs a;
   a.sh = AttnShape{tokens, (int)batch, (int)(q_heads / cache->heads), cache->heads, (int)max_new, (int)max_len,
                    causal, (int)window};
+  a.by_groups = make_divider((uint32_t)a.sh.groups);
+  a.by_heads = make_divider((uint32_t)a.sh.heads);
   a.q = (const uint16_t *)q;
   a.q_st = q_token_stride;
   a.q_sh = q_head_stride;

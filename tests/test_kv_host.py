@@ -210,6 +210,7 @@ extern "C" int64_t cut(int64_t total, int64_t spans, int64_t i) { return attn_cu
 extern "C" void part(int64_t from, int64_t to, int64_t n, int64_t *o) {
   AttnPart p = attn_part(from, to, (int)n); o[0] = p.t0; o[1] = p.t1;
 }
+extern "C" int64_t div_by(int64_t n, int64_t d) { return divide((uint32_t)n, make_divider((uint32_t)d)); }
 extern "C" int64_t unit_cost() { return kUnitCost; }
 extern "C" int64_t worth(int64_t total, int64_t spans) { return attn_spans(total, (int)spans); }
 extern "C" int64_t span_of(int64_t total, int64_t spans, int64_t p) { return attn_span_of(total, spans, p); }
@@ -228,6 +229,7 @@ def host(tmp_path_factory):
     P, I = ctypes.c_void_p, ctypes.c_int64
     lib.seq.argtypes, lib.keys.argtypes = [P, I, I, I, I, I, P], [P, I, I, I, I, P]
     lib.part.argtypes, lib.unit_cost.restype = [I, I, I, P], I
+    lib.div_by.argtypes, lib.div_by.restype = [I, I], I
     lib.worth.argtypes, lib.worth.restype = [I, I], I
     for f in (lib.cut, lib.span_of):
         f.argtypes, f.restype = [I, I, I], I
@@ -330,3 +332,14 @@ def test_units_of_spans_cover_every_tile_once_and_join(host):
             assert sum(parts[k][1] for k in slots) == tiles[u] and all(parts[k][0] == u for k in slots)
             used |= set(slots)
         assert used == set(parts)
+
+
+def test_divider_is_exact(host):
+    rng = np.random.default_rng(2)
+    for d in list(range(1, 300)) + [1 << k for k in range(17)] + [65535, 65521] + rng.integers(1, 65537, 200).tolist():
+        top = (2 ** 31 - 1) // d
+        ns = {0, 1, d - 1, d, d + 1, top * d - 1, top * d, 2 ** 31 - 1} | {int(q) * d + e for q in
+                                                                          rng.integers(1, top + 1, 5) for e in (-1, 0)}
+        for n in ns:
+            if 0 <= n < 2 ** 31:
+                assert host.div_by(n, d) == n // d, (n, d)

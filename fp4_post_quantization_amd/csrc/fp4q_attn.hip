@@ -1095,34 +1095,57 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
 // Joins the partial results of units that several spans share: workgroups
 // (w, y) join the rows y, y + gridDim.y, ... of the unit that begins in span w
 // and ends in a later one, from span w's second slot and the first slots of
-// the spans after it.
+// the spans after it; each wave takes every fourth part, up to eight at a time
+// with their loads together.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  using P = Part<D, ROWS>;
   constexpr int PER = D / 64;  // elements of a lane
   __shared__ float so[4][D];
   __shared__ float sm[4], sl[4];
   const int lane = threadIdx.x & 63, wave = wave_index();
-  const int64_t span = blockIdx.x;
+  const int span = blockIdx.x;
   const Join j = a.joins[span];
-  const int64_t last = j.last;
+  const int n = j.last - span + 1;
   for (int row = blockIdx.y; row < j.rows; row += gridDim.y) {
-    using P = Part<D, ROWS>;
     float m = kNegInf, l = 0.0f, o[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) o[k] = 0.0f;
-    for (int64_t s = span + wave; s <= last; s += 4) {
-      const int64_t slot = 2 * s + (s == span ? 1 : 0);
-      const float pm = P::m(a.parts, slot)[row], pl = P::l(a.parts, slot)[row];
-      const float *po = P::o(a.parts, slot) + row * D + lane * PER;
-      float v[PER];
+    auto take = [&](auto count, int base) {
+      constexpr int CH = decltype(count)::value;
+      float pm[CH], pl[CH], v[CH][PER];
 #pragma unroll
-      for (int k = 0; k < PER; ++k) v[k] = po[k];
-      const float top = fmaxf(m, pm);
-      const float f0 = part_weight(m, top), f1 = part_weight(pm, top);
+      for (int k = 0; k < CH; ++k) {
+        const int part = min(base + 4 * k, n - 1);
+        const int64_t slot = 2 * (int64_t)(span + part) + (part == 0 ? 1 : 0);
+        pm[k] = base + 4 * k < n ? P::m(a.parts, slot)[row] : kNegInf;
+        pl[k] = P::l(a.parts, slot)[row];
+        const float *po = P::o(a.parts, slot) + row * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[k][e] = po[e];
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) top = fmaxf(top, pm[k]);
+      const float f = part_weight(m, top);
       m = top;
-      l = l * f0 + pl * f1;
+      l *= f;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) o[k] = o[k] * f0 + v[k] * f1;
+      for (int e = 0; e < PER; ++e) o[e] *= f;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const float w = part_weight(pm[k], top);
+        l = fmaf(pl[k], w, l);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = fmaf(v[k][e], w, o[e]);
+      }
+    };
+    if (n <= 4) {
+      if (wave < n) take(std::integral_constant<int, 1>{}, wave);
+    } else if (n <= 8) {
+      take(std::integral_constant<int, 2>{}, wave);
+    } else {
+      for (int base = wave; base < n; base += 32) take(std::integral_constant<int, 8>{}, base);
     }
     if (lane == 0) {
       sm[wave] = m;
@@ -1132,7 +1155,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     for (int k = 0; k < PER; ++k) so[wave][lane * PER + k] = o[k];
     __syncthreads();
     if (threadIdx.x < D / 2) {
-      float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+      const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
       float sum = 0.0f, x = 0.0f, y = 0.0f;
       const int d = 2 * threadIdx.x;
 #pragma unroll
@@ -1160,6 +1183,7 @@ constexpr int kCus = 256;
 
 struct Plan {
   int rows;       // of a row tile: 16 (attn_rows_kernel), 128 or 256 (attn_prompt_kernel)
+  int waves;      // of attn_rows_kernel
   int64_t units;  // upper bound of (sequence, row tile, head) units
   int spans;
   int64_t part_floats;
@@ -1191,6 +1215,10 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
   const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
   const bool direct = tiles <= 34 || (p.units >= fit && (p.rows != 16 || tiles <= 66));
   p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
+  // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
+  // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26
+  // with four; 200 of up to 500, 25 and 32; 128 of up to 1000, 34 and 29.
+  p.waves = direct && p.units > 512 && tiles <= 18 ? 1 : 4;
   p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * p.rows * (head_dim + 2);
   return p;
 }
@@ -1210,8 +1238,10 @@ void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
   const dim3 grid((unsigned)(p.spans ? p.spans : p.units) + 1);
   if constexpr (ROWS >= 128)
     hipLaunchKernelGGL((attn_prompt_kernel<D, ROWS / 32>), grid, dim3(2 * ROWS), 0, s, a);
-  else
+  else if (p.waves == 4)
     hipLaunchKernelGGL((attn_rows_kernel<D, 4>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_rows_kernel<D, 1>), grid, dim3(64), 0, s, a);
   if (!p.spans) return;
   const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
   hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),

@@ -33,6 +33,9 @@ struct HeadMap {
   int rotary, interleaved, hadamard;
 };
 
+// n * stride for a non-negative 32-bit n: a product of 32 by 64 bits.
+__device__ __forceinline__ int64_t times(int n, int64_t stride) { return (int64_t)((uint64_t)(uint32_t)n * (uint64_t)stride); }
+
 __device__ __forceinline__ void load8(const uint16_t *p, float z[8]) {
   const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
@@ -69,13 +72,28 @@ __device__ __forceinline__ void store8(float *p, const float z[8]) {
   __builtin_nontemporal_store(f32x4{z[4], z[5], z[6], z[7]}, q + 1);
 }
 
+// Value of lane l ^ M of the wave, M a power of two up to 16.
+template <int M>
+__device__ __forceinline__ float lane_xor(float v) {
+  if constexpr (M <= 4) return xor_lane<M>(v);
+  else if constexpr (M == 8)  // 8 places round within the row of 16
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xF, 0xF, true));
+  else return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));  // and 0x1F, xor 16
+}
+template <int M>
+__device__ __forceinline__ double lane_xor(double v) {
+  const uint64_t b = __double_as_longlong(v);
+  const uint32_t lo = as_u(lane_xor<M>(as_f((uint32_t)b))), hi = as_u(lane_xor<M>(as_f((uint32_t)(b >> 32))));
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
 // One stage of the block Hadamard over lanes l and l ^ M.
 template <int M>
 __device__ __forceinline__ void hadamard_lanes(float z[8], int lane) {
   const bool hi = lane & M;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float o = __shfl_xor(z[i], M);
+    const float o = lane_xor<M>(z[i]);
     z[i] = hi ? (o - z[i]) : (z[i] + o);
   }
 }
@@ -104,34 +122,47 @@ __device__ __forceinline__ void hadamard8(float z[8], int n, int lane) {
   for (int i = 0; i < 8; ++i) z[i] = z[i] * c;
 }
 
-// The lane's 8 elements (chunk c) of the head at x after the map.  Every
-// lane of a head calls this together; active lanes have a head.  The sum of
+// What a lane loads of a head: its 8 elements (chunk c) and, where the head
+// is rotated in halves, the 8 that they are paired with; and where its angles
+// are.
+struct HeadLoad {
+  float z[8], p[8];
+  int64_t pos;
+};
+
+template <typename T>
+__device__ __forceinline__ void load_head(const T *x, int c, int64_t token, bool active, const HeadMap &m,
+                                          HeadLoad &h) {
+  const int half = m.rotary / 2, at = c * kChunk;
+  const bool turned = m.table != nullptr && at < m.rotary;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h.z[i] = h.p[i] = 0.0f;
+  h.pos = 0;
+  if (!active) return;
+  if (turned) {
+    h.pos = m.positions[token];
+    if (!m.interleaved) load8(x + (at < half ? at + half : at - half), h.p);
+  }
+  load8(x + at, h.z);
+}
+
+// The lane's 8 elements of a loaded head after the map.  Every lane of a head
+// calls this together; counts: whether a bad position is an error.  The sum of
 // squares is kept in float64, where the square of a float32 is exact and 256
 // of them lose at most 2^-45 of the sum, so r does not depend on the order
 // in which lanes add.
-template <typename T, int D>
-__device__ __forceinline__ void map_head(const T *x, int c, int lane, int64_t token, bool active, const HeadMap &m,
-                                         float z[8], uint32_t &err) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = 0.0f;
-  // the pair's other element, 8 elements at a time: chunk c + half / 8 or c - half / 8
+template <int D>
+__device__ __forceinline__ void map_head(HeadLoad &h, int c, int lane, bool counts, const HeadMap &m, uint32_t &err) {
   const int half = m.rotary / 2, at = c * kChunk;
   const bool turned = m.table != nullptr && at < m.rotary;
-  const bool first = at < half;
-  float p[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = 0.0f;
-  const int other = first ? at + half : at - half;
-  const bool paired = turned && !m.interleaved;
-  if (active) {
-    load8(x + at, z);
-    if (paired) load8(x + other, p);
-  }
+  const bool first = at < half, paired = turned && !m.interleaved;
+  float(&z)[8] = h.z;
+  float(&p)[8] = h.p;
   float cs[8], sn[8];
-  if (active && turned) {
-    int64_t pos = m.positions[token];
+  if (turned) {
+    int64_t pos = h.pos;
     if (pos < 0 || pos >= m.n_positions) {
-      err |= FP4Q_DATA_BAD_POSITION;
+      if (counts) err |= FP4Q_DATA_BAD_POSITION;
       pos = 0;
     }
     const float *row = m.table + pos * m.rotary;
@@ -153,20 +184,23 @@ __device__ __forceinline__ void map_head(const T *x, int c, int lane, int64_t to
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += (double)z[i] * (double)z[i];
-#pragma unroll
-    for (int d = 1; d < D / kChunk; d <<= 1) s += __shfl_xor(s, d);
+    s += lane_xor<1>(s);
+    s += lane_xor<2>(s);
+    s += lane_xor<4>(s);
+    if constexpr (D >= 128) s += lane_xor<8>(s);
+    if constexpr (D >= 256) s += lane_xor<16>(s);
     const float r = (float)(1.0 / sqrt(s * (1.0 / D) + m.eps));
     float w[8];
     load8(m.weight + at, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = (z[i] * r) * w[i];
     if (paired) {
-      load8(m.weight + other, w);
+      load8(m.weight + (first ? at + half : at - half), w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = (p[i] * r) * w[i];
     }
   }
-  if (active && turned) {
+  if (turned) {
     if (m.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -187,19 +221,20 @@ __device__ __forceinline__ void map_head(const T *x, int c, int lane, int64_t to
 
 // -------------------------------------------------------- rotate_heads ----
 template <typename T, typename OutT, int D>
-__global__ __launch_bounds__(kThreads) void rotate_heads_kernel(const T *x, int units, int heads, int64_t st,
+__global__ __launch_bounds__(kThreads) void rotate_heads_kernel(const T *x, int units, Divider heads, int64_t st,
                                                                  int64_t sh, HeadMap m, OutT *out,
                                                                  uint32_t *status) {
   constexpr int LPH = D / kChunk;
   const int lane = threadIdx.x & 63, c = threadIdx.x % LPH;
   const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
   const bool active = u < units;
-  const int token = active ? (int)((uint32_t)u / (uint32_t)heads) : 0;
-  const int h = active ? (int)u - token * heads : 0;
+  const int token = active ? (int)divide((uint32_t)u, heads) : 0;
+  const int h = active ? (int)u - token * (int)heads.d : 0;
   uint32_t err = 0u;
-  float z[8];
-  map_head<T, D>(x + token * st + h * sh, c, lane, token, active, m, z, err);
-  if (active) store8(out + u * D + c * kChunk, z);
+  HeadLoad l;
+  load_head(x + times(token, st) + times(h, sh), c, token, active, m, l);
+  map_head<D>(l, c, lane, active, m, err);
+  if (active) store8(out + u * D + c * kChunk, l.z);
   Status{status, true}.finish(err);
 }
 
@@ -211,8 +246,8 @@ struct CacheView {
   int64_t page_stride, head_stride, token_stride;
   // byte offset of a row's codes; its scales are at a sixteenth of it
   __device__ __forceinline__ int64_t at(int64_t slot, int h) const {
-    const int64_t page = slot >> log_page, r = slot & ((1 << log_page) - 1);
-    return page * page_stride + h * head_stride + r * token_stride;
+    const int page = (int)(slot >> log_page), r = (int)slot & ((1 << log_page) - 1);
+    return times(page, page_stride) + times(h, head_stride) + times(r, token_stride);
   }
 };
 
@@ -274,7 +309,8 @@ struct AppendArgs {
   const void *src[2];  // keys, values
   int64_t st[2], sh[2];
   const int64_t *slots;
-  int units, heads;  // units = tokens * heads of each
+  int units;  // tokens * heads of each
+  Divider heads;
   HeadMap m;
   int lo, hi;
   CacheView cache;
@@ -289,31 +325,31 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   const int lane = threadIdx.x & 63, c = threadIdx.x % LPH;
   const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
   uint32_t err = 0u;
-  bool active = u < a.units;
-  const int token = active ? (int)((uint32_t)u / (uint32_t)a.heads) : 0;
-  const int h = active ? (int)u - token * a.heads : 0;
-  int64_t slot = -1;
-  if (active) {
-    slot = a.slots[token];
-    if (slot >= a.cache.rows) {
-      err |= FP4Q_DATA_BAD_SLOT;
-      slot = -1;
-    }
-  }
-  active = slot >= 0;
-  const T *x = static_cast<const T *>(a.src[kv]) + token * a.st[kv] + h * a.sh[kv];
-  float z[8];
+  const bool here = u < a.units;
+  const int token = here ? (int)divide((uint32_t)u, a.heads) : 0;
+  const int h = here ? (int)u - token * (int)a.heads.d : 0;
+  // a skipped token's row is loaded all the same, so that nothing waits for its slot
+  const T *x = static_cast<const T *>(a.src[kv]) + times(token, a.st[kv]) + times(h, a.sh[kv]);
+  int64_t slot = here ? a.slots[token] : -1;
+  HeadLoad l;
   if (kv == 0) {
-    map_head<T, D>(x, c, lane, token, active, a.m, z, err);
+    load_head(x, c, token, here, a.m, l);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = 0.0f;
-    if (active) load8(x + c * kChunk, z);
+    for (int i = 0; i < 8; ++i) l.z[i] = 0.0f;
+    if (here) load8(x + c * kChunk, l.z);
   }
+  if (slot >= a.cache.rows) {
+    err |= FP4Q_DATA_BAD_SLOT;
+    slot = -1;
+  }
+  const bool active = slot >= 0;
+  if (kv == 0) map_head<D>(l, c, lane, active, a.m, err);
+  const float(&z)[8] = l.z;
   bool finite = true;
 #pragma unroll
   for (int i = 0; i < 8; ++i) finite &= fabsf(z[i]) <= 3.402823466e38f;
-  if (!finite) err |= FP4Q_DATA_NONFINITE_INPUT;
+  if (!finite && active) err |= FP4Q_DATA_NONFINITE_INPUT;
   int E;
   const uint32_t codes = quantize_quad(z, a.lo, a.hi, E);
   if (active) {
@@ -329,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
 // ------------------------------------------------------------- kv_read ----
 template <typename OutT, int D>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, const int64_t *__restrict__ slots,
-                                                            int units, int heads, OutT *k_out, OutT *v_out,
+                                                            int units, Divider heads, OutT *k_out, OutT *v_out,
                                                             uint32_t *status) {
   constexpr int LPH = D / kChunk;
   const int kv = blockIdx.y;
@@ -338,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, cons
   const int64_t u = (int64_t)blockIdx.x * (kThreads / LPH) + threadIdx.x / LPH;
   uint32_t err = 0u;
   if (u < units) {
-    const int token = (int)((uint32_t)u / (uint32_t)heads), h = (int)u - token * heads;
+    const int token = (int)divide((uint32_t)u, heads), h = (int)u - token * (int)heads.d;
     int64_t slot = slots[token];
     if (slot >= cache.rows) {
       err |= FP4Q_DATA_BAD_SLOT;
@@ -430,8 +466,8 @@ extern "C" fp4q_status_t fp4q_rotate_heads(const void *x, fp4q_dtype_t dtype, in
       using T = std::remove_pointer_t<decltype(tp)>;
       with_type(out_dtype, [&](auto op) {
         using O = std::remove_pointer_t<decltype(op)>;
-        hipLaunchKernelGGL((rotate_heads_kernel<T, O, D>), grid, dim3(kThreads), 0, s, (const T *)x, units, (int)heads,
-                           token_stride, head_stride, m, (O *)out, status);
+        hipLaunchKernelGGL((rotate_heads_kernel<T, O, D>), grid, dim3(kThreads), 0, s, (const T *)x, units,
+                           make_divider((uint32_t)heads),                           token_stride, head_stride, m, (O *)out, status);
       });
     });
   });
@@ -461,7 +497,7 @@ extern "C" fp4q_status_t fp4q_kv_append_mxfp4(const fp4q_kv_cache_t *cache, cons
     return hip_status();
   }
   const AppendArgs a{{k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, slots,
-                     (int)(tokens * cache->heads), cache->heads, head_map(*map), off_lo, off_hi, view(*cache),
+                     (int)(tokens * cache->heads), make_divider((uint32_t)cache->heads), head_map(*map), off_lo, off_hi, view(*cache),
                      status};
   with_dim(cache->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
@@ -499,8 +535,8 @@ extern "C" fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const 
     const dim3 grid((unsigned)(((int64_t)units + U - 1) / U), 2);
     with_type(out_dtype, [&](auto op) {
       using O = std::remove_pointer_t<decltype(op)>;
-      hipLaunchKernelGGL((kv_read_kernel<O, D>), grid, dim3(kThreads), 0, s, c, slots, units, cache->heads,
-                         (O *)k_out, (O *)v_out, status);
+      hipLaunchKernelGGL((kv_read_kernel<O, D>), grid, dim3(kThreads), 0, s, c, slots, units,
+                         make_divider((uint32_t)cache->heads),                         (O *)k_out, (O *)v_out, status);
     });
   });
   return hip_status();

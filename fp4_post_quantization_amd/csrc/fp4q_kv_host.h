@@ -95,8 +95,6 @@ inline fp4q_status_t kv_check_cache(const fp4q_kv_cache_t &c) {
   return FP4Q_OK;
 }
 
-// ------------------------------------------------- attention's work list ----
-
 // Division of numbers below 2^31 by a fixed d (1 .. 65536): with l the least
 // power of two 2^l >= d and m = ceil(2^(31 + l) / d), m d exceeds 2^(31 + l)
 // by less than d <= 2^l, so n m / 2^(31 + l) exceeds n / d by less than
@@ -110,6 +108,8 @@ inline Divider make_divider(uint32_t d) {
   return Divider{d, (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
 }
 FP4Q_HD uint32_t divide(uint32_t n, const Divider &v) { return (uint32_t)(((uint64_t)n * v.m) >> v.shift); }
+
+// ------------------------------------------------- attention's work list ----
 
 struct AttnShape {
   int64_t tokens;       // rows of q

@@ -54,16 +54,11 @@ __device__ __forceinline__ void load8(const float *p, float z[8]) {
   }
 }
 
-// bfloat16 nearest to f, ties to even (NaN stays NaN).
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = as_u(f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-__device__ __forceinline__ void store8(uint16_t *p, const float z[8]) {
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void store8(uint16_t *p, const float z[8]) {  // to nearest, ties to even
   u32x4 w;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = bf16_bits(z[2 * k]) | (bf16_bits(z[2 * k + 1]) << 16);
+  for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)z[2 * k], (__bf16)z[2 * k + 1]});
   __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(p));
 }
 __device__ __forceinline__ void store8(float *p, const float z[8]) {
@@ -90,12 +85,9 @@ __device__ __forceinline__ double lane_xor(double v) {
 // One stage of the block Hadamard over lanes l and l ^ M.
 template <int M>
 __device__ __forceinline__ void hadamard_lanes(float z[8], int lane) {
-  const bool hi = lane & M;
+  const uint32_t flip = lane & M ? 0x80000000u : 0u;  // the upper lane takes o - z, which is o + -z
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float o = lane_xor<M>(z[i]);
-    z[i] = hi ? (o - z[i]) : (z[i] + o);
-  }
+  for (int i = 0; i < 8; ++i) z[i] = lane_xor<M>(z[i]) + as_f(as_u(z[i]) ^ flip);
 }
 
 // fp4q_block_hadamard's stages on a lane's 8 elements: h = 1, 2, 4 inside
@@ -209,11 +201,9 @@ __device__ __forceinline__ void map_head(HeadLoad &h, int c, int lane, bool coun
         z[2 * i + 1] = b * cs[i] + a * sn[i];
       }
     } else {
+      const uint32_t flip = first ? 0x80000000u : 0u;  // a c - b s is a c + -b s
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = p[i] * sn[i];
-        z[i] = first ? z[i] * cs[i] - t : z[i] * cs[i] + t;
-      }
+      for (int i = 0; i < 8; ++i) z[i] = z[i] * cs[i] + as_f(as_u(p[i]) ^ flip) * sn[i];
     }
   }
   if (m.hadamard) hadamard8(z, m.hadamard, lane);
@@ -270,14 +260,16 @@ __device__ __forceinline__ float chain8(const float z[8], const float q[8], floa
 // fp4q_quantize_mxfp4 of a block of 32 spread over a quad: the base
 // exponent from the block's maximum, then the window's exponents in
 // ascending order with the loss as one chain in element order, handed from
-// lane to lane.  Returns the lane's 8 codes; E is the block's exponent.
-__device__ __forceinline__ uint32_t quantize_quad(const float z[8], int lo, int hi, int &E) {
-  float a = 0.0f;
+// lane to lane.  Returns the lane's 8 codes; E is the block's exponent.  Codes
+// and E of a block that is not finite mean nothing.
+__device__ __forceinline__ uint32_t quantize_quad(const float z[8], int lo, int hi, int &E, bool &finite) {
+  uint32_t a = 0u;  // the order of |z|'s bits is the order of |z|, infinities and NaN above
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(z[i]));
-  a = fmaxf(a, xor_lane<1>(a));
-  a = fmaxf(a, xor_lane<2>(a));
-  const int eb = mx_base_exponent(a);
+  for (int i = 0; i < 8; ++i) a = max(a, as_u(z[i]) & 0x7FFFFFFFu);
+  a = max(a, as_u(xor_lane<1>(as_f(a))));
+  a = max(a, as_u(xor_lane<2>(as_f(a))));
+  finite = a < 0x7F800000u;
+  const int eb = mx_base_exponent(as_f(a));
   E = max(-127, eb + lo);
   if (lo < hi) {
     float best = __builtin_inff();
@@ -346,12 +338,10 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   const bool active = slot >= 0;
   if (kv == 0) map_head<D>(l, c, lane, active, a.m, err);
   const float(&z)[8] = l.z;
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) finite &= fabsf(z[i]) <= 3.402823466e38f;
-  if (!finite && active) err |= FP4Q_DATA_NONFINITE_INPUT;
   int E;
-  const uint32_t codes = quantize_quad(z, a.lo, a.hi, E);
+  bool finite;
+  const uint32_t codes = quantize_quad(z, a.lo, a.hi, E, finite);
+  if (!finite && active) err |= FP4Q_DATA_NONFINITE_INPUT;
   if (active) {
     const int64_t row = a.cache.at(slot, h);
     *reinterpret_cast<uint32_t *>(a.cache.codes[kv] + row + c * 4) = codes;
@@ -382,6 +372,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, cons
     }
     if (out) {
       float z[8];
+      u32x4 raw = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = 0.0f;
       if (slot >= 0) {
@@ -389,11 +380,21 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, cons
         const uint32_t w = *reinterpret_cast<const uint32_t *>(cache.codes[kv] + row + c * 4);
         const uint32_t b = cache.scales[kv][row / 16 + c / 4];
         const float s = b == 255u ? __builtin_nanf("") : pow2f((int)b - 127);
-        fp4x8_to_f32(w, z);
+        if constexpr (sizeof(OutT) == 2) {  // the conversion takes b in the exponent bits of its scale
+          const float e = as_f(b << 23);
+          raw = u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, e, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, e, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, e, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, e, 3))};
+        } else {
+          fp4x8_to_f32(w, z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = z[i] * s;
+          for (int i = 0; i < 8; ++i) z[i] = z[i] * s;
+        }
       }
-      store8(out + u * D + c * kChunk, z);
+      OutT *to = out + u * D + c * kChunk;
+      if constexpr (sizeof(OutT) == 2) __builtin_nontemporal_store(raw, reinterpret_cast<u32x4 *>(to));
+      else store8(to, z);
     }
   }
   const Status st{status, true};

@@ -1269,7 +1269,7 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
                                               int64_t window, void *out, float *lse, void *workspace,
                                               size_t workspace_bytes, void *stream) {
   const bool empty = tokens == 0 || batch == 0;
-  if (!cache || (!empty && (!q || !block_table || !seq_lens || !out))) return FP4Q_ERR_NULL;
+  if (!cache || (!empty && (!q || (!block_table && max_len > 0) || !seq_lens || !out))) return FP4Q_ERR_NULL;
   fp4q_status_t st = kv_check_cache(*cache);
   if (st != FP4Q_OK) return st;
   if (!sizes_ok(tokens, batch, q_heads, cache->heads, cache->head_dim, max_new, max_len)) return FP4Q_ERR_SHAPE;
@@ -1294,10 +1294,6 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
     return hip_status();
   }
   const Plan p = make_plan(tokens, batch, q_heads, cache->heads, cache->head_dim, max_new, max_len, window);
-  if (p.units == 0) {  // no sequence has a row
-    hipLaunchKernelGGL(attn_status_kernel, dim3(1), dim3(64), 0, s, status);
-    return hip_status();
-  }
   AttnArgs a;
   a.sh = AttnShape{tokens, (int)batch, (int)(q_heads / cache->heads), cache->heads, (int)max_new, (int)max_len,
                    causal, (int)window};

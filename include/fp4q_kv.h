@@ -46,9 +46,8 @@ extern "C" {
  *   codes of (p, h, r) start at p * page_stride + h * head_stride +
  *   r * token_stride (bytes), the same for keys and values; scales start at
  *   a sixteenth of that offset, so they lie in the same order as the codes.
- *   Strides are multiples of 64 (those of heads and rows of head_dim 64: of
- *   32) and do not make rows overlap, the code pointers are 16-byte aligned
- *   and the scale pointers 4-byte (head_dim 64: 2-byte), page_size is a power of two from 16 to
+ *   Strides are multiples of 16 and do not make rows overlap, the code
+ *   pointers are 16-byte aligned, page_size is a power of two from 16 to
  *   1024, heads * head_dim at most 65536, and pages * page_size * heads below
  *   2^40.  Any byte may be in the rows that no token was written to. */
 typedef struct fp4q_kv_cache {
@@ -144,7 +143,8 @@ fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *sl
  *            each, tokens == batch.
  *   block_table, seq_lens, cu_q  int32, 4-byte aligned; table_width is the
  *            number of entries of a row of the table.  Entries past a
- *            sequence's last page are not read.
+ *            sequence's last page are not read.  block_table may be NULL
+ *            where max_len is 0.
  *   max_new, max_len  no sequence has more rows of q, or more cached tokens
  *            (max_len at most table_width * page_size and 2^30).
  *   causal   1: row i of n sees the keys up to its own position, seq_len - n
@@ -152,7 +152,8 @@ fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *sl
  *   window   0: no limit; w > 0: no row sees keys at its position minus w or
  *            before.
  *   scale    factor of the scores (float32).
- *   out      [tokens][q_heads][head_dim] bfloat16, dense, 16-byte aligned.
+ *   out      [tokens][q_heads][head_dim] bfloat16, dense, 16-byte aligned;
+ *            it must not overlap the inputs.
  *   lse      [tokens][q_heads] float32 natural logarithm of the row's sum of
  *            exp(scores), or NULL.
  * A row that sees no key gets zeros and minus infinity.  Rows of q that

@@ -413,6 +413,90 @@ def test_attention_leaves_other_rows_alone():
     assert bool((out == 3).all())
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,news", [([700, 90], [1, 1]), ([9000], [1]), ([300, 5], [3, 2])])
+def test_attention_many_query_heads_on_one(dim, lens, news):
+    """128 query heads on one cache head: many rows for few tokens."""
+    _run(_fq(), np.random.default_rng(dim), lens, news, 128, 1, dim, 64)
+
+
+@pytest.mark.parametrize("dim,order", [(64, "pthd"), (64, "hptd"), (256, "pthd")])
+def test_attention_prompts_in_other_orders(dim, order):
+    rng = np.random.default_rng(dim)
+    rows = np.array([0, 1, 63, 64, 127, 128, 200, 299])
+    _run(_fq(), rng, [300, 211, 1100], [300, 200, 120], 6, 3, dim, 16, order=order, rows=rows)
+
+
+def test_attention_long_prompts_split_and_whole():
+    """Chunks of prompts on long contexts, whose keys several workgroups share, and prompts with enough rows to fill
+    the chip, 128 and 256 rows a workgroup."""
+    rows = np.array([0, 31, 32, 63, 64, 127, 128, 255, 256, 511, 700, 1023])
+    _run(_fq(), np.random.default_rng(1), [9000, 5000], [130, 40], 8, 2, 128, 64, rows=rows)
+    _run(_fq(), np.random.default_rng(2), [6000], [200], 4, 1, 256, 128, rows=rows)
+    _run(_fq(), np.random.default_rng(3), [7000, 300], [150, 300], 6, 2, 64, 32, window=4500, rows=rows)
+    _run(_fq(), np.random.default_rng(4), [3000], [2900], 24, 2, 64, 64, rows=np.array([0, 1000, 2047, 2048, 2899]))
+    _run(_fq(), np.random.default_rng(5), [2300], [2200], 128, 8, 128, 64, rows=np.array([0, 1111, 2199]))
+
+
+def test_attention_rows_with_nan_keep_to_themselves():
+    fq = _fq()
+    rng = np.random.default_rng(21)
+    for new in (1, 3, 150):
+        cache = _filled(fq, rng, 12, 2, 16, 128)
+        lens = torch.tensor([180], dtype=torch.int32, device=DEV)
+        ids = torch.from_numpy(rng.permutation(12).astype(np.int32))[None].to(DEV)
+        cu = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+        q = torch.from_numpy(rng.standard_normal((new, 8, 128)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+        want = fq.attention_mxfp4(q, cache, ids, lens, cu, check=True)
+        bad = q.clone()
+        bad[new // 2, 3, 7], bad[0, 6, 0] = float("nan"), float("inf")
+        got = fq.attention_mxfp4(bad, cache, ids, lens, cu, check=True)
+        hit = torch.zeros(new, 8, dtype=torch.bool, device=DEV)
+        hit[new // 2, 3] = hit[0, 6] = True
+        assert torch.equal(got[~hit], want[~hit]), new
+        assert bool(torch.isnan(got[new // 2, 3]).all())
+
+
+def test_attention_without_keys_or_table():
+    fq = _fq()
+    cache = fq.kv_cache_mxfp4(1, 2, 16, 64, DEV)
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    lens = torch.zeros(3, dtype=torch.int32, device=DEV)
+    for width in (0, 1):
+        o, lse = fq.attention_mxfp4(q, cache, torch.zeros((3, width), dtype=torch.int32, device=DEV), lens,
+                                    return_lse=True, check=True)
+        assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    with pytest.raises(fq.FP4QError, match="page number"):
+        fq.attention_mxfp4(q, cache, torch.zeros((3, 1), dtype=torch.int32, device=DEV), lens + 9, max_len=0,
+                           check=True)
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device=DEV)
+    with pytest.raises(fq.FP4QError, match="row offset"):
+        fq.attention_mxfp4(q, cache, torch.zeros((3, 1), dtype=torch.int32, device=DEV), lens, cu, max_new=0,
+                           check=True)
+
+
+def test_attention_bad_pages_in_every_kernel():
+    """A page number out of range masks its tokens and is reported, whichever kernel the sizes choose; sequences
+    beside it are as they would be."""
+    fq = _fq()
+    rng = np.random.default_rng(31)
+    for lens, new in (([600, 600], 1), ([5000, 5000], 1), ([600, 600], 300), ([5000, 5000], 40)):
+        width = -(-max(lens) // 64)
+        cache = _filled(fq, rng, 2 * width, 2, 64, 64)
+        ids = torch.from_numpy(rng.permutation(2 * width).reshape(2, width).astype(np.int32))
+        cu = torch.tensor([0, new, 2 * new], dtype=torch.int32, device=DEV)
+        q = torch.from_numpy(rng.standard_normal((2 * new, 8, 64)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+        le = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        good = fq.attention_mxfp4(q, cache, ids.to(DEV), le, cu, check=True)
+        bad = ids.clone()
+        bad[0, width // 2] = 2 * width
+        bad[0, 0] = -3
+        with pytest.raises(fq.FP4QError, match="page number"):
+            fq.attention_mxfp4(q, cache, bad.to(DEV), le, cu, check=True)
+        got = fq.attention_mxfp4(q, cache, bad.to(DEV), le, cu)
+        assert torch.equal(got[new:], good[new:]) and bool(torch.isfinite(got).all())
+
+
 def test_attention_strided_queries_and_padded_table():
     fq = _fq()
     rng = np.random.default_rng(6)

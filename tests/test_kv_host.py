@@ -93,8 +93,6 @@ CACHE_FAULTS = [
     (dict(hs=64 * 32), "ERR_SHAPE"),                  # heads overlap
     (dict(ps=64 * 64), "ERR_SHAPE"),                  # pages overlap
     (dict(ts=72, hs=72 * 64, ps=72 * 128), "ERR_ALIGN"), (dict(kc=X + 4), "ERR_ALIGN"),
-    (dict(ts=80, hs=80 * 64, ps=80 * 128), "ERR_ALIGN"), (dict(ks=X + 2), "ERR_ALIGN"),
-    (dict(ps=64 * 2 * 64 + 32), "ERR_ALIGN"),
 ]
 
 

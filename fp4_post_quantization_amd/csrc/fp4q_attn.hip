@@ -286,82 +286,73 @@ struct RowState {
 };
 
 // One key tile: scores, softmax, and the tile's part of the output.
-template <int D, int NR>
-__device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> &t, const QFrag<D> (&q)[NR],
-                                             const int (&lo)[NR], const int (&hi)[NR], int token0, bool full,
+template <int D>
+__device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> &t, const QFrag<D> &q, int lo,
+                                             int hi, int token0, bool full,
                                              uint32_t groups_ok, int keys_lo, int keys_hi, int lane,
-                                             RowState<D> (&st)[NR]) {
+                                             RowState<D> &st) {
   using G = Geo<D>;
   const int g = lane >> 4;
-  f32x4 s[NR][G::TG];
+  f32x4 s[G::TG];
 #pragma unroll
   for (int tg = 0; tg < G::TG; ++tg) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) s[r][tg] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    s[tg] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < G::KP; ++k) {
       const float ks = as_f(t.ks[tg][k] << 23);
 #pragma unroll
       for (int w = 0; w < G::KW; ++w) {
         const bf16x8 kv = fp4x8_to_bf16(t.k[tg][k][w], ks);
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-          s[r][tg] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              kv, __builtin_bit_cast(bf16x8, q[r].x[k * G::KW + w]), s[r][tg], 0, 0, 0);
+        s[tg] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              kv, __builtin_bit_cast(bf16x8, q.x[k * G::KW + w]), s[tg], 0, 0, 0);
       }
     }
   }
-  uint32_t p[NR][G::TG / 2][4];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    float mx = kNegInf;
+  for (int tg = 0; tg < G::TG; ++tg)
 #pragma unroll
-    for (int tg = 0; tg < G::TG; ++tg) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[r][tg][i] *= a.scale_log2;
-      }
-    }
-    if (!full) {
-      not_speculated();
-#pragma unroll
-      for (int tg = 0; tg < G::TG; ++tg) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = token0 + 16 * tg + 4 * i + g;
-          s[r][tg][i] = (tok >= lo[r]) & (tok < hi[r]) & ((groups_ok >> tg) & 1u) ? s[r][tg][i] : kNegInf;
-        }
-      }
-    }
-#pragma unroll
-    for (int tg = 0; tg < G::TG; ++tg)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[r][tg][i]);
-    // the running maximum moves only when a score passes it by more than 2^8: until then the exponentials stay
-    // below 2^8, and neither the sum nor the outputs need rescaling
-    if (__ballot(mx > st[r].m + 8.0f)) {
-      mx = fmaxf(mx, xor16(mx));
-      mx = fmaxf(mx, xor32(mx));
-      const float m = fmaxf(st[r].m, mx);
-      const float shrink = st[r].m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(st[r].m - m);
-      st[r].m = m;
-      st[r].l *= shrink;
-#pragma unroll
-      for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st[r].o[dt][i] *= shrink;
-    }
-    const float ref = st[r].m == kNegInf ? 0.0f : st[r].m;
+    for (int i = 0; i < 4; ++i) s[tg][i] *= a.scale_log2;
+  if (!full) {
+    not_speculated();
 #pragma unroll
     for (int tg = 0; tg < G::TG; ++tg) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[r][tg][i] = __builtin_amdgcn_exp2f(s[r][tg][i] - ref);
-        st[r].l += s[r][tg][i];
+        const int tok = token0 + 16 * tg + 4 * i + g;
+        s[tg][i] = (tok >= lo) & (tok < hi) & ((groups_ok >> tg) & 1u) ? s[tg][i] : kNegInf;
       }
-      p[r][tg / 2][2 * (tg & 1)] = pack_bf16(s[r][tg][0], s[r][tg][1]);
-      p[r][tg / 2][2 * (tg & 1) + 1] = pack_bf16(s[r][tg][2], s[r][tg][3]);
     }
+  }
+  float mx = kNegInf;
+#pragma unroll
+  for (int tg = 0; tg < G::TG; ++tg)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[tg][i]);
+  // the running maximum moves only when a score passes it by more than 2^8: until then the exponentials stay
+  // below 2^8, and neither the sum nor the outputs need rescaling
+  if (__ballot(mx > st.m + 8.0f)) {
+    mx = fmaxf(mx, xor16(mx));
+    mx = fmaxf(mx, xor32(mx));
+    const float m = fmaxf(st.m, mx);
+    const float shrink = st.m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(st.m - m);
+    st.m = m;
+    st.l *= shrink;
+#pragma unroll
+    for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.o[dt][i] *= shrink;
+  }
+  const float ref = st.m == kNegInf ? 0.0f : st.m;
+  uint32_t p[G::TG / 2][4];
+#pragma unroll
+  for (int tg = 0; tg < G::TG; ++tg) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[tg][i] = __builtin_amdgcn_exp2f(s[tg][i] - ref);
+      st.l += s[tg][i];
+    }
+    p[tg / 2][2 * (tg & 1)] = pack_bf16(s[tg][0], s[tg][1]);
+    p[tg / 2][2 * (tg & 1) + 1] = pack_bf16(s[tg][2], s[tg][3]);
   }
 #pragma unroll
   for (int h = 0; h < G::TG / 2; ++h) {
@@ -385,12 +376,7 @@ __device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> 
         }
       }
     }
-    bf16x8 pv[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const u32x4 w = {p[r][h][0], p[r][h][1], p[r][h][2], p[r][h][3]};
-      pv[r] = __builtin_bit_cast(bf16x8, w);
-    }
+    const bf16x8 pv = __builtin_bit_cast(bf16x8, u32x4{p[h][0], p[h][1], p[h][2], p[h][3]});
 #pragma unroll
     for (int d2 = 0; d2 < G::DT / 2; ++d2) {  // elements 2 d2 and 2 d2 + 1 of the lane
       uint32_t x[8];
@@ -410,13 +396,10 @@ __device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> 
         e0[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x05040100u);
         e1[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x07060302u);
       }
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        st[r].o[2 * d2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e0), pv[r],
-                                                                  st[r].o[2 * d2], 0, 0, 0);
-        st[r].o[2 * d2 + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e1), pv[r],
-                                                                      st[r].o[2 * d2 + 1], 0, 0, 0);
-      }
+      st.o[2 * d2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e0), pv,
+                                                             st.o[2 * d2], 0, 0, 0);
+      st.o[2 * d2 + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e1), pv,
+                                                                 st.o[2 * d2 + 1], 0, 0, 0);
     }
   }
 }
@@ -558,7 +541,7 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_tab
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(AttnArgs a) {
   using G = Geo<D>;
-  constexpr int NR = 1, ROWS = 16 * NR, TT = G::TT, TG = G::TG;
+  constexpr int ROWS = 16, TT = G::TT, TG = G::TG;
   constexpr int LD = D + 4;  // padded row of the merge buffer
   __shared__ __align__(16) float mo[NW][16][LD];
   __shared__ float mm[NW][16], ml[NW][16];
@@ -573,23 +556,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
     // keys that all rows of the tile see
     const int all_lo = uniform(attn_lo(a.sh, u.sq, u.i1)), all_hi = uniform(attn_hi(a.sh, u.sq, u.i0));
     const int ln = opaque(lane), ng = ln >> 4, nn = ln & 15;
-    QFrag<D> q[NR];
-    RowState<D> st[NR];
-    int lo[NR], hi[NR];
+    QFrag<D> q;
+    RowState<D> st;
+    const bool on = nn < u.live;
+    const int64_t row = u.r0 + (on ? nn : 0);
+    const int i = (int)divide((uint32_t)row, a.by_groups);
+    const int qh = u.h * a.sh.groups + (int)(row - (int64_t)i * a.sh.groups);
+    load_query<D>(a.q + (u.sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q);
+    const int lo = attn_lo(a.sh, u.sq, i), hi = attn_hi(a.sh, u.sq, i);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const bool on = 16 * r + nn < u.live;
-      const int64_t row = u.r0 + (on ? 16 * r + nn : 0);
-      const int i = (int)divide((uint32_t)row, a.by_groups);
-      const int qh = u.h * a.sh.groups + (int)(row - (int64_t)i * a.sh.groups);
-      load_query<D>(a.q + (u.sq.first + i) * a.q_st + qh * a.q_sh, on, ng, q[r]);
-      lo[r] = attn_lo(a.sh, u.sq, i);
-      hi[r] = attn_hi(a.sh, u.sq, i);
-#pragma unroll
-      for (int dt = 0; dt < G::DT; ++dt) st[r].o[dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      st[r].m = kNegInf;
-      st[r].l = 0.0f;
-    }
+    for (int dt = 0; dt < G::DT; ++dt) st.o[dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    st.m = kNegInf;
+    st.l = 0.0f;
 
     // the workgroup's tiles, a contiguous part for each wave
     const int nt = t1 - t0;
@@ -633,7 +611,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
         }
         const int token0 = (u.lo + tile) * TT;
         const bool full = ok == (1u << TG) - 1u && token0 >= all_lo && token0 + TT <= all_hi;
-        consume_tile<D, NR>(a, cur, q, lo, hi, token0, full, ok, u.keys_lo, u.keys_hi, lane, st);
+        consume_tile<D>(a, cur, q, lo, hi, token0, full, ok, u.keys_lo, u.keys_hi, lane, st);
       };
       for (int tile = w0; tile < w1; tile += 2) {
         step(tile, even, ok_even, odd, ok_odd);
@@ -643,61 +621,58 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
 
     // merge the waves, 16 rows at a time
     const int mt = opaque((int)threadIdx.x), mn = mt & 15, mg = (mt >> 4) & 3;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float l = st[r].l;
-      l += xor16(l);
-      l += xor32(l);
-      if (mg == 0) {
-        mm[wave][mn] = st[r].m;
-        ml[wave][mn] = l;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int dt = 0; dt < G::DT; dt += 4)
-          *reinterpret_cast<f32x4 *>(&mo[wave][mn][(4 * mg + i) * G::DT + dt]) =
-              f32x4{st[r].o[dt][i], st[r].o[dt + 1][i], st[r].o[dt + 2][i], st[r].o[dt + 3][i]};
-      __syncthreads();
-      // 8 elements of a row a thread
-      for (int e = mt; e < 16 * D / 8; e += 64 * NW) {
-        const int row = e / (D / 8), d = e % (D / 8) * 8;
-        if (16 * r + row >= u.live) continue;
-        float top = mm[0][row];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w][row]);
-        float sum = 0.0f, o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float f = part_weight(mm[w][row], top);
-          sum = fmaf(ml[w][row], f, sum);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = fmaf(mo[w][row][d + k], f, o[k]);
-        }
-        if (u.whole) {
-          const float inv = row_factor(sum);
-          const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + 16 * r + row);
-          u32x4 w;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-          *reinterpret_cast<u32x4 *>(a.out + head * D + d) = w;
-          if (a.lse && d == 0) a.lse[head] = row_lse(top, sum);
-        } else {
-          using P = Part<D, ROWS>;
-          const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (t0 == 0 ? 1 : 0);
-          float *po = P::o(a.parts, slot) + (16 * r + row) * D + d;
-          *reinterpret_cast<f32x4 *>(po) = f32x4{o[0], o[1], o[2], o[3]};
-          *reinterpret_cast<f32x4 *>(po + 4) = f32x4{o[4], o[5], o[6], o[7]};
-          if (d == 0) {
-            P::m(a.parts, slot)[16 * r + row] = top;
-            P::l(a.parts, slot)[16 * r + row] = sum;
-          }
-        }
-      }
-      __syncthreads();
+    float l = st.l;
+    l += xor16(l);
+    l += xor32(l);
+    if (mg == 0) {
+      mm[wave][mn] = st.m;
+      ml[wave][mn] = l;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int dt = 0; dt < G::DT; dt += 4)
+        *reinterpret_cast<f32x4 *>(&mo[wave][mn][(4 * mg + i) * G::DT + dt]) =
+            f32x4{st.o[dt][i], st.o[dt + 1][i], st.o[dt + 2][i], st.o[dt + 3][i]};
+    __syncthreads();
+    // 8 elements of a row a thread
+    for (int e = mt; e < 16 * D / 8; e += 64 * NW) {
+      const int row = e / (D / 8), d = e % (D / 8) * 8;
+      if (row >= u.live) continue;
+      float top = mm[0][row];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) top = fmaxf(top, mm[w][row]);
+      float sum = 0.0f, o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = part_weight(mm[w][row], top);
+        sum = fmaf(ml[w][row], f, sum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(mo[w][row][d + k], f, o[k]);
+      }
+      if (u.whole) {
+        const float inv = row_factor(sum);
+        const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + row);
+        u32x4 w;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+        *reinterpret_cast<u32x4 *>(a.out + head * D + d) = w;
+        if (a.lse && d == 0) a.lse[head] = row_lse(top, sum);
+      } else {
+        using P = Part<D, ROWS>;
+        const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (t0 == 0 ? 1 : 0);
+        float *po = P::o(a.parts, slot) + row * D + d;
+        *reinterpret_cast<f32x4 *>(po) = f32x4{o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<f32x4 *>(po + 4) = f32x4{o[4], o[5], o[6], o[7]};
+        if (d == 0) {
+          P::m(a.parts, slot)[row] = top;
+          P::l(a.parts, slot)[row] = sum;
+        }
+      }
+    }
+    __syncthreads();
   }
   walk.finish();
   if (__builtin_expect(err != 0u, 0)) Status{a.status, true}.report(err);
@@ -765,7 +740,7 @@ struct StageAt {
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(AttnArgs a) {
   using G = PromptGeo<D>;
-  constexpr int TT = G::TT, NR = 1, W = 32 * NR, M = W * NW, THREADS = 64 * NW;
+  constexpr int TT = G::TT, M = 32 * NW, THREADS = 64 * NW;
   constexpr int PT = (G::ITEMS + THREADS - 1) / THREADS;  // staging items of a thread
   __shared__ __align__(16) uint8_t smem[3 * G::BUF];
   const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 31, hh = lane >> 5;
@@ -786,36 +761,33 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     // key tiles that the row tile's own rows see
     const int see_lo = attn_lo(a.sh, u.sq, u.i0) / TT, see_hi = (attn_hi(a.sh, u.sq, u.i1) + TT - 1) / TT;
     const int tb = uniform(max(u.lo + u.t0, see_lo)), te = uniform(min(u.lo + u.t1, see_hi));
-    const int w_rows = u.live - W * wave;  // of the wave: W or fewer, none where it is not positive
-    const int j0 = uniform((int)divide((uint32_t)(u.r0 + (w_rows > 0 ? W * wave : 0)), a.by_groups));
-    const int j1 = uniform((int)divide((uint32_t)(u.r0 + (w_rows > 0 ? W * wave + min(w_rows, W) - 1 : 0)), a.by_groups));
+    const int w_rows = u.live - 32 * wave;  // of the wave: 32 or fewer, none where it is not positive
+    const int j0 = uniform((int)divide((uint32_t)(u.r0 + (w_rows > 0 ? 32 * wave : 0)), a.by_groups));
+    const int j1 = uniform(
+        (int)divide((uint32_t)(u.r0 + (w_rows > 0 ? 32 * wave + min(w_rows, 32) - 1 : 0)), a.by_groups));
     const int all_lo = uniform(attn_lo(a.sh, u.sq, j1)), all_hi = uniform(attn_hi(a.sh, u.sq, j0));
 
-    u32x4 q[NR][G::HG * 4];
-    f32x16 o[NR][G::DT];
-    float m[NR], l[NR];
-    int lo[NR], hi[NR];
+    u32x4 q[G::HG * 4];
+    f32x16 o[G::DT];
+    float m, l;
+    const bool on = n < w_rows;
+    const int64_t row = u.r0 + (on ? 32 * wave + n : 0);
+    const int i = (int)divide((uint32_t)row, a.by_groups);
+    const int lo = attn_lo(a.sh, u.sq, i), hi = attn_hi(a.sh, u.sq, i);
+    const uint16_t *qp =
+        a.q + (u.sq.first + i) * a.q_st + (u.h * a.sh.groups + (row - (int64_t)i * a.sh.groups)) * a.q_sh;
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const bool on = 32 * r + n < w_rows;
-      const int64_t row = u.r0 + (on ? W * wave + 32 * r + n : 0);
-      const int i = (int)divide((uint32_t)row, a.by_groups);
-      lo[r] = attn_lo(a.sh, u.sq, i);
-      hi[r] = attn_hi(a.sh, u.sq, i);
-      const uint16_t *qp = a.q + (u.sq.first + i) * a.q_st + (u.h * a.sh.groups + (row - (int64_t)i * a.sh.groups)) * a.q_sh;
-#pragma unroll
-      for (int x = 0; x < G::HG * 4; ++x) {
-        q[r][x] = u32x4{0u, 0u, 0u, 0u};
-        if (on) q[r][x] = *reinterpret_cast<const u32x4 *>(qp + hh * (D / 2) + 8 * x);
-        q[r][x] ^= flip;
-      }
-#pragma unroll
-      for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[r][dt][x] = 0.0f;
-      m[r] = kNegInf;
-      l[r] = 0.0f;
+    for (int x = 0; x < G::HG * 4; ++x) {
+      q[x] = u32x4{0u, 0u, 0u, 0u};
+      if (on) q[x] = *reinterpret_cast<const u32x4 *>(qp + hh * (D / 2) + 8 * x);
+      q[x] ^= flip;
     }
+#pragma unroll
+    for (int dt = 0; dt < G::DT; ++dt)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[dt][x] = 0.0f;
+    m = kNegInf;
+    l = 0.0f;
 
     const int64_t head_off = u.h * a.head_stride;
     const int32_t *row_table = a.table + u.b * a.table_stride;
@@ -918,19 +890,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       }
     };
     // their scores
-    auto scores = [&](f32x16 (&s)[NR]) {
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) s[r][x] = 0.0f;
+    auto scores = [&](f32x16 &s) {
+      #pragma unroll
+        for (int x = 0; x < 16; ++x) s[x] = 0.0f;
 #pragma unroll
       for (int p = 0; p < G::HG; ++p)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const bf16x8 kv = fp4x8_to_bf16(kc[p][w], ks[p]);
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv, __builtin_bit_cast(bf16x8, q[r][4 * p + w]), s[r], 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kv, __builtin_bit_cast(bf16x8, q[4 * p + w]), s, 0, 0, 0);
         }
     };
     // value operands of 16 tokens of a tile
@@ -944,68 +912,48 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       }
     };
     // masks them and keeps the running maximum
-    auto settle = [&](int token0, uint32_t ok, f32x16 (&s)[NR]) {
+    auto settle = [&](int token0, uint32_t ok, f32x16 &s) {
       if (!(ok == 3u && token0 >= all_lo && token0 + 32 <= all_hi)) {
         not_speculated();
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int tok = token0 + 16 * (x / 8) + 8 * hh + x % 8;
-            s[r][x] = (tok >= lo[r]) & (tok < hi[r]) & ((ok >> (x / 8)) & 1u) ? s[r][x] : kNegInf;
-          }
+        for (int x = 0; x < 16; ++x) {
+          const int tok = token0 + 16 * (x / 8) + 8 * hh + x % 8;
+          s[x] = (tok >= lo) & (tok < hi) & ((ok >> (x / 8)) & 1u) ? s[x] : kNegInf;
+        }
       }
-      float mx[NR];
-      bool far = false;
+      float mx = s[0];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        mx[r] = s[r][0];
-#pragma unroll
-        for (int x = 1; x < 16; ++x) mx[r] = fmaxf(mx[r], s[r][x]);
-        far |= mx[r] > m[r] + slack;
-      }
+      for (int x = 1; x < 16; ++x) mx = fmaxf(mx, s[x]);
       // the running maximum moves only when a score passes it by more than 2^8 (see consume_tile)
-      if (__ballot(far)) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float top = fmaxf(m[r], fmaxf(mx[r], xor32(mx[r])));
-          const float shrink = m[r] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m[r] - top) * c);
-          m[r] = top;
-          l[r] *= shrink;
-#pragma unroll
-          for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[r][dt][x] *= shrink;
-        }
-      }
-    };
-    // their part of the output; the first 16 tokens' value operands are loaded
-    auto outputs = [&](const uint8_t *buf, int sub, f32x16 (&s)[NR]) {
-      float ref[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) ref[r] = m[r] == kNegInf ? 0.0f : m[r] * c;
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {  // 16 tokens each
-        bf16x8 pv[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          u32x4 pw;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            s[r][8 * st + x] = __builtin_amdgcn_exp2f(fmaf(s[r][8 * st + x], c, -ref[r]));
-            l[r] += s[r][8 * st + x];
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[r][8 * st + 2 * x], s[r][8 * st + 2 * x + 1]);
-          pv[r] = __builtin_bit_cast(bf16x8, pw);
-        }
-        if (st == 1) load_values(buf, 2 * sub + 1);
+      if (__ballot(mx > m + slack)) {
+        const float top = fmaxf(m, fmaxf(mx, xor32(mx)));
+        const float shrink = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((m - top) * c);
+        m = top;
+        l *= shrink;
 #pragma unroll
         for (int dt = 0; dt < G::DT; ++dt)
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-            o[r][dt] =
-                __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv[dt]), pv[r], o[r][dt], 0, 0, 0);
+          for (int x = 0; x < 16; ++x) o[dt][x] *= shrink;
+      }
+    };
+    // their part of the output; the first 16 tokens' value operands are loaded
+    auto outputs = [&](const uint8_t *buf, int sub, f32x16 &s) {
+      const float ref = m == kNegInf ? 0.0f : m * c;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {  // 16 tokens each
+        u32x4 pw;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          s[8 * st + x] = __builtin_amdgcn_exp2f(fmaf(s[8 * st + x], c, -ref));
+          l += s[8 * st + x];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pw[x] = pack_bf16(s[8 * st + 2 * x], s[8 * st + 2 * x + 1]);
+        const bf16x8 pv = __builtin_bit_cast(bf16x8, pw);
+        if (st == 1) load_values(buf, 2 * sub + 1);
+#pragma unroll
+        for (int dt = 0; dt < G::DT; ++dt)
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vv[dt]), pv, o[dt], 0, 0, 0);
       }
     };
 
@@ -1027,7 +975,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       store(tb, smem, ok_cur);
       if (tb + 1 < te) fetch_next(tb + 1);
       __syncthreads();
-      f32x16 s0[NR], s1[NR];
+      f32x16 s0, s1;
       load_keys(smem, 0);
       scores(s0);
       int at_cur = 0, at_nxt = G::BUF;
@@ -1053,38 +1001,34 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
       __syncthreads();  // the buffers are free for the next unit
     }
 
+    const float sum = l + xor32(l);
+    const float top = m == kNegInf ? kNegInf : m * c;
+    const int pr = 32 * wave + n;  // row of the tile
+    if (pr < u.live && u.whole) {
+      const float inv = row_factor(sum);
+      const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + pr);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float sum = l[r] + xor32(l[r]);
-      const float top = m[r] == kNegInf ? kNegInf : m[r] * c;
-      const int pr = W * wave + 32 * r + n;  // row of the tile
-      if (pr >= u.live) continue;
-      if (u.whole) {
-        const float inv = row_factor(sum);
-        const int64_t head = out_row(a, u.sq.first, u.h, u.r0 + pr);
+      for (int dt = 0; dt < G::DT; ++dt) {
+        u32x4 w[2];
 #pragma unroll
-        for (int dt = 0; dt < G::DT; ++dt) {
-          u32x4 w[2];
+        for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = pack_bf16(o[dt][2 * x] * inv, o[dt][2 * x + 1] * inv);
+        u32x4 *p = reinterpret_cast<u32x4 *>(a.out + head * D + dt * 32 + hh * 16);
+        p[0] = w[0];
+        p[1] = w[1];
+      }
+      if (a.lse && hh == 0) a.lse[head] = row_lse(top, sum);
+    } else if (pr < u.live) {
+      using P = Part<D, M>;
+      const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (u.t0 == 0 ? 1 : 0);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = pack_bf16(o[r][dt][2 * x] * inv, o[r][dt][2 * x + 1] * inv);
-          u32x4 *p = reinterpret_cast<u32x4 *>(a.out + head * D + dt * 32 + hh * 16);
-          p[0] = w[0];
-          p[1] = w[1];
-        }
-        if (a.lse && hh == 0) a.lse[head] = row_lse(top, sum);
-      } else {
-        using P = Part<D, M>;
-        const int64_t slot = 2 * (int64_t)(blockIdx.x - 1) + (u.t0 == 0 ? 1 : 0);
+      for (int dt = 0; dt < G::DT; ++dt)
 #pragma unroll
-        for (int dt = 0; dt < G::DT; ++dt)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<f32x4 *>(P::o(a.parts, slot) + pr * D + dt * 32 + hh * 16 + 4 * x) =
-                f32x4{o[r][dt][4 * x], o[r][dt][4 * x + 1], o[r][dt][4 * x + 2], o[r][dt][4 * x + 3]};
-        if (hh == 0) {
-          P::m(a.parts, slot)[pr] = top;
-          P::l(a.parts, slot)[pr] = sum;
-        }
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<f32x4 *>(P::o(a.parts, slot) + pr * D + dt * 32 + hh * 16 + 4 * x) =
+              f32x4{o[dt][4 * x], o[dt][4 * x + 1], o[dt][4 * x + 2], o[dt][4 * x + 3]};
+      if (hh == 0) {
+        P::m(a.parts, slot)[pr] = top;
+        P::l(a.parts, slot)[pr] = sum;
       }
     }
   }
@@ -1180,6 +1124,7 @@ __global__ __launch_bounds__(64) void attn_status_kernel(uint32_t *status) {
 
 // ------------------------------------------------------------ dispatch ----
 constexpr int kCus = 256;
+constexpr int64_t kMaxGroups = 1 << 22;  // with 512 threads each, half of what a launch may have
 
 struct Plan {
   int rows;       // of a row tile: 16 (attn_rows_kernel), 128 or 256 (attn_prompt_kernel)
@@ -1194,7 +1139,8 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
   const int64_t groups = q_heads / heads, seq_rows = max_new * groups;
   const int64_t keys = window && window + max_new < max_len ? window + max_new : max_len;  // of a row tile, at most
   auto units_of = [&](int64_t rows) {  // a sequence's rows fill its row tiles except the last one
-    const int64_t tiles = tokens * groups / rows + batch, most = batch * ((seq_rows + rows - 1) / rows);
+    const int64_t live = batch < tokens ? batch : tokens;  // sequences that have rows
+    const int64_t tiles = tokens * groups / rows + live, most = live * ((seq_rows + rows - 1) / rows);
     return (tiles < most ? tiles : most) * heads;
   };
   Plan p;
@@ -1213,7 +1159,9 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
   // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
   // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
   const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
-  const bool direct = tiles <= 34 || (p.units >= fit && (p.rows != 16 || tiles <= 66));
+  // More units than a launch may have workgroups are taken in spans too.
+  const bool direct =
+      p.units <= kMaxGroups && (tiles <= 34 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));
   p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
   // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
   // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26
@@ -1226,7 +1174,7 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
 bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_new,
               int64_t max_len) {
   return kv_head_dim_ok(head_dim) && heads >= 1 && heads * head_dim <= 65536 && q_heads >= heads &&
-         q_heads <= 65536 && q_heads % heads == 0 && tokens >= 0 && tokens < kKvMaxUnits / q_heads && batch >= 0 &&
+         q_heads <= 65536 && q_heads % heads == 0 && kv_size_ok(tokens, q_heads, head_dim) && batch >= 0 &&
          batch < ((int64_t)1 << 24) && max_new >= 0 && max_new <= tokens && max_len >= 0 &&
          max_len <= ((int64_t)1 << 30);
 }

@@ -34,7 +34,9 @@ struct HeadMap {
 };
 
 // n * stride for a non-negative 32-bit n: a product of 32 by 64 bits.
-__device__ __forceinline__ int64_t times(int n, int64_t stride) { return (int64_t)((uint64_t)(uint32_t)n * (uint64_t)stride); }
+__device__ __forceinline__ int64_t times(int n, int64_t stride) {
+  return (int64_t)((uint64_t)(uint32_t)n * (uint64_t)stride);
+}
 
 __device__ __forceinline__ void load8(const uint16_t *p, float z[8]) {
   const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
@@ -480,8 +482,8 @@ extern "C" fp4q_status_t fp4q_rotate_heads(const void *x, fp4q_dtype_t dtype, in
         // two units a thread for long float32 inputs: 268 MB in 49 us, 54 with one (bfloat16: 36 and 34)
         if constexpr (sizeof(T) == 4) {
           if (groups >= 4096) {
-            hipLaunchKernelGGL((rotate_heads_kernel<T, O, D, 2>), dim3((unsigned)((groups + 1) / 2)), dim3(kThreads), 0, s,
-                               (const T *)x, units, make_divider((uint32_t)heads), token_stride, head_stride, m,
+            hipLaunchKernelGGL((rotate_heads_kernel<T, O, D, 2>), dim3((unsigned)((groups + 1) / 2)), dim3(kThreads), 0,
+                               s, (const T *)x, units, make_divider((uint32_t)heads), token_stride, head_stride, m,
                                (O *)out, status);
             return;
           }
@@ -517,8 +519,8 @@ extern "C" fp4q_status_t fp4q_kv_append_mxfp4(const fp4q_kv_cache_t *cache, cons
     return hip_status();
   }
   const AppendArgs a{{k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, slots,
-                     (int)(tokens * cache->heads), make_divider((uint32_t)cache->heads), head_map(*map), off_lo, off_hi, view(*cache),
-                     status};
+                     (int)(tokens * cache->heads), make_divider((uint32_t)cache->heads), head_map(*map), off_lo,
+                     off_hi, view(*cache), status};
   with_dim(cache->head_dim, [&](auto dc) {
     constexpr int D = decltype(dc)::value;
     constexpr int U = kThreads / (D / kChunk);
@@ -539,7 +541,7 @@ extern "C" fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const 
   if (out_dtype != FP4Q_F32 && out_dtype != FP4Q_BF16) return FP4Q_ERR_ARG;
   fp4q_status_t st = kv_check_cache(*cache);
   if (st != FP4Q_OK) return st;
-  if (tokens < 0 || tokens * cache->heads >= kKvMaxUnits) return FP4Q_ERR_SHAPE;
+  if (!kv_size_ok(tokens, cache->heads, cache->head_dim)) return FP4Q_ERR_SHAPE;
   if (tokens && (!kv_aligned(slots, 8) || !kv_aligned(k_out, 16) || !kv_aligned(v_out, 16))) return FP4Q_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
   uint32_t *status = (uint32_t *)((char *)workspace + kWsStatus);
@@ -556,7 +558,7 @@ extern "C" fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const 
     with_type(out_dtype, [&](auto op) {
       using O = std::remove_pointer_t<decltype(op)>;
       hipLaunchKernelGGL((kv_read_kernel<O, D>), grid, dim3(kThreads), 0, s, c, slots, units,
-                         make_divider((uint32_t)cache->heads),                         (O *)k_out, (O *)v_out, status);
+                         make_divider((uint32_t)cache->heads), (O *)k_out, (O *)v_out, status);
     });
   });
   return hip_status();

@@ -17,7 +17,6 @@
 
 namespace fp4q {
 
-constexpr int64_t kKvMaxUnits = (int64_t)1 << 30;  // (token, head) pairs of a call
 
 inline bool kv_aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -29,12 +28,18 @@ inline int kv_log2(int64_t n) {
 
 inline bool kv_head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
+// Elements of a tensor of heads: below 2^33, so that a grid of one thread for
+// every 8 of them has fewer than the 2^32 threads that a launch may have.
+inline bool kv_size_ok(int64_t tokens, int64_t heads, int64_t head_dim) {
+  return tokens >= 0 && (heads == 0 || tokens < ((int64_t)1 << 33) / (heads * head_dim));
+}
+
 inline fp4q_status_t kv_check_heads(fp4q_dtype_t dtype, int64_t tokens, int64_t heads, int64_t head_dim,
                                     int64_t token_stride, int64_t head_stride, const void *x) {
   if (dtype != FP4Q_F32 && dtype != FP4Q_BF16) return FP4Q_ERR_ARG;
   if (tokens < 0 || heads < 0 || heads > 65536 || !kv_head_dim_ok(head_dim)) return FP4Q_ERR_SHAPE;
   if (tokens == 0 || heads == 0) return FP4Q_OK;
-  if (tokens >= kKvMaxUnits || tokens * heads >= kKvMaxUnits) return FP4Q_ERR_SHAPE;
+  if (!kv_size_ok(tokens, heads, head_dim)) return FP4Q_ERR_SHAPE;
   const int64_t limit = (int64_t)1 << 40;  // so that no byte offset passes 63 bits
   if (token_stride < 0 || head_stride < 0 || token_stride > limit || head_stride > limit) return FP4Q_ERR_SHAPE;
   const int64_t size = dtype == FP4Q_BF16 ? 2 : 4;

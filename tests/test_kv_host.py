@@ -80,6 +80,32 @@ def test_map_refusals(m, want):
     assert _rotate(L, lib, m=m) == getattr(L, want)
 
 
+@pytest.mark.parametrize("dim,most", [(64, 1 << 21), (128, 1 << 20), (256, 1 << 19)])
+def test_sizes_that_a_launch_could_not_cover_are_refused(dim, most):
+    """2^33 elements and more, among them counts whose product passes 64 bits."""
+    L, lib = _lib()
+    c = _cache(L, heads=64, dim=dim, ps=dim // 2 * 64 * 64, hs=dim // 2 * 64, ts=dim // 2)
+    wsb, st = lib.fp4q_workspace_bytes(), 64 * dim
+    for tokens in (most, 1 << 30, 1 << 40, (1 << 58) + 1, (1 << 62) + 1):
+        assert _rotate(L, lib, tokens=tokens, heads=64, dim=dim, st=st, sh=dim) == L.ERR_SHAPE
+        assert lib.fp4q_kv_append_mxfp4(ctypes.byref(c), X, st, dim, X, st, dim, L.BF16, tokens, IDX,
+                                        ctypes.byref(_map(L, rot=64)), -1, 0, WS, wsb, None) == L.ERR_SHAPE
+        assert lib.fp4q_kv_read_mxfp4(ctypes.byref(c), IDX, tokens, L.BF16, OUT, OUT, WS, wsb, None) == L.ERR_SHAPE
+        assert lib.fp4q_attention_mxfp4_workspace_bytes(tokens, 1, 64, 64, dim, 1, 64, 0) == 0
+    assert lib.fp4q_attention_mxfp4_workspace_bytes(most - 1, 1, 64, 64, dim, 1, 64, 0) > 0
+
+
+def test_more_units_than_a_launch_has_workgroups_are_split():
+    """2^21 sequences of one token and 32 heads: a workgroup a unit would be 2^26 of them."""
+    L, lib = _lib()
+    f = lib.fp4q_attention_mxfp4_workspace_bytes
+    one = f(1 << 17, 1 << 17, 32, 32, 64, 1, 64, 0)
+    many = f(1 << 21, 1 << 21, 32, 32, 64, 1, 64, 0)
+    assert one == 256 < many < 1 << 23
+    # sequences without tokens have no units
+    assert f(4, 1 << 23, 8, 8, 64, 1, 64, 0) == 256
+
+
 def test_map_hadamard_wider_than_the_head():
     L, lib = _lib()
     assert _rotate(L, lib, m=dict(rot=64, had=128), dim=64, st=128, sh=64) == L.ERR_SHAPE

@@ -65,8 +65,8 @@ __device__ __forceinline__ void store8(uint16_t *p, const float z[8]) {  // to n
 }
 __device__ __forceinline__ void store8(float *p, const float z[8]) {
   f32x4 *q = reinterpret_cast<f32x4 *>(p);
-  __builtin_nontemporal_store(f32x4{z[0], z[1], z[2], z[3]}, q);
-  __builtin_nontemporal_store(f32x4{z[4], z[5], z[6], z[7]}, q + 1);
+  q[0] = f32x4{z[0], z[1], z[2], z[3]};
+  q[1] = f32x4{z[4], z[5], z[6], z[7]};
 }
 
 // Value of lane l ^ M of the wave, M a power of two up to 16.
@@ -288,15 +288,22 @@ __device__ __forceinline__ uint32_t quantize_quad(const float z[8], int lo, int 
   finite = a < 0x7F800000u;
   const int eb = mx_base_exponent(as_f(a));
   E = max(-127, eb + lo);
+  auto codes_at = [&](int e) {
+    const float down = pow2f(-e);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = z[i] * down;
+    return cvt_fp4x8(y);
+  };
+  uint32_t codes = codes_at(E);
   if (lo < hi) {
     float best = __builtin_inff();
     const int top = min(127, eb + hi);
-    for (int e = E; e <= top; ++e) {
-      const float down = pow2f(-e), V = pow2f(e);
-      float y[8], q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = z[i] * down;
-      fp4x8_to_f32(cvt_fp4x8(y), q);
+    uint32_t w = codes;
+    for (int e = E;;) {
+      const float V = pow2f(e);
+      float q[8];
+      fp4x8_to_f32(w, q);
       float L = quad_bcast<0>(chain8(z, q, V, 0.0f));
       L = quad_bcast<1>(chain8(z, q, V, L));
       L = quad_bcast<2>(chain8(z, q, V, L));
@@ -304,14 +311,13 @@ __device__ __forceinline__ uint32_t quantize_quad(const float z[8], int lo, int 
       if (L < best) {
         best = L;
         E = e;
+        codes = w;
       }
+      if (++e > top) break;
+      w = codes_at(e);
     }
   }
-  const float down = pow2f(-E);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = z[i] * down;
-  return cvt_fp4x8(y);
+  return codes;
 }
 
 struct AppendArgs {

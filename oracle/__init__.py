@@ -21,7 +21,8 @@ Modules: ``formats`` (E2M1 / E4M3 / E8M0 and rounding), ``quant`` (NVFP4
 ScaleSweep, MXFP4 exponent sweep, dequantization), ``hadamard`` (block
 rotation), ``study`` (float64 exhaustive sweeps that pin the lemmas),
 ``focus`` (FOCUS forward quantizer), ``gptq`` (GPTQ with sweep-chosen group
-scales), ``gemm`` (W4A4 products in float64).  Import them directly.
+scales), ``gemm`` (W4A4 products in float64), ``kv`` (key/value cache: rotation,
+append, read, attention in float64).  Import them directly.
 
 Parity-unpinned (no value on the pages fixes them): the FP32 evaluation
 order of the per-candidate loss and the reciprocal-multiply form

@@ -741,7 +741,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
 // at a clock that the load lowers to 1.7 - 2.1 GHz.  Measured and not kept:
 // 64 rows for each wave (620 us against 505: one wave on a SIMD), a fixed
 // interleaving of the two pipes' instructions (4% slower), wave priorities
-// (slower).
+// (slower), a SIMD's two waves held in opposite phases, vector work of one
+// beside matrix work of the other, by four barriers a tile (525 us against
+// 418), values staged by all eight waves in pieces of half the size (461).
 template <int D>
 struct PromptGeo {
   static constexpr int TT = 64;

@@ -204,6 +204,7 @@ struct Geo {
   static constexpr int DT = D / 16;              // output tiles; lane c of 16 owns elements c DT .. c DT + DT - 1
   static constexpr int TT = 32;                  // tokens of a key tile
   static constexpr int TG = TT / 16;
+  static constexpr int VS = D == 256 ? 4 : 1;    // value scales of 16 tokens that a lane loads
   using KT = std::conditional_t<D == 64, u32x2, u32x4>;
   using VT = std::conditional_t<D == 64, uint16_t, std::conditional_t<D == 128, uint32_t, u32x2>>;
   // first element of lane group g's 8 in step (p, w) of a score: any order of the row will do, as long as queries
@@ -218,14 +219,18 @@ struct KvTile {
   typename G::KT k[G::TG][G::KP];
   uint32_t ks[G::TG][G::KP];
   typename G::VT v[G::TG][4];
-  uint32_t vs[G::TG][4];
+  uint32_t vs[G::TG][G::VS];
 };
 
 // Offsets of a lane within the 16 tokens of a group (bytes of codes).  Keys:
 // lane (m = lane % 16, g = lane / 16) takes part g of token (m % 4) 4 + m / 4,
 // so that register i of the score tile is token 4 i + g.  Values: lane
 // (c, g) takes the elements it owns of token 4 j + g in load j: a wave's load
-// covers 4 whole rows.
+// covers 4 whole rows.  Up to heads of 128 a lane's values are of the same
+// block as its quad's, so it loads the scale of token 4 (m % 4) + g and takes
+// the others from its neighbours (value_scale): 2 loads in place of 8 of a
+// tile's 20.  131072 keys 35.7 -> 34.8 us, 128 sequences of up to 1000 30.0 ->
+// 29.2; for heads of 256, by pairs, it was slower (19.8 -> 20.5).
 template <int D>
 struct LaneAt {
   uint32_t k, ks, v, vs;
@@ -235,9 +240,16 @@ struct LaneAt {
     k = kt * ts + g * 4 * Geo<D>::KW;
     ks = kt * (ts / 16) + (D == 64 ? g / 2 : g);
     v = g * ts + m * (D / 32);
-    vs = g * (ts / 16) + m * Geo<D>::DT / 32;
+    vs = (D == 256 ? g : 4 * (m & 3) + g) * (ts / 16) + m * Geo<D>::DT / 32;
   }
 };
+
+// The scale of the lane's values of token 4 j + g, in a float32's exponent bits.
+template <int D, int J>
+__device__ __forceinline__ float value_scale(const uint32_t (&vs)[Geo<D>::VS]) {
+  if constexpr (D == 256) return as_f(vs[J] << 23);
+  else return as_f((uint32_t)__builtin_amdgcn_mov_dpp((int)(vs[0] << 23), J * 0x55, 0xF, 0xF, true));  // quad_perm
+}
 
 // off[tg]: byte offset of the first code row of the tile's 16-token group tg.
 template <int D>
@@ -259,8 +271,9 @@ __device__ __forceinline__ void load_tile(const AttnArgs &a, const LaneAt<D> &at
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       t.v[tg][j] = *reinterpret_cast<const typename G::VT *>(vc + (v_at + j * v_step));
-      t.vs[tg][j] = vs[vs_at + j * vs_step];
     }
+#pragma unroll
+    for (int y = 0; y < G::VS; ++y) t.vs[tg][y] = vs[vs_at + y * vs_step];
   }
 }
 
@@ -387,7 +400,14 @@ __device__ __forceinline__ void consume_tile(const AttnArgs &a, const KvTile<D> 
     for (int j = 0; j < 8; ++j) {
       const int tg = 2 * h + j / 4;
       v[j] = t.v[tg][j & 3];
-      vs[j] = as_f(t.vs[tg][j & 3] << 23);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t(&b)[G::VS] = t.vs[2 * h + k];
+      vs[4 * k] = value_scale<D, 0>(b);
+      vs[4 * k + 1] = value_scale<D, 1>(b);
+      vs[4 * k + 2] = value_scale<D, 2>(b);
+      vs[4 * k + 3] = value_scale<D, 3>(b);
     }
     if (!full) {  // what lies outside every row's keys must not reach a product, where 0 * NaN is NaN
       not_speculated();
@@ -571,8 +591,11 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_tab
 // Bound by the cache's bytes: 64 sequences of 0 to 8192 tokens (64 query
 // heads on 8, 128 wide; 292 MB) 61 us, 4.8 TB/s; 131072 tokens of one
 // sequence (32 on 8, 143 MB) 31 us, 4.6 TB/s, and 5 us for the join.  HBM
-// traffic is 1.00 of the bytes.  4096 tokens of it 17 us with the join, 1000
-// tokens 12: nothing but the chain of loads and the launch.
+// traffic is 1.00 of the bytes.  Short ones are bound by latency: 100 tokens
+// take 6 us (launch, length, page, codes, merge), and each further tile of a
+// wave 0.8 us, with one wave on a SIMD: 1024 tokens 12.5 us.  A third register
+// set, two tiles ahead, was no faster, so it is the tile's own chain (decode,
+// scores, maximum, exponentials, decode, outputs).
 // Measured and not kept: tiles of 64 tokens (short units wait longer for their
 // first), eight waves (0.5 us less for one short sequence, more for the rest),
 // 32 rows for each wave (the registers leave one wave on a SIMD), codes to LDS

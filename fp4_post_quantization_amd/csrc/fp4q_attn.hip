@@ -590,7 +590,7 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_tab
 // rows for each 16 lanes), the next tile's while it computes this one's.
 // Bound by the cache's bytes: 64 sequences of 0 to 8192 tokens (64 query
 // heads on 8, 128 wide; 292 MB) 61 us, 4.8 TB/s; 131072 tokens of one
-// sequence (32 on 8, 143 MB) 31 us, 4.6 TB/s, and 5 us for the join.  HBM
+// sequence (32 on 8, 143 MB) 30 us, 4.7 TB/s, and 5 us for the join.  HBM
 // traffic is 1.00 of the bytes.  Short ones are bound by latency: 100 tokens
 // take 6 us (launch, length, page, codes, merge), and each further tile of a
 // wave 0.8 us, with one wave on a SIMD: 1024 tokens 12.5 us.  A third register
@@ -758,8 +758,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
 // 16-byte pieces of both are swizzled so that 16 lanes that read or write
 // together fall on different banks.
 // 2048 new tokens on 8192 keys (64 query heads on 8, 128 wide; 412 GFLOP)
-// take 390 us, 1.05 PFLOP/s, 76% of what a large bfloat16 matrix product of
-// the vendor's library reaches on the same card (1.38).  The vector pipe (key
+// take 390 to 430 us, as the clock allows: 0.96 to 1.05 PFLOP/s, 69 to 76% of
+// what a large bfloat16 matrix product of the vendor's library reaches (1.38).  The vector pipe (key
 // decoding, exponentials) is busy 70% of the cycles and the matrix cores 48%,
 // at a clock that the load lowers to 1.7 - 2.1 GHz.  Measured and not kept:
 // 64 rows for each wave (620 us against 505: one wave on a SIMD), a fixed

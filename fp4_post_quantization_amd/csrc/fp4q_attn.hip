@@ -495,7 +495,16 @@ struct Walk {
       end = index < spans ? attn_cut(total, spans, pos + 1) : 0;
       pos = index < spans ? attn_cut(total, spans, pos) : 0;
     }
-    if (pos < end && !scan.find(pos, b, off)) end = pos;
+    if (!a.spans && !a.cu) {
+      // One row each: all sequences have the same units, and no workgroup scans a large batch for its own (4096
+      // sequences of up to 200 keys 437 -> 161 us, 256 of up to 100 11.9 -> 11).
+      const uint32_t per = (uint32_t)((a.sh.groups + ROWS - 1) / ROWS) * (uint32_t)a.sh.heads;
+      b = (int)((uint32_t)pos / per);
+      off = pos - (int64_t)b * per;
+      if (b >= a.sh.batch) end = pos;
+    } else if (pos < end && !scan.find(pos, b, off)) {
+      end = pos;
+    }
     b = uniform(b);
     off = uniform64(off);
   }

@@ -337,6 +337,14 @@ def test_attention_many_sequences():
     _run(_fq(), rng, lens, [1] * 131, 4, 2, 64, 16, rows=None)
 
 
+@pytest.mark.parametrize("cu", [False, True])
+def test_attention_many_short_sequences_of_two_row_tiles(cu):
+    """More sequences than a wave has lanes, 20 query heads on one, a workgroup for each unit."""
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 60, 150).tolist()
+    _run(_fq(), rng, lens, [1] * 150, 40, 2, 64, 16, cu=cu)
+
+
 def test_attention_large_and_small_scores():
     """Scores far apart (one key takes everything), and a scale of zero and a negative one."""
     fq = _fq()

@@ -1242,8 +1242,9 @@ Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, in
   // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
   const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
   // More units than a launch may have workgroups are taken in spans too.
+  // No units (max_new 0): nothing to split, and a second kernel without rows would be no launch at all.
   const bool direct =
-      p.units <= kMaxGroups && (tiles <= 34 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));
+      p.units <= kMaxGroups && (tiles <= 34 || p.units == 0 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));
   p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
   // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
   // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26

@@ -483,6 +483,24 @@ def test_attention_without_keys_or_table():
                            check=True)
 
 
+def test_attention_without_new_tokens_on_a_long_cache():
+    """max_new 0 with a table long enough to be split: no row belongs to a sequence, out is left as it is, and an
+    offset that gives one a row is reported."""
+    fq = _fq()
+    cache = fq.kv_cache_mxfp4(64, 2, 64, 64, DEV)
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    table = torch.arange(64, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([4096], dtype=torch.int32, device=DEV)
+    out = torch.full((3, 4, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    fq.attention_mxfp4(q, cache, table, lens, none, max_new=0, out=out, check=True)
+    assert bool((out == 5).all())
+    with pytest.raises(fq.FP4QError, match="row offset"):
+        fq.attention_mxfp4(q, cache, table, lens, none + torch.tensor([0, 2], dtype=torch.int32, device=DEV),
+                           max_new=0, out=out, check=True)
+    assert bool((out == 5).all())
+
+
 def test_attention_bad_pages_in_every_kernel():
     """A page number out of range masks its tokens and is reported, whichever kernel the sizes choose; sequences
     beside it are as they would be."""

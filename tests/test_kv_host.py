@@ -106,6 +106,14 @@ def test_more_units_than_a_launch_has_workgroups_are_split():
     assert f(4, 1 << 23, 8, 8, 64, 1, 64, 0) == 256
 
 
+def test_calls_without_new_tokens_are_not_split():
+    """max_new 0 on a long cache has no units, so no partial results and no second kernel, which would have a grid
+    without workgroups."""
+    L, lib = _lib()
+    for dim in (64, 128, 256):
+        assert lib.fp4q_attention_mxfp4_workspace_bytes(5, 3, 32, 8, dim, 0, 100000, 0) == 256
+
+
 def test_map_hadamard_wider_than_the_head():
     L, lib = _lib()
     assert _rotate(L, lib, m=dict(rot=64, had=128), dim=64, st=128, sh=64) == L.ERR_SHAPE

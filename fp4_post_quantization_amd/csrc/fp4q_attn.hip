@@ -1308,6 +1308,8 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
       max_len > table_width * cache->page_size || (!cu_q && !empty && tokens != batch))
     return FP4Q_ERR_SHAPE;
   if (!cu_q && !empty && max_new < 1) return FP4Q_ERR_SHAPE;
+  // the table's last entry, below 2^60: no byte offset passes 63 bits
+  if (!empty && (__int128)table_stride * (batch - 1) + table_width >= ((__int128)1 << 60)) return FP4Q_ERR_SHAPE;
   if ((causal != 0 && causal != 1) || window < 0 || window > 0x7FFFFFFF || !(scale >= -3e38f && scale <= 3e38f))
     return FP4Q_ERR_ARG;
   if ((st = kv_check_heads(FP4Q_BF16, tokens, q_heads, cache->head_dim, q_token_stride, q_head_stride, q)) != FP4Q_OK)

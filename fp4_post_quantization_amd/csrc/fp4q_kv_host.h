@@ -40,10 +40,12 @@ inline fp4q_status_t kv_check_heads(fp4q_dtype_t dtype, int64_t tokens, int64_t 
   if (tokens < 0 || heads < 0 || heads > 65536 || !kv_head_dim_ok(head_dim)) return FP4Q_ERR_SHAPE;
   if (tokens == 0 || heads == 0) return FP4Q_OK;
   if (!kv_size_ok(tokens, heads, head_dim)) return FP4Q_ERR_SHAPE;
-  const int64_t limit = (int64_t)1 << 40;  // so that no byte offset passes 63 bits
-  if (token_stride < 0 || head_stride < 0 || token_stride > limit || head_stride > limit) return FP4Q_ERR_SHAPE;
-  const int64_t size = dtype == FP4Q_BF16 ? 2 : 4;
-  if (!kv_aligned(x, 16) || token_stride * size % 16 || head_stride * size % 16) return FP4Q_ERR_ALIGN;
+  // the last element, below 2^60: no byte offset passes 63 bits
+  if (token_stride < 0 || head_stride < 0 ||
+      (__int128)token_stride * (tokens - 1) + (__int128)head_stride * (heads - 1) >= ((__int128)1 << 60) - head_dim)
+    return FP4Q_ERR_SHAPE;
+  const int64_t chunk = dtype == FP4Q_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (!kv_aligned(x, 16) || token_stride % chunk || head_stride % chunk) return FP4Q_ERR_ALIGN;
   return FP4Q_OK;
 }
 

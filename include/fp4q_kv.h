@@ -12,8 +12,9 @@
  * Conventions of every call, beyond those of fp4q.h
  *   - Tensors of heads are [tokens][heads][head_dim] with a dense last axis
  *     and given strides (elements) of the other two; head_dim is 64, 128 or
- *     256, and a tensor has fewer than 2^33 elements.  Pointers are 16-byte
- *     aligned and the strides, in bytes, multiples of 16.
+ *     256, and a tensor has fewer than 2^33 elements, the last of them less
+ *     than 2^60 elements from the first.  Pointers are 16-byte aligned and
+ *     the strides, in bytes, multiples of 16.
  *   - The cache is described by fp4q_kv_cache_t (host memory, read during the
  *     call).  A slot number s names row s % page_size of page s / page_size.
  *   - Data errors set bits of the status word at byte 0 of the workspace, as

@@ -114,6 +114,20 @@ def test_calls_without_new_tokens_are_not_split():
         assert lib.fp4q_attention_mxfp4_workspace_bytes(5, 3, 32, 8, dim, 0, 100000, 0) == 256
 
 
+@pytest.mark.parametrize("tokens,heads,st,sh", [
+    (1 << 26, 1, 1 << 40, 64), (1 << 26, 1, 1 << 36, 64), (2, 1, 1 << 61, 64), (1, 1 << 16, 64, 1 << 46),
+    (1 << 13, 1 << 13, 1 << 47, 1 << 47), (3, 2, (1 << 63) - 16, 64),
+])
+def test_strides_whose_offsets_pass_63_bits_are_refused(tokens, heads, st, sh):
+    """The last element's byte offset is checked as a whole, not stride by stride."""
+    L, lib = _lib()
+    for dtype in (L.BF16, L.F32):
+        assert _rotate(L, lib, m=dict(rot=64), tokens=tokens, heads=heads, dim=64, st=st, sh=sh,
+                       dtype=dtype) == L.ERR_SHAPE
+    assert _attend(L, lib, tst=1 << 61) == L.ERR_SHAPE
+    assert _attend(L, lib, tokens=1 << 20, batch=1 << 20, tst=1 << 41) == L.ERR_SHAPE
+
+
 def test_map_hadamard_wider_than_the_head():
     L, lib = _lib()
     assert _rotate(L, lib, m=dict(rot=64, had=128), dim=64, st=128, sh=64) == L.ERR_SHAPE

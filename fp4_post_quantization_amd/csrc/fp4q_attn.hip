@@ -827,9 +827,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
   const int lane = threadIdx.x & 63, wave = wave_index(), n = lane & 31, hh = lane >> 5;
   if (is_status_group(a, lane, wave)) return;
   uint32_t err = 0u;
-  const float c = fmaxf(fabsf(a.scale_log2), 1e-30f);  // the sign of the scale goes into the queries
+  // the sign of the scale goes into the queries; never zero, since a masked score times zero would be NaN: the least
+  // float32 moves no finite score by 2^-20
+  const float c = fmaxf(fabsf(a.scale_log2), as_f(1u));
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-  const float slack = 8.0f / c;
+  const float slack = 8.0f / fmaxf(c, 1e-30f);  // finite; a tiny scale moves the maximum at less than 2^8
   // the lane's places in a buffer
   const int kt = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
   const int vd = 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3);
@@ -1310,7 +1312,7 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   if (!cu_q && !empty && max_new < 1) return FP4Q_ERR_SHAPE;
   // the table's last entry, below 2^60: no byte offset passes 63 bits
   if (!empty && (__int128)table_stride * (batch - 1) + table_width >= ((__int128)1 << 60)) return FP4Q_ERR_SHAPE;
-  if ((causal != 0 && causal != 1) || window < 0 || window > 0x7FFFFFFF || !(scale >= -3e38f && scale <= 3e38f))
+  if ((causal != 0 && causal != 1) || window < 0 || window > 0x7FFFFFFF || !(fabsf(scale) <= 0x1p127f))
     return FP4Q_ERR_ARG;
   if ((st = kv_check_heads(FP4Q_BF16, tokens, q_heads, cache->head_dim, q_token_stride, q_head_stride, q)) != FP4Q_OK)
     return st;

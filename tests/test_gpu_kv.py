@@ -353,6 +353,16 @@ def test_attention_large_and_small_scores():
         _run(fq, rng, [500, 33, 2000], [1, 1, 1], 8, 2, 128, 32, q_gain=gain, scale=scale)
 
 
+@pytest.mark.parametrize("gain,scale", [(1e33, 1e-34), (1e36, -1e-37), (1e30, 0.0), (1.0, 1e-40), (1e-36, 1e35)])
+@pytest.mark.parametrize("dim,new", [(64, 300), (128, 300), (256, 300), (128, 1)])
+def test_attention_scales_far_from_one(dim, new, gain, scale):
+    """Scores near one from huge queries and a tiny scale or the reverse, and a scale of zero: in one-row tiles and
+    in a prompt's (300 rows a head of 8 query heads: 152 row tiles of 128)."""
+    rng = np.random.default_rng(dim + new)
+    rows = np.array([0, 1, 31, 32, 150, 299])
+    _run(_fq(), rng, [max(new, 40)], [new], 64, 8, dim, 16, cu=True, q_gain=gain, scale=scale, rows=rows)
+
+
 def test_attention_ignores_what_no_row_sees():
     """NaN scales and every byte value behind the last key, before the window and in other pages."""
     fq = _fq()

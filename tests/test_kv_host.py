@@ -199,6 +199,13 @@ def test_attention_refusals(kw, want):
     assert _attend(L, lib, **kw) == getattr(L, want)
 
 
+@pytest.mark.parametrize("scale", [1.8e38, -1.8e38, 2.5e38, 3e38])
+def test_scales_that_overflow_in_units_of_log_2_are_refused(scale):
+    """scale * log2(e) has to be a finite float32: 2^127 and less in magnitude are."""
+    L, lib = _lib()
+    assert _attend(L, lib, scale=scale) == L.ERR_ARG
+
+
 def test_attention_workspace_of_invalid_sizes_is_zero():
     L, lib = _lib()
     f = lib.fp4q_attention_mxfp4_workspace_bytes

@@ -1207,55 +1207,6 @@ __global__ __launch_bounds__(64) void attn_status_kernel(uint32_t *status) {
 }
 
 // ------------------------------------------------------------ dispatch ----
-constexpr int kCus = 256;
-constexpr int64_t kMaxGroups = 1 << 22;  // with 512 threads each, half of what a launch may have
-
-struct Plan {
-  int rows;       // of a row tile: 16 (attn_rows_kernel), 128 or 256 (attn_prompt_kernel)
-  int waves;      // of attn_rows_kernel
-  int64_t units;  // upper bound of (sequence, row tile, head) units
-  int spans;
-  int64_t part_floats;
-};
-
-Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_new,
-               int64_t max_len, int64_t window) {
-  const int64_t groups = q_heads / heads, seq_rows = max_new * groups;
-  const int64_t keys = window && window + max_new < max_len ? window + max_new : max_len;  // of a row tile, at most
-  auto units_of = [&](int64_t rows) {  // a sequence's rows fill its row tiles except the last one
-    const int64_t live = batch < tokens ? batch : tokens;  // sequences that have rows
-    const int64_t tiles = tokens * groups / rows + live, most = live * ((seq_rows + rows - 1) / rows);
-    return (tiles < most ? tiles : most) * heads;
-  };
-  Plan p;
-  // A row tile of 128 costs a fifth of eight of 16 for each key, but it has to be filled, and there have to be
-  // enough of them for half the CUs, or keys enough to be split.  Measured (32 heads on 8, 128 wide; one sequence
-  // unless said): 80 rows a head on 8192 keys, two sequences: 37 us with 16, 52 with 128; 512 rows on 16384 keys
-  // 103 and 85; 2048 rows on 512 keys 34 (with 32) and 25; five sequences of up to 951 rows behind a window of 1000
-  // (12 heads on 4 of 64) 20 and 37.  256 rows share the staging of a key tile among twice the waves where there
-  // are still two workgroups for each CU: 16384 rows a head on 8192 keys 505 us with 128, 470 with 256; 8192 rows on
-  // 2048 keys 65 and 71.
-  p.rows = 16;
-  if (seq_rows > 96 && (units_of(128) >= kCus / 2 || keys > 4096))
-    p.rows = head_dim != 256 && units_of(256) >= 2 * kCus ? 256 : 128;
-  p.units = units_of(p.rows);
-  const int64_t fit = kCus * (head_dim == 256 || p.rows == 256 ? 1 : 2);  // workgroups on the chip at once
-  // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
-  // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
-  const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
-  // More units than a launch may have workgroups are taken in spans too.
-  // No units (max_new 0): nothing to split, and a second kernel without rows would be no launch at all.
-  const bool direct =
-      p.units <= kMaxGroups && (tiles <= 34 || p.units == 0 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));
-  p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
-  // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
-  // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26
-  // with four; 200 of up to 500, 25 and 32; 128 of up to 1000, 34 and 29.
-  p.waves = direct && p.units > 512 && tiles <= 18 ? 1 : 4;
-  p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * p.rows * (head_dim + 2);
-  return p;
-}
-
 bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_new,
               int64_t max_len) {
   return kv_head_dim_ok(head_dim) && heads >= 1 && heads * head_dim <= 65536 && q_heads >= heads &&

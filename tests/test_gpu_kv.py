@@ -432,6 +432,17 @@ def test_attention_leaves_other_rows_alone():
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kw", [{}, dict(max_new=200)])
+def test_attention_chunk_beside_decoding_sequences(dim, kw):
+    """Tokens of one prompt and single tokens in one call, with and without a bound on a sequence's rows: 52 and 600
+    rows a sequence and head on average, which tiles of 16 and of 128 rows take."""
+    rows = np.array([0, 1, 15, 63, 99, 127, 128, 199])
+    lens = [40, 5000, 700, 1, 320, 16, 17, 999]
+    _run(_fq(), np.random.default_rng(dim), lens, [1, 1, 100, 1, 0, 1, 1, 1], 8, 2, dim, 64, rows=rows)
+    _run(_fq(), np.random.default_rng(dim), lens[:3], [1, 1, 199], 36, 4, dim, 64, rows=rows, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("lens,news", [([700, 90], [1, 1]), ([9000], [1]), ([300, 5], [3, 2])])
 def test_attention_many_query_heads_on_one(dim, lens, news):
     """128 query heads on one cache head: many rows for few tokens."""

@@ -1240,7 +1240,7 @@ using namespace fp4q;
 extern "C" size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads,
                                                        int64_t head_dim, int64_t max_new, int64_t max_len,
                                                        int64_t window) {
-  if (window < 0 || !sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
+  if (window < 0 || window > 0x7FFFFFFF || !sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
   const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len, window);
   return kAttnHeader + p.spans * sizeof(Join) + 4 * (size_t)p.part_floats;
 }

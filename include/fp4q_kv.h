@@ -150,8 +150,8 @@ fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *sl
  *            (max_len at most table_width * page_size and 2^30).
  *   causal   1: row i of n sees the keys up to its own position, seq_len - n
  *            + i; 0: every key.
- *   window   0: no limit; w > 0: no row sees keys at its position minus w or
- *            before.
+ *   window   0: no limit; w > 0 (below 2^31): no row sees keys at its
+ *            position minus w or before.
  *   scale    factor of the scores (float32), at most 2^127 in magnitude.
  *   out      [tokens][q_heads][head_dim] bfloat16, dense, 16-byte aligned;
  *            it must not overlap the inputs.

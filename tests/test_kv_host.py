@@ -106,6 +106,16 @@ def test_more_units_than_a_launch_has_workgroups_are_split():
     assert f(4, 1 << 23, 8, 8, 64, 1, 64, 0) == 256
 
 
+def test_workspace_of_windows_that_a_call_refuses_is_zero():
+    """From 2^31 on, where a window and the new tokens behind it could pass 63 bits as well."""
+    L, lib = _lib()
+    f = lib.fp4q_attention_mxfp4_workspace_bytes
+    assert f(8, 8, 8, 2, 128, 1, 4096, (1 << 31) - 1) == f(8, 8, 8, 2, 128, 1, 4096, 0) > 0
+    for window in (1 << 31, (1 << 63) - 1):
+        assert f(8, 8, 8, 2, 128, 1, 4096, window) == 0
+        assert _attend(L, lib, window=window) == L.ERR_ARG
+
+
 def test_calls_without_new_tokens_are_not_split():
     """max_new 0 on a long cache has no units, so no partial results and no second kernel, which would have a grid
     without workgroups."""

@@ -8,6 +8,8 @@ from collections import namedtuple
 
 import pytest
 
+import test_gpu_kv_prompts as prompts
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 _PROGRAM = r"""
@@ -71,3 +73,12 @@ def test_plans_stay_inside_what_a_launch_and_a_workspace_may_have(plan):
             assert 0 <= p.units <= 1 << 22 and 0 <= p.spans < 512
             assert p.part_floats == (2 * p.spans * p.rows * (dim + 2) if p.spans else 0)
             assert p.spans == 0 or p.units > 0
+
+
+@pytest.mark.parametrize("name,dim", prompts.CASES)
+def test_shapes_of_the_prompt_tests_reach_their_kernels(plan, name, dim):
+    rows, split, lens, news, heads, kv_heads, page = prompts.SHAPES[name]
+    windows = (0,) if split else (0, 1, 77, 90, 300, 400)  # a window bounds the keys that are worth a split
+    for window in windows:
+        p = plan(lens, news, heads, kv_heads, dim, page, window)
+        assert (p.rows, p.spans > 0) == (rows, split), window

@@ -1226,10 +1226,12 @@ void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL((attn_rows_kernel<D, 4>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attn_rows_kernel<D, 1>), grid, dim3(64), 0, s, a);
-  if (!p.spans) return;
-  const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
-  hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),
-                     dim3(256), 0, s, a);
+  if constexpr (ROWS < 256) {  // tiles of 256 rows are never split (make_plan)
+    if (!p.spans) return;
+    const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
+    hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),
+                       dim3(256), 0, s, a);
+  }
 }
 
 }  // namespace
@@ -1240,7 +1242,8 @@ using namespace fp4q;
 extern "C" size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads,
                                                        int64_t head_dim, int64_t max_new, int64_t max_len,
                                                        int64_t window) {
-  if (window < 0 || window > 0x7FFFFFFF || !sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
+  if (window < 0 || window > 0x7FFFFFFF) return 0;
+  if (!sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
   const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len, window);
   return kAttnHeader + p.spans * sizeof(Join) + 4 * (size_t)p.part_floats;
 }

@@ -265,7 +265,8 @@ inline Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t he
   // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
   // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
   const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
-  // More units than a launch may have workgroups are taken in spans too.
+  // More units than a launch may have workgroups are taken in spans too.  Tiles of 256 rows never are: there are 512
+  // units at least, and with 512 rows a sequence on average and fewer than 2^27 rows in all fewer than 2^20.
   // No units (max_new 0): nothing to split, and a second kernel without rows would be no launch at all.
   const bool direct =
       p.units <= kMaxGroups && (tiles <= 34 || p.units == 0 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));

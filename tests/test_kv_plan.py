@@ -75,6 +75,26 @@ def test_plans_stay_inside_what_a_launch_and_a_workspace_may_have(plan):
             assert p.spans == 0 or p.units > 0
 
 
+def test_tiles_of_256_rows_are_never_split(plan):
+    """Over sizes up to the largest that a call may have."""
+    found = 0
+    for dim in (64, 128):
+        for kv_heads in (1, 8, 64, 65536 // dim):
+            for groups in (1, 4, 64):
+                for log_batch in (0, 3, 9, 16):
+                    for new in (1, 7, 512, 100000, (1 << 33) // (kv_heads * groups * dim) >> log_batch):
+                        batch = 1 << log_batch
+                        if not 0 < batch * new * kv_heads * groups * dim < 1 << 33 or kv_heads * groups > 65536:
+                            continue
+                        for length in (new, 1 << 20):
+                            p = plan([length] * batch, [new] * batch, kv_heads * groups, kv_heads, dim, 1024,
+                                     max_new=new)
+                            if p.rows == 256:
+                                found += 1
+                                assert p.spans == 0 and p.units < 1 << 20
+    assert found > 50
+
+
 @pytest.mark.parametrize("name,dim", prompts.CASES)
 def test_shapes_of_the_prompt_tests_reach_their_kernels(plan, name, dim):
     rows, split, lens, news, heads, kv_heads, page = prompts.SHAPES[name]

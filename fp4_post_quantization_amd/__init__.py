@@ -792,8 +792,8 @@ def rotate_heads(x, positions=None, table=None, *, interleaved=False, norm_weigh
     the first rotary_dim elements of a head are rotated (a multiple of 16),
     element i paired with i + rotary_dim/2, or 2i with 2i + 1 when
     interleaved.  hadamard_n: rotate by the block Hadamard matrix at the end.
-    out: a dense tensor to write into (x itself is allowed).  check:
-    synchronize and raise on data errors."""
+    out: a dense tensor to write into (x itself is allowed; it must not
+    overlap x otherwise).  check: synchronize and raise on data errors."""
     lib = L.load()
     x = _heads(x, "x")
     tokens, heads, dim = x.shape
@@ -885,7 +885,7 @@ def attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, *, max_new=None,
     Returns out [tokens, q_heads, head_dim] in bfloat16, with return_lse
     also the float32 [tokens, q_heads] natural log-sum-exp of the scores.
     Rows of q beyond cu_q's last offset are left as they are in a given out
-    (unspecified in a fresh one).  ws: a workspace of
+    (unspecified in a fresh one); out must not overlap the inputs.  ws: a workspace of
     ``fp4q_attention_mxfp4_workspace_bytes`` bytes (a fresh one by default);
     calls that may overlap need one each.  check: synchronize and raise on
     data errors."""

@@ -14,7 +14,7 @@
 //  * Both are computed transposed, S^T = K Q^T and O^T += V^T P^T: a lane's
 //    score registers belong to one query row, and after exponentiation they
 //    are P^T's operand as they lie, so that no score passes through LDS.
-//    P is rounded to bfloat16 there (2^-9 of each term at most); the sum l
+//    P is rounded to bfloat16 there (2^-8 of each term at most); the sum l
 //    adds the exponentials before that, in float32, as are m, S and O.
 //  * Few rows (attn_rows_kernel) are bound by the cache's bytes and, where
 //    there are few of those, by a chain of dependent loads: lengths, page
@@ -599,7 +599,7 @@ __device__ __forceinline__ int page_of(const AttnArgs &a, const int32_t *row_tab
 // rows for each 16 lanes), the next tile's while it computes this one's.
 // Bound by the cache's bytes: 64 sequences of 0 to 8192 tokens (64 query
 // heads on 8, 128 wide; 292 MB) 61 us, 4.8 TB/s; 131072 tokens of one
-// sequence (32 on 8, 143 MB) 30 us, 4.7 TB/s, and 5 us for the join.  HBM
+// sequence (64 on 8, 143 MB) 30 us, 4.7 TB/s; the join takes 5 us more.  HBM
 // traffic is 1.00 of the bytes.  Short ones are bound by latency: 100 tokens
 // take 6 us (launch, length, page, codes, merge), and each further tile of a
 // wave 0.8 us, with one wave on a SIMD: 1024 tokens 12.5 us.  A third register
@@ -766,8 +766,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
 //    16 consecutive elements of its row.
 // 16-byte pieces of both are swizzled so that 16 lanes that read or write
 // together fall on different banks.
-// 2048 new tokens on 8192 keys (64 query heads on 8, 128 wide; 412 GFLOP)
-// take 390 to 430 us, as the clock allows: 0.96 to 1.05 PFLOP/s, 69 to 76% of
+// 4096 new tokens on 8192 keys (32 query heads on 8, 128 wide; 412 GFLOP)
+// take 385 to 430 us, as the clock allows: 0.96 to 1.07 PFLOP/s, 69 to 77% of
 // what a large bfloat16 matrix product of the vendor's library reaches (1.38).  The vector pipe (key
 // decoding, exponentials) is busy 70% of the cycles and the matrix cores 48%,
 // at a clock that the load lowers to 1.7 - 2.1 GHz.  Measured and not kept:

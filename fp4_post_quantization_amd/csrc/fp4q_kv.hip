@@ -221,7 +221,7 @@ __device__ __forceinline__ void map_head(HeadLoad &h, int c, int lane, bool coun
 // Per head: z = x r w with r = 1 / sqrt(mean x^2 + eps), pairs (a, b) turned
 // to (a c - b s, b c + a s), groups of n multiplied by H_n / sqrt(n).  Bound by
 // the bytes for long inputs: 8192 tokens of 32 heads of 128 in float32 (268 MB)
-// take 45 us, 6.0 TB/s (part of it from the last level cache), bfloat16 34 us;
+// take 45 us, 6.0 TB/s (part of it from the last level cache), bfloat16 26 us;
 // one token takes 2.7 us, a launch.
 // float32 results are stored through the cache: a lane's 32 bytes are two
 // stores, and streamed past it they were written 16% more than once (48.5 us
@@ -331,10 +331,15 @@ struct AppendArgs {
   uint32_t *status;
 };
 
-// blockIdx.y: keys or values.  8192 tokens of 8 heads of 128, bfloat16, two
-// exponents searched (34 + 9 MB and 4 MB of the rotation table): 14.8 us, bound
-// by the vector pipe: of its 220 instructions a wave 80 are the two losses,
-// which are sums in element order and so pass from lane to lane.
+// blockIdx.y: keys or values.  8192 tokens of 8 heads of 128, bfloat16, keys
+// rotated and put through H_128 (34 + 9 MB and 4 MB of the rotation table), in
+// a graph: 15.5 us with one exponent (window 0, 0), 19.3 with two searched (-1, 0),
+// 25.1 with four; the bytes alone would take 9.0.  Bound by the vector pipe: 226
+// instructions a wave (the mean of keys and values) without a search and 364
+// with two exponents, since a loss is a sum in element order and so passes from
+// lane to lane.  Of the 226, a lane whose keys are rotated in halves spends some
+// on its partner's 8 elements, which it loads (and norms) a second time; without a
+// map two exponents take 13.9 us.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int LPH = D / kChunk;
@@ -373,8 +378,9 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
 }
 
 // ------------------------------------------------------------- kv_read ----
-// 8192 tokens of 8 heads of 128 to bfloat16 (9 MB read, 34 written): 8.8 us,
-// 4.9 TB/s; with multiplications in place of the conversion to bfloat16 10.6.
+// 8192 tokens of 8 heads of 128 to bfloat16 (9 MB read, 34 written): 7.4 us in a
+// graph, 8.8 among other kernels (4.9 TB/s; 10.6 with multiplications in place of
+// the conversion to bfloat16); to float32 (67 MB written) 17 us, 4.5 TB/s.
 template <typename OutT, int D>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(CacheView cache, const int64_t *__restrict__ slots,
                                                             int units, Divider heads, OutT *k_out, OutT *v_out,

@@ -263,7 +263,10 @@ inline Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t he
   p.units = units_of(p.rows);
   const int64_t fit = kCus * (head_dim == 256 || p.rows == 256 ? 1 : 2);  // workgroups on the chip at once
   // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
-  // are enough to fill the chip: 64 sequences of up to 2048 keys (512 units of up to 64 tiles) 33 us, split 38.
+  // are enough to fill the chip: 64 sequences of up to 2000 keys (512 units of up to 63 tiles) 25.0 us, split 27.3.
+  // Short is up to 1024 keys of 16 rows and 2048 of more.  Whole and split: 512 keys 9.3 us and 12.2; 1000 keys 12.9
+  // and 12.4, of 16 sequences 13.4 and 15.9, heads of 256 (16 on 2) 19.3 and 17.1; 2000 keys 19.8 and 12.9; a prompt
+  // of 2000 tokens 61 and 91, two chunks of 600 on 1500 keys 49 and 76.
   const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
   // More units than a launch may have workgroups are taken in spans too.  Tiles of 256 rows never are: there are 512
   // units at least, and with 512 rows a sequence on average and fewer than 2^27 rows in all fewer than 2^20.

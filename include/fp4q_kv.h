@@ -47,8 +47,8 @@ extern "C" {
  *   codes of (p, h, r) start at p * page_stride + h * head_stride +
  *   r * token_stride (bytes), the same for keys and values; scales start at
  *   a sixteenth of that offset, so they lie in the same order as the codes.
- *   Strides are multiples of 16 and do not make rows overlap, the code
- *   pointers are 16-byte aligned, page_size is a power of two from 16 to
+ *   Strides are multiples of 16 and do not make rows overlap, token_stride is
+ *   at most 2^26, the code pointers are 16-byte aligned, page_size is a power of two from 16 to
  *   1024, heads * head_dim at most 65536, and pages * page_size * heads below
  *   2^40.  Any byte may be in the rows that no token was written to. */
 typedef struct fp4q_kv_cache {
@@ -147,7 +147,8 @@ fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *sl
  *            sequence's last page are not read.  block_table may be NULL
  *            where max_len is 0.
  *   max_new, max_len  no sequence has more rows of q, or more cached tokens
- *            (max_len at most table_width * page_size and 2^30).
+ *            (max_new at most tokens, max_len at most table_width * page_size
+ *            and 2^30).
  *   causal   1: row i of n sees the keys up to its own position, seq_len - n
  *            + i; 0: every key.
  *   window   0: no limit; w > 0 (below 2^31): no row sees keys at its
@@ -172,7 +173,8 @@ fp4q_status_t fp4q_kv_read_mxfp4(const fp4q_kv_cache_t *cache, const int64_t *sl
  *
  * Data errors: a page number outside 0 .. pages - 1 (its tokens count as
  * masked), a sequence length or row offset outside its bounds (cut to them)
- * set FP4Q_DATA_BAD_TABLE and leave that sequence's rows unspecified.  Bytes
+ * set FP4Q_DATA_BAD_TABLE and leave that sequence's rows unspecified, and row
+ * offsets that decrease those of every sequence.  Bytes
  * of tokens that no row of a sequence sees do not matter, whatever they are;
  * a key or value scale of 255 (NaN) that some row sees can reach the other
  * rows of its sequence.

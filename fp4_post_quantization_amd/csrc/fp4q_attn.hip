@@ -15,7 +15,12 @@
 //    score registers belong to one query row, and after exponentiation they
 //    are P^T's operand as they lie, so that no score passes through LDS.
 //    P is rounded to bfloat16 there (2^-8 of each term at most); the sum l
-//    adds the exponentials before that, in float32, as are m, S and O.
+//    adds the exponentials before that, in float32, as are m, S and O.  The
+//    result, bfloat16 itself, is then off by 0.0017 to 0.0024 (relative, root
+//    mean square) where its own rounding alone gives 0.0016.  P in two parts
+//    gave that 0.0016 for few rows, at 3 to 8% of the time (64 sequences 63.9
+//    -> 68.7 us), and would take half as many matrix instructions again in a
+//    prompt, which they bound beside the vector pipe.
 //  * Few rows (attn_rows_kernel) are bound by the cache's bytes and, where
 //    there are few of those, by a chain of dependent loads: lengths, page
 //    number, codes.  Many rows (attn_prompt_kernel) are bound by the vector

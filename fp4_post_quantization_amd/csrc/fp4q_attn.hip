@@ -24,7 +24,8 @@
 //  * Few rows (attn_rows_kernel) are bound by the cache's bytes and, where
 //    there are few of those, by a chain of dependent loads: lengths, page
 //    number, codes.  Many rows (attn_prompt_kernel) are bound by the vector
-//    and matrix pipes.
+//    and matrix pipes.  A call whose sequences differ much runs both, each on
+//    its own sequences, one after the other (make_plan).
 //  * A long cache with few units is cut into equal spans of work, one for
 //    each workgroup that the chip holds, whatever sequence they fall in; a
 //    span keeps what it has of a unit in float32 and attn_join_kernel joins
@@ -73,6 +74,7 @@ struct AttnArgs {
   uint16_t *out;
   float *lse;
   uint32_t *status;
+  bool first;  // the call's first kernel, which takes the status slot
   float *parts;
   Join *joins;  // [spans]
   int spans;  // work items of the split form; 0: one workgroup per (sequence, row tile, head)
@@ -576,10 +578,10 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 
 // The first workgroup of a call takes the status slot and checks every
 // sequence's length and rows; it has no other work, so that nobody's work
-// waits for the slot's atomics.
+// waits for the slot's atomics.  In a second pass it has none at all.
 __device__ __forceinline__ bool is_status_group(const AttnArgs &a, int lane, int wave) {
   if (blockIdx.x != 0) return false;
-  if (wave == 0) {
+  if (wave == 0 && a.first) {
     bool bad = false;
     for (int i = lane; i < a.sh.batch; i += 64) bad |= seq_of(a, i).bad;
     const uint32_t bits = __ballot(bad) ? FP4Q_DATA_BAD_TABLE : 0u;
@@ -751,7 +753,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_rows_kernel(At
     __syncthreads();
   }
   walk.finish();
-  if (__builtin_expect(err != 0u, 0)) Status{a.status, true}.report(err);
+  if (__builtin_expect(err != 0u, 0)) Status{a.status, a.first}.report(err);
 }
 
 // ------------------------------------------------------------ prompts ----
@@ -1121,7 +1123,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_prompt_kernel(
     }
   }
   walk.finish();
-  if (__builtin_expect(err != 0u, 0)) Status{a.status, true}.report(err);
+  if (__builtin_expect(err != 0u, 0)) Status{a.status, a.first}.report(err);
 }
 
 // Joins the partial results of units that several spans share: workgroups
@@ -1223,7 +1225,7 @@ bool sizes_ok(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
 
 template <int D, int ROWS>
-void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
+void launch(const AttnArgs &a, const Pass &p, hipStream_t s) {
   const dim3 grid((unsigned)(p.spans ? p.spans : p.units) + 1);
   if constexpr (ROWS >= 128)
     hipLaunchKernelGGL((attn_prompt_kernel<D, ROWS / 32>), grid, dim3(2 * ROWS), 0, s, a);
@@ -1231,13 +1233,16 @@ void launch(const AttnArgs &a, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL((attn_rows_kernel<D, 4>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((attn_rows_kernel<D, 1>), grid, dim3(64), 0, s, a);
-  if constexpr (ROWS < 256) {  // tiles of 256 rows are never split (make_plan)
+  if constexpr (ROWS < 256) {  // tiles of 256 rows are never split (make_pass)
     if (!p.spans) return;
     const int64_t rows = (int64_t)a.sh.max_new * a.sh.groups;  // no unit has more than its sequence
     hipLaunchKernelGGL((attn_join_kernel<D, ROWS>), dim3((unsigned)p.spans, (unsigned)(rows < 16 ? rows : 16)),
                        dim3(256), 0, s, a);
   }
 }
+
+// Bytes that a pass leaves for its joining kernel.
+size_t shared_bytes(const Pass &p) { return p.spans * sizeof(Join) + 4 * (size_t)p.part_floats; }
 
 }  // namespace
 }  // namespace fp4q
@@ -1250,7 +1255,9 @@ extern "C" size_t fp4q_attention_mxfp4_workspace_bytes(int64_t tokens, int64_t b
   if (window < 0 || window > 0x7FFFFFFF) return 0;
   if (!sizes_ok(tokens, batch, q_heads, heads, head_dim, max_new, max_len)) return 0;
   const Plan p = make_plan(tokens, batch, q_heads, heads, head_dim, max_new, max_len, window);
-  return kAttnHeader + p.spans * sizeof(Join) + 4 * (size_t)p.part_floats;
+  size_t most = 0;  // the passes run one after the other
+  for (int i = 0; i < p.passes; ++i) most = shared_bytes(p.pass[i]) > most ? shared_bytes(p.pass[i]) : most;
+  return kAttnHeader + most;
 }
 
 extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, const void *q, int64_t q_token_stride,
@@ -1313,17 +1320,26 @@ extern "C" fp4q_status_t fp4q_attention_mxfp4(const fp4q_kv_cache_t *cache, cons
   a.out = (uint16_t *)out;
   a.lse = lse;
   a.status = status;
+  a.first = true;
   a.joins = (Join *)((char *)workspace + kAttnHeader);
-  a.parts = (float *)(a.joins + p.spans);
-  a.spans = p.spans;
-  auto go = [&](auto dc) {
-    constexpr int D = decltype(dc)::value;
-    if (p.rows == 16) launch<D, 16>(a, p, s);
-    else if (p.rows == 128) launch<D, 128>(a, p, s);
-    else if constexpr (D != 256) launch<D, 256>(a, p, s);
-  };
-  if (cache->head_dim == 64) go(std::integral_constant<int, 64>{});
-  else if (cache->head_dim == 128) go(std::integral_constant<int, 128>{});
-  else go(std::integral_constant<int, 256>{});
+  for (int i = 0; i < p.passes; ++i) {
+    const Pass &pass = p.pass[i];
+    // without cu_q every sequence has the rows of one token, and one pass serves them all
+    if (!cu_q && (a.sh.groups < pass.min_rows || a.sh.groups > pass.max_rows)) continue;
+    a.sh.min_rows = pass.min_rows;
+    a.sh.max_rows = pass.max_rows;
+    a.spans = pass.spans;
+    a.parts = (float *)(a.joins + pass.spans);
+    auto go = [&](auto dc) {
+      constexpr int D = decltype(dc)::value;
+      if (pass.rows == 16) launch<D, 16>(a, pass, s);
+      else if (pass.rows == 128) launch<D, 128>(a, pass, s);
+      else if constexpr (D != 256) launch<D, 256>(a, pass, s);
+    };
+    if (cache->head_dim == 64) go(std::integral_constant<int, 64>{});
+    else if (cache->head_dim == 128) go(std::integral_constant<int, 128>{});
+    else go(std::integral_constant<int, 256>{});
+    a.first = false;
+  }
   return hip_status();
 }

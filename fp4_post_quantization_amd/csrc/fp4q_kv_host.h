@@ -122,6 +122,7 @@ struct AttnShape {
   int heads;            // cache heads
   int max_new, max_len; // host bounds on a sequence's new tokens and length
   int causal, window;
+  int min_rows = 0, max_rows = INT32_MAX;  // (token, head of the group) rows of the sequences that are served
 };
 
 // One sequence as the kernels see it: its values cut to what the call's
@@ -163,16 +164,18 @@ FP4Q_HD int attn_lo(const AttnShape &a, const AttnSeq &s, int i) {
   return p < 0 ? 0 : (p > s.len ? s.len : (int)p);
 }
 
-// Row tiles of a sequence (rows_per_tile of its fresh * groups rows each) and
-// the key tiles of tile_len tokens that any of its rows can see: key tiles
-// lo .. lo + n - 1, at least one, so that every row tile is somebody's work.
+// Row tiles of a sequence (rows_per_tile of its fresh * groups rows each; none
+// where another pass serves it) and the key tiles of tile_len tokens that any
+// of its rows can see: key tiles lo .. lo + n - 1, at least one, so that every
+// row tile is somebody's work.
 struct AttnWork {
   int64_t row_tiles;
   int lo, n;
 };
 FP4Q_HD AttnWork attn_work(const AttnShape &a, const AttnSeq &s, int rows_per_tile, int tile_len) {
   AttnWork w;
-  w.row_tiles = ((int64_t)s.fresh * a.groups + rows_per_tile - 1) / rows_per_tile;
+  const int rows = s.fresh * a.groups;  // below 2^27
+  w.row_tiles = rows < a.min_rows || rows > a.max_rows ? 0 : (rows + rows_per_tile - 1) / rows_per_tile;
   w.lo = attn_lo(a, s, 0) / tile_len;
   const int hi = s.fresh ? attn_hi(a, s, s.fresh - 1) : 0;
   w.n = (int)(((int64_t)hi + tile_len - 1) / tile_len) - w.lo;
@@ -226,59 +229,94 @@ FP4Q_HD int64_t attn_span_of(int64_t total, int64_t spans, int64_t pos) {
 constexpr int kCus = 256;
 constexpr int64_t kMaxGroups = 1 << 22;  // with 512 threads each, half of what a launch may have
 
-struct Plan {
+constexpr int kFewRows = 96;  // of a sequence and cache head, up to which tiles of 16 serve it
+
+// One kernel's part of a call: the sequences that have min_rows to max_rows rows (of one head).
+struct Pass {
   int rows;       // of a row tile: 16 (attn_rows_kernel), 128 or 256 (attn_prompt_kernel)
   int waves;      // of attn_rows_kernel
   int64_t units;  // upper bound of (sequence, row tile, head) units
   int spans;
   int64_t part_floats;
+  int min_rows, max_rows;
 };
+struct Plan {
+  int passes;  // 1 or 2, one after the other in the same workspace
+  Pass pass[2];
+};
+
+inline Pass make_pass(int rows, int64_t units, int64_t keys, int64_t head_dim, int min_rows, int max_rows) {
+  const int64_t fit = kCus * (head_dim == 256 || rows == 256 ? 1 : 2);  // workgroups on the chip at once
+  // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
+  // are enough to fill the chip: 64 sequences of up to 2000 keys (512 units of up to 63 tiles) 25.0 us, split 27.3.
+  // Short is up to 1024 keys of 16 rows and 2048 of more.  Whole and split: 512 keys 9.3 us and 12.2; 1000 keys 12.9
+  // and 12.4, of 16 sequences 13.4 and 15.9, heads of 256 (16 on 2) 19.3 and 17.1; 2000 keys 19.8 and 12.9; a prompt
+  // of 2000 tokens 61 and 91, two chunks of 600 on 1500 keys 49 and 76.
+  const int64_t tiles = keys / (rows == 16 ? 32 : 64) + 2;
+  // More units than a launch may have workgroups are taken in spans too.  Tiles of 256 rows never are: there are 512
+  // units at least, and with 512 rows a sequence on average and fewer than 2^27 rows in all fewer than 2^20.
+  // No units (max_new 0): nothing to split, and a second kernel without rows would be no launch at all.
+  const bool direct =
+      units <= kMaxGroups && (tiles <= 34 || units == 0 || (units >= fit && (rows != 16 || tiles <= 66)));
+  Pass p;
+  p.rows = rows;
+  p.units = units;
+  p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
+  // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
+  // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26
+  // with four; 200 of up to 500, 25 and 32; 128 of up to 1000, 34 and 29.
+  p.waves = direct && units > 512 && tiles <= 18 ? 1 : 4;
+  p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * rows * (head_dim + 2);
+  p.min_rows = min_rows;
+  p.max_rows = max_rows;
+  return p;
+}
 
 inline Plan make_plan(int64_t tokens, int64_t batch, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t max_new,
                       int64_t max_len, int64_t window) {
   const int64_t groups = q_heads / heads, seq_rows = max_new * groups, all_rows = tokens * groups;
   const int64_t live = batch < tokens ? batch : tokens;  // sequences that have rows, at most
   const int64_t keys = window && window + max_new < max_len ? window + max_new : max_len;  // of a row tile, at most
-  auto units_of = [&](int64_t rows) {  // a sequence's rows fill its row tiles except the last one
-    const int64_t tiles = all_rows / rows + live, most = live * ((seq_rows + rows - 1) / rows);
+  // units of so many sequences of so many rows, at most: a sequence's rows fill its row tiles except the last one
+  auto units_of = [&](int64_t rows, int64_t seqs, int64_t most_rows) {
+    const int64_t tiles = all_rows / rows + seqs, most = seqs * ((most_rows + rows - 1) / rows);
     return (tiles < most ? tiles : most) * heads;
   };
-  Plan p;
+  // The average sequence has half of the longest one's rows or more: one kernel for all.  Else there can be a few long
+  // ones among short or empty ones (a chunk of a prompt beside decoding tokens, a padded batch, no bound on the new
+  // tokens), and a row tile costs the same however few of its rows are live: each kernel serves its own.
+  // Measured, us (32 heads on 8, 128 wide): two passes, one of tiles of 128, one of 16: 63 tokens and a chunk of 512 on
+  // 8192 keys 232, 409, 289; 60 and four of 512 on 4096 228, 296, 426; 31 and 2048 on 4096 160, 201, 405; 127 and 128
+  // on 2048 113, 174, 74; 512 alone in a batch of 64 on 8192 116, 190, 169; 64 tokens without a bound (64 heads) 78,
+  // 234, 71.  Units that run at once, most of them full, need no second pass: three tokens and 1000 on 2048 keys 70
+  // and 57.
+  const bool even =
+      2 * all_rows >= seq_rows * live ||
+      (all_rows >= 128 * live && units_of(128, live, seq_rows) <= kCus * (head_dim == 256 ? 1 : 2));
+  int64_t long_ones = all_rows / (kFewRows + 1);
+  if (even || live < long_ones) long_ones = live;
   // A row tile of 128 costs a fifth of eight of 16 for each key, but it has to be filled, and there have to be
   // enough of them for half the CUs, or keys enough to be split.  Measured (32 heads on 8, 128 wide; one sequence
   // unless said): 80 rows a head on 8192 keys, two sequences: 37 us with 16, 52 with 128; 512 rows on 16384 keys
   // 103 and 85; 2048 rows on 512 keys 34 (with 32) and 25; five sequences of up to 951 rows behind a window of 1000
-  // (12 heads on 4 of 64) 20 and 37.  256 rows share the staging of a key tile among twice the waves where there
-  // are still two workgroups for each CU: 16384 rows a head on 8192 keys 505 us with 128, 470 with 256; 8192 rows on
-  // 2048 keys 65 and 71.
-  // A row tile costs the same however few of its rows are live, so the average sequence has to fill it as well as the
-  // longest (its rows: T): a chunk of a prompt beside decoding tokens.  64 sequences of 4096 keys, rows in all over
-  // sequences: T 67: 240 us with 16, 234 with 128; 131: 405 and 289; T 36 (8192 keys) 285 and 434; T 8 (2048 keys)
-  // 73 and 175, and without a bound on the new tokens, which leaves seq_rows the rows of all, 71 and 344.  256 rows
-  // from T 512 on: 64 sequences of 128 rows on 4096 keys 177 us with 128, 274 with 256; of 512 on 2048 keys 320 and
-  // 297; 31 of 4 and one of 8192 on 4096 keys (T 260) 193 and 234.
-  p.rows = 16;
-  if (seq_rows > 96 && all_rows > 64 * live && (units_of(128) >= kCus / 2 || keys > 4096))
-    p.rows = head_dim != 256 && all_rows >= 512 * live && units_of(256) >= 2 * kCus ? 256 : 128;
-  p.units = units_of(p.rows);
-  const int64_t fit = kCus * (head_dim == 256 || p.rows == 256 ? 1 : 2);  // workgroups on the chip at once
-  // Not split: one workgroup a unit, no second kernel (5 us).  For short units, and for middling ones where there
-  // are enough to fill the chip: 64 sequences of up to 2000 keys (512 units of up to 63 tiles) 25.0 us, split 27.3.
-  // Short is up to 1024 keys of 16 rows and 2048 of more.  Whole and split: 512 keys 9.3 us and 12.2; 1000 keys 12.9
-  // and 12.4, of 16 sequences 13.4 and 15.9, heads of 256 (16 on 2) 19.3 and 17.1; 2000 keys 19.8 and 12.9; a prompt
-  // of 2000 tokens 61 and 91, two chunks of 600 on 1500 keys 49 and 76.
-  const int64_t tiles = keys / (p.rows == 16 ? 32 : 64) + 2;
-  // More units than a launch may have workgroups are taken in spans too.  Tiles of 256 rows never are: there are 512
-  // units at least, and with 512 rows a sequence on average and fewer than 2^27 rows in all fewer than 2^20.
-  // No units (max_new 0): nothing to split, and a second kernel without rows would be no launch at all.
-  const bool direct =
-      p.units <= kMaxGroups && (tiles <= 34 || p.units == 0 || (p.units >= fit && (p.rows != 16 || tiles <= 66)));
-  p.spans = direct ? 0 : (int)fit - 1;  // one workgroup serves the status
-  // Waves that share a unit of attn_rows_kernel: four, and one for many short units, each of which costs its waves
-  // about six key tiles' time whatever their number.  256 sequences of up to 100 keys (2048 units) 12 us with one, 26
-  // with four; 200 of up to 500, 25 and 32; 128 of up to 1000, 34 and 29.
-  p.waves = direct && p.units > 512 && tiles <= 18 ? 1 : 4;
-  p.part_floats = direct ? 0 : 2 * (int64_t)p.spans * p.rows * (head_dim + 2);
+  // (12 heads on 4 of 64) 20 and 37.
+  Plan p;
+  p.passes = 1;
+  if (seq_rows <= kFewRows || (units_of(128, long_ones, seq_rows) < kCus / 2 && keys <= 4096)) {
+    p.pass[0] = make_pass(16, units_of(16, live, seq_rows), keys, head_dim, 0, INT32_MAX);
+    return p;
+  }
+  // 256 rows share the staging of a key tile among twice the waves where there are still two workgroups for each CU:
+  // 16384 rows a head on 8192 keys 505 us with 128, 470 with 256; 8192 rows on 2048 keys 65 and 71; 64 sequences of
+  // 512 rows on 2048 keys 320 and 297.  Sequences with fewer rows leave much of them empty: 64 of 128 rows on 4096
+  // keys 177 and 274.
+  const int64_t most = units_of(256, long_ones, seq_rows);
+  const int rows = head_dim != 256 && all_rows >= 512 * long_ones && most >= 2 * kCus ? 256 : 128;
+  p.pass[0] = make_pass(rows, units_of(rows, long_ones, seq_rows), keys, head_dim, even ? 0 : kFewRows + 1, INT32_MAX);
+  if (!even) {
+    p.passes = 2;
+    p.pass[1] = make_pass(16, units_of(16, live, kFewRows), keys, head_dim, 0, kFewRows);
+  }
   return p;
 }
 

@@ -433,13 +433,66 @@ def test_attention_leaves_other_rows_alone():
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("kw", [{}, dict(max_new=200)])
-def test_attention_chunk_beside_decoding_sequences(dim, kw):
-    """Tokens of one prompt and single tokens in one call, with and without a bound on a sequence's rows: 52 and 600
-    rows a sequence and head on average, which tiles of 16 and of 128 rows take."""
-    rows = np.array([0, 1, 15, 63, 99, 127, 128, 199])
-    lens = [40, 5000, 700, 1, 320, 16, 17, 999]
-    _run(_fq(), np.random.default_rng(dim), lens, [1, 1, 100, 1, 0, 1, 1, 1], 8, 2, dim, 64, rows=rows)
-    _run(_fq(), np.random.default_rng(dim), lens[:3], [1, 1, 199], 36, 4, dim, 64, rows=rows, **kw)
+@pytest.mark.parametrize("window", [0, 130])
+def test_attention_chunk_beside_decoding_sequences(dim, kw, window):
+    """Rows of prompts and single tokens in one call, which the two kernels share between them: with and without a
+    bound on a sequence's rows, sequences at the border between them (96 and 97 rows of a head), empty ones."""
+    rows = np.array([0, 1, 15, 23, 24, 63, 99, 127, 128, 199])
+    lens = [40, 5000, 700, 1, 320, 16, 17, 999, 90, 200, 210, 2300]
+    news = [1, 1, 100, 1, 0, 1, 1, 1, 2, 24, 25, 200]
+    _run(_fq(), np.random.default_rng(dim), lens, news, 8, 2, dim, 64, rows=rows, window=window, **kw)
+    _run(_fq(), np.random.default_rng(dim), lens[:3], [1, 1, 199], 36, 4, dim, 64, rows=rows, window=window, **kw)
+    _run(_fq(), np.random.default_rng(dim), [0] * 40 + [300], [0] * 40 + [200], 64, 16, dim, 16, rows=rows,
+         window=window)  # a padded batch
+
+
+def test_attention_errors_of_both_kernels_are_kept():
+    """A call that both kernels share reports what either finds, and leaves the other sequences as they would be; a
+    call without errors on the same workspace clears them; captured and replayed it gives the same bits."""
+    fq = _fq()
+    rng = np.random.default_rng(17)
+    lens, news, page, heads, kv, dim = [5000, 40, 70, 600], [200, 1, 1, 150], 64, 8, 2, 128
+    width = -(-max(lens) // page)
+    cache = _filled(fq, rng, 4 * width, kv, page, dim)
+    ids = torch.from_numpy(rng.permutation(4 * width).reshape(4, width).astype(np.int32)).to(DEV)
+    starts = np.concatenate([[0], np.cumsum(news)]).tolist()
+    cu = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    le = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = torch.from_numpy(rng.standard_normal((starts[-1], heads, dim)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    need = fq._lib.load().fp4q_attention_mxfp4_workspace_bytes(starts[-1], 4, heads, kv, dim, starts[-1],
+                                                               width * page, 0)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
+    good = fq.attention_mxfp4(q, cache, ids, le, cu, ws=ws, check=True)
+    for b in range(4):
+        bad_ids, bad_len = ids.clone(), le.clone()
+        bad_ids[b, 0] = 4 * width
+        bad_len[b] = width * page + 1
+        for t, n in ((bad_ids, le), (ids, bad_len)):
+            with pytest.raises(fq.FP4QError, match="page number"):
+                fq.attention_mxfp4(q, cache, t, n, cu, ws=ws, check=True)
+            got = fq.attention_mxfp4(q, cache, t, n, cu, ws=ws)
+            # another length moves the cuts of the work, so the others are as near as two results of one call may be:
+            # twice 2^-8 of the value and of sum p |v|, which are at most 1.5, and 2^-10 for the scores
+            near = 0.0 if n is le else 2 * 1.5 * (2.0 ** -7 + 2.0 ** -10)
+            assert bool(((got - good).float().abs()[:starts[b]] <= near).all())
+            assert bool(((got - good).float().abs()[starts[b + 1]:] <= near).all())
+        assert torch.equal(fq.attention_mxfp4(q, cache, ids, le, cu, ws=ws, check=True), good)
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fq.attention_mxfp4(q, cache, ids, le, cu, out=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fq.attention_mxfp4(q, cache, ids, le, cu, out=out, ws=ws)
+    for k in range(4):
+        ids[2, 0] = ids[2, 0] if k % 2 == 0 else -1
+        want = fq.attention_mxfp4(q, cache, ids, le, cu)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and fq.read_status(ws) == (0 if k == 0 else fq._lib.DATA_BAD_TABLE)
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])

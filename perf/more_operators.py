@@ -333,7 +333,7 @@ def _plain(s):
         live = int(s["offsets"][-1])
         x, there = _by_group(s["x"][rows].float(), s["offsets"], s["most"])
         u = torch.matmul(x, s["a"].float().transpose(1, 2)) * s["scales"][:, None, None]
-        out = s["y"].float()
+        out = s["y"].to(torch.float32, copy=True)
         out[rows[:live]] += torch.matmul(u, s["b"].float().transpose(1, 2))[there]
         return [out.to(s["y"].dtype)]
     k = c["k"]

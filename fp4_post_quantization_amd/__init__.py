@@ -1,8 +1,8 @@
 """fp4_post_quantization_amd -- FP4 microscaling block quantization with
 block-scale search on AMD MI355X (gfx950).
 
-Thin Python binding over the C ABI in include/fp4q.h, fp4q_gemm.h and
-fp4q_kv.h (libfp4q.so, built in place).  It only marshals arguments: torch supplies device memory and the
+Thin Python binding over the C ABI in include/fp4q.h, fp4q_gemm.h, fp4q_kv.h
+and fp4q_grouped.h (libfp4q.so, built in place).  It only marshals arguments: torch supplies device memory and the
 current HIP stream, and every step of the computation runs in the library's
 HIP kernels.  There is no CPU fallback; a missing library raises.
 
@@ -16,6 +16,11 @@ HIP kernels.  There is no CPU fallback; a missing library raises.
     kv_append_mxfp4(cache, k, v, slots, positions=None, table=None, ...)
     kv_read_mxfp4(cache, slots)
     attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, ...)
+    route_experts(logits, top_k, *, score="softmax", bias=None, n_groups=1, ...)
+    group_rows(ids, n_groups)
+    gemm_mxfp4_grouped(a, b, groups, *, gather=0, scatter=False, gated=False, ...)
+    combine_experts(y, weights, experts=None, *, add=None, ...)
+    lora_add(y, x, a, b, groups, *, scales=None, ...)
 """
 
 from typing import NamedTuple, Optional
@@ -30,6 +35,7 @@ __all__ = [
     "gptq_nvfp4", "gptq_mxfp4", "gptq_static_nvfp4", "gptq_static_mxfp4", "dequantize",
     "block_hadamard", "gemm_mxfp4", "gemm_nvfp4",
     "rotate_heads", "kv_cache_mxfp4", "kv_append_mxfp4", "kv_read_mxfp4", "attention_mxfp4", "KVCacheMXFP4",
+    "route_experts", "group_rows", "gemm_mxfp4_grouped", "combine_experts", "lora_add", "RowGroups", "ExpertRoute",
     "NVFP4Result", "MXFP4Result", "workspace", "read_status", "clear_status", "FP4QError",
 ]
 
@@ -101,6 +107,8 @@ def _check_data(ws):
             names.append("slot past the end of the cache")
         if st & L.DATA_BAD_TABLE:
             names.append("page number, sequence length or row offset out of range")
+        if st & L.DATA_BAD_GROUP:
+            names.append("group number, group offset or entry number out of range")
         raise FP4QError("data error: " + ", ".join(names))
 
 
@@ -932,3 +940,265 @@ def attention_mxfp4(q, cache, block_table, seq_lens, cu_q=None, *, max_new=None,
     if check:
         _check_data(ws)
     return (out, lse) if return_lse else out
+
+
+class RowGroups(NamedTuple):
+    """Entries (rows that belong to at most one group: an expert, an adapter)
+    by group: group g's are rows[offsets[g] : offsets[g + 1]], ascending; those
+    of no group come last.  ``rows`` holds every entry's number once."""
+    offsets: torch.Tensor  # int32 [groups + 1]
+    rows: torch.Tensor     # int32 [entries]
+
+
+class ExpertRoute(NamedTuple):
+    weights: torch.Tensor        # float32 [tokens, top_k]
+    experts: torch.Tensor        # int32 [tokens, top_k], best first; -1: none
+    groups: Optional[RowGroups]  # the entries token * top_k + choice by expert
+
+
+_SCORES = {"softmax": L.SOFTMAX, "sigmoid": L.SIGMOID}
+
+
+def _sized_ws(ws, device, need):
+    """The caller's workspace, the default one for a status word alone, or a
+    fresh one: calls captured into different graphs share the default one."""
+    if ws is None and need > 256:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    return _ws(ws, device)
+
+
+def _groups_struct(groups, device):
+    """fp4q_row_groups_t, packed, its groups and its entries."""
+    offsets, rows = groups
+    for name, t in (("offsets", offsets), ("rows", rows)):
+        if (not isinstance(t, torch.Tensor) or t.dim() != 1 or t.dtype is not torch.int32 or t.device != device
+                or (t.size(0) > 1 and t.stride(0) != 1)):
+            raise ValueError(f"groups.{name} must be a contiguous int32 vector on {device}")
+    n, entries = offsets.size(0) - 1, rows.size(0)
+    if n < 1:
+        raise ValueError("groups.offsets must have one entry more than there are groups")
+    return L.ROW_GROUPS_PACK(offsets.data_ptr(), rows.data_ptr(), n, entries), n, entries
+
+
+def _rows(t, name, device=None, dtypes=(torch.float32, torch.bfloat16)):
+    """A [rows, columns] device tensor with dense rows that do not overlap,
+    and their stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}, must be on {device or 'a GPU'}")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (rows > 1 and s0 < cols):
+        t, s0 = t.contiguous(), cols
+    return t, max(s0, cols) if rows > 1 else cols
+
+
+def _result(out, shape, dtype, device):
+    """A fresh result, or the caller's, and the stride of its rows."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    if (not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype not in (torch.float32, torch.bfloat16)
+            or out.device != device or (out.stride(1) != 1 and shape[1] > 1)
+            or (shape[0] > 1 and out.stride(0) < shape[1])):
+        raise ValueError(f"out must be a row-major float32 or bfloat16 tensor of shape {tuple(shape)} on {device}")
+    return out, max(out.stride(0), shape[1]) if shape[0] > 1 else shape[1]
+
+
+def group_rows(ids, n_groups, *, ws=None, check=False):
+    """RowGroups of a vector of group numbers (int32, any shape, taken in
+    order; negative: none), such as the adapter of each row of a batch.  A
+    number of n_groups or more is a data error and counts as none.  n_groups:
+    1 to 2048.  ws: a workspace of ``fp4q_group_rows_workspace_bytes`` bytes
+    (by default the stream's or a fresh one).  check: synchronize and raise on
+    data errors."""
+    lib = L.load()
+    if not isinstance(ids, torch.Tensor) or ids.dtype is not torch.int32 or not ids.is_cuda:
+        raise ValueError("ids must be an int32 device tensor")
+    dev = ids.device
+    ids = ids.contiguous()
+    n_groups, entries = int(n_groups), ids.numel()
+    if n_groups < 1:
+        raise ValueError("n_groups must be positive")
+    offsets = torch.empty(n_groups + 1, dtype=torch.int32, device=dev)
+    rows = torch.empty(entries, dtype=torch.int32, device=dev)
+    ws = _sized_ws(ws, dev, lib.fp4q_group_rows_workspace_bytes(entries, n_groups))
+    _launch(dev, lib.fp4q_group_rows, ids.data_ptr(), entries, n_groups, offsets.data_ptr(), rows.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    if check:
+        _check_data(ws)
+    return RowGroups(offsets, rows)
+
+
+def route_experts(logits, top_k, *, score="softmax", bias=None, n_groups=1, top_groups=1, group_best=1,
+                  renormalize=True, scale=1.0, group=True, ws=None, check=False):
+    """The top_k experts of each token and their weights, from router logits
+    [tokens, experts] (float32 or bfloat16; up to 1024 experts, top_k up to
+    64): scores are the softmax over the experts or each logit's sigmoid.
+
+    bias: float32 [experts], added to the scores for the choice alone.
+    n_groups, top_groups: experts in runs of equal length, of which a token
+    chooses within the top_groups best by the sum of their group_best (1 or 2)
+    best choices.  renormalize: divide the weights of a token by their sum.
+    scale: factor of the weights.  Choices are compared in float64 (without a
+    bias by the logits themselves); ties go to the lowest index.
+
+    A logit or bias of minus infinity turns an expert off; choices that a token
+    lacks are -1 with weight 0, and all of a token with a NaN or plus infinity,
+    which is a data error.  group: also sort the entries by expert
+    (ExpertRoute.groups).  ws: a workspace of
+    ``fp4q_route_experts_workspace_bytes`` bytes (by default the stream's or a
+    fresh one).  check: synchronize and raise on data errors."""
+    lib = L.load()
+    logits, ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    dev, top_k = logits.device, int(top_k)
+    if not 1 <= top_k <= experts:
+        raise ValueError("top_k must be 1 to the number of experts")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.device != dev or not bias.is_contiguous():
+            bias = bias.to(device=dev, dtype=torch.float32).contiguous()
+        if bias.shape != (experts,):
+            raise ValueError("bias must have one entry per expert")
+    router = L.ROUTER_PACK(_SCORES[score], _ptr(bias) or 0, top_k, int(n_groups), int(top_groups), int(group_best),
+                           bool(renormalize), scale)
+    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+    chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+    groups = None
+    if group:
+        groups = RowGroups(torch.empty(experts + 1, dtype=torch.int32, device=dev),
+                           torch.empty(tokens * top_k, dtype=torch.int32, device=dev))
+    ws = _sized_ws(ws, dev, lib.fp4q_route_experts_workspace_bytes(tokens, experts, top_k))
+    _launch(dev, lib.fp4q_route_experts, logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, router,
+            weights.data_ptr(), chosen.data_ptr(), groups.offsets.data_ptr() if group else None,
+            groups.rows.data_ptr() if group else None, ws.data_ptr(), ws.numel())
+    if check:
+        _check_data(ws)
+    return ExpertRoute(weights, chosen, groups)
+
+
+def gemm_mxfp4_grouped(a, b, groups, *, gather=0, scatter=False, gated=False, alpha=1.0, out_dtype=torch.float32,
+                       out=None, ws=None, check=False):
+    """alpha * A_hat[row of e] @ B_hat[g]^T for every entry e of every group g.
+
+    a: MXFP4Result or (codes, scales) of [rows, K] as ``quantize_mxfp4`` writes
+    it.  b: (codes uint8 [groups, N, K/2], scales uint8 [groups, N, K/32]), a
+    matrix of such rows for each group.  groups: RowGroups.
+    gather: 0: A has a row for each entry, in the groups' order; f: entry e
+    takes row e // f (f = top_k: its token's).  scatter: False: result rows in
+    the groups' order; True: row e is entry e's.  gated: B's first N/2 rows are
+    gates, the result [entries, N/2] is silu(gate) * up.
+
+    Returns [entries, N] (gated: N/2) in float32 or bfloat16; rows of entries
+    of no group are left as they are in a given out (unspecified in a fresh
+    one).  check: synchronize and raise on data errors."""
+    lib = L.load()
+    ac, as_ = (a.codes, a.scales) if isinstance(a, MXFP4Result) else a
+    bc, bs = (b.codes, b.scales) if isinstance(b, MXFP4Result) else b
+    if ac.dim() != 2 or bc.dim() != 3 or as_.dim() != 2 or bs.dim() != 3:
+        raise ValueError("a must be [rows, K/2] codes, b [groups, N, K/2] codes, with their scales")
+    m, kh = ac.shape
+    g, n, kh2 = bc.shape
+    if kh != kh2:
+        raise ValueError(f"K mismatch: A has {2 * kh}, B has {2 * kh2}")
+    dev = ac.device
+    ac, as_, bc, bs = (t.contiguous() for t in (ac, as_, bc, bs))
+    _same_device(dev, a_scales=as_, b_codes=bc, b_scales=bs)
+    if any(t.dtype is not torch.uint8 for t in (ac, as_, bc, bs)):
+        raise ValueError("codes and scales must be uint8")
+    if as_.shape != (m, kh // 16) or bs.shape != (g, n, kh // 16):
+        raise ValueError("scales must be rows x K/32")
+    packed, n_groups, entries = _groups_struct(groups, dev)
+    if n_groups != g:
+        raise ValueError(f"groups has {n_groups} groups, b {g}")
+    out, ldc = _result(out, (entries, n // 2 if gated else n), out_dtype, dev)
+    ws = _ws(ws, dev)
+    _launch(dev, lib.fp4q_gemm_mxfp4_grouped, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(), bs.data_ptr(), packed,
+            n, 2 * kh, int(gather), bool(scatter), bool(gated), alpha, _dtype_code(out), out.data_ptr(), ldc,
+            ws.data_ptr(), ws.numel())
+    if check:
+        _check_data(ws)
+    return out
+
+
+def combine_experts(y, weights, experts=None, *, add=None, out_dtype=None, out=None):
+    """sum over j of weights[t, j] * y[t, j] (+ add[t]) in float32, rounded
+    once: [tokens, N] of y [tokens, top_k, N] (float32 or bfloat16).
+
+    weights: float32 [tokens, top_k]; experts: int32 [tokens, top_k], rows of
+    negative ones are not read.  add: [tokens, N] of the result's type.
+    out_dtype: y's by default.  out: a tensor to write into; it may be add, and
+    must not overlap y."""
+    lib = L.load()
+    if not isinstance(y, torch.Tensor) or y.dim() != 3 or not y.is_cuda:
+        raise ValueError("y must be a [tokens, top_k, N] device tensor")
+    tokens, k, n = y.shape
+    dev = y.device
+    if y.stride(2) != 1 or (tokens > 1 and y.stride(0) != k * y.stride(1)) or (k > 1 and y.stride(1) < n):
+        y = y.contiguous()
+    ld_y = max(n, y.stride(1) if k > 1 else (y.stride(0) if tokens > 1 else n))
+    code = _dtype_code(y)
+    w = _given(weights, (tokens, k), torch.float32, dev, "weights")
+    if experts is not None:
+        _given(experts, (tokens, k), torch.int32, dev, "experts")
+    out, ld_out = _result(out, (tokens, n), out_dtype or y.dtype, dev)
+    ld_add = n
+    if add is not None:
+        add, ld_add = _rows(add, "add", dev, (out.dtype,))
+        if add.shape != (tokens, n):
+            raise ValueError("add must be [tokens, N]")
+    _launch(dev, lib.fp4q_combine_experts, y.data_ptr(), code, tokens, k, n, ld_y, w.data_ptr(), _ptr(experts),
+            _ptr(add), ld_add, _dtype_code(out), out.data_ptr(), ld_out)
+    return out
+
+
+def lora_add(y, x, a, b, groups, *, scales=None, out=None, ws=None, check=False):
+    """y + scales[g] * (x @ a[g]^T) @ b[g]^T for the rows of each group g
+    (adapter), y for rows of none: what low-rank adapters of many requests add
+    to a shared projection's result.
+
+    y: [rows, N] float32 or bfloat16, the projection's result; x: [rows, K]
+    bfloat16, its input.  a: bfloat16 [groups, rank, K]; b: bfloat16 [groups,
+    N, rank]; K and rank multiples of 8, rank up to 256.  groups: RowGroups of
+    the rows (``group_rows`` of each row's adapter).  scales: float32 [groups]
+    (default 1).  out: a tensor of y's type to write into; y itself is allowed,
+    it must not overlap y otherwise.  x A^T is kept in float32.
+    ws: a workspace of ``fp4q_lora_add_workspace_bytes`` bytes (a fresh one by
+    default); calls that may overlap need one each.  check: synchronize and
+    raise on data errors."""
+    lib = L.load()
+    y, ld_y = _rows(y, "y")
+    dev = y.device
+    x, ld_x = _rows(x, "x", dev, (torch.bfloat16,))
+    rows, n = y.shape
+    if not isinstance(a, torch.Tensor) or not isinstance(b, torch.Tensor) or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [groups, rank, K], b [groups, N, rank]")
+    if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16:
+        raise ValueError("a and b must be bfloat16")
+    g, rank, k = a.shape
+    if x.shape != (rows, k) or b.shape != (g, n, rank):
+        raise ValueError("x must be [rows, K], a [groups, rank, K] and b [groups, N, rank]")
+    a, b = a.contiguous(), b.contiguous()
+    _same_device(dev, a=a, b=b, scales=scales)
+    packed, n_groups, entries = _groups_struct(groups, dev)
+    if n_groups != g or entries != rows:
+        raise ValueError(f"groups must have {g} groups and {rows} entries")
+    if scales is not None:
+        _given(scales, (g,), torch.float32, dev, "scales")
+    if out is None:
+        out, ld_out = _result(None, (rows, n), y.dtype, dev)
+    else:
+        out, ld_out = _result(out, (rows, n), y.dtype, dev)
+        if out.dtype != y.dtype:
+            raise ValueError("out must have y's type")
+    if x.data_ptr() % 16 or (rows > 1 and ld_x % 8):
+        x, ld_x = x.clone(memory_format=torch.contiguous_format), k
+    need = lib.fp4q_lora_add_workspace_bytes(rows, g, n, k, rank)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if ws is None else _ws(ws, dev)
+    _launch(dev, lib.fp4q_lora_add, y.data_ptr(), _dtype_code(y), ld_y, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(),
+            _ptr(scales), packed, n, k, rank, out.data_ptr(), ld_out, ws.data_ptr(), ws.numel())
+    if check:
+        _check_data(ws)
+    return out

@@ -1,4 +1,4 @@
-"""ctypes declarations of the fp4q C ABI (include/fp4q.h, include/fp4q_gemm.h, include/fp4q_kv.h)."""
+"""ctypes declarations of the fp4q C ABI (include/fp4q.h, fp4q_gemm.h, fp4q_kv.h and fp4q_grouped.h)."""
 
 import ctypes
 import os
@@ -26,6 +26,8 @@ DATA_BAD_PERM = 0x20
 DATA_BAD_POSITION = 0x40
 DATA_BAD_SLOT = 0x80
 DATA_BAD_TABLE = 0x100
+DATA_BAD_GROUP = 0x200
+SOFTMAX, SIGMOID = 0, 1
 
 EXPORTS = (
     "fp4q_version",
@@ -59,6 +61,18 @@ KV_EXPORTS = (
     "fp4q_attention_mxfp4_workspace_bytes",
 )
 
+# include/fp4q_grouped.h
+GROUPED_EXPORTS = (
+    "fp4q_group_rows",
+    "fp4q_group_rows_workspace_bytes",
+    "fp4q_route_experts",
+    "fp4q_route_experts_workspace_bytes",
+    "fp4q_gemm_mxfp4_grouped",
+    "fp4q_combine_experts",
+    "fp4q_lora_add",
+    "fp4q_lora_add_workspace_bytes",
+)
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -81,12 +95,27 @@ class HeadMapStruct(ctypes.Structure):
                 ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("hadamard_n", ctypes.c_int32)]
 
 
+class RowGroupsStruct(ctypes.Structure):
+    """fp4q_row_groups_t"""
+    _fields_ = [("offsets", _P), ("rows", _P), ("groups", _I64), ("entries", _I64)]
+
+
+class RouterStruct(ctypes.Structure):
+    """fp4q_router_t"""
+    _fields_ = [("score", ctypes.c_int32), ("bias", _P), ("top_k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 # The same structs packed to bytes, which a call takes as well: building a
 # ctypes struct costs several times more host time.
 KV_CACHE_PACK = struct.Struct("4Qq3i3q").pack
 HEAD_MAP_PACK = struct.Struct("Qd2Qq3i0q").pack
 
-_CACHE = _MAP = _P  # host pointers: bytes or byref(struct)
+ROW_GROUPS_PACK = struct.Struct("2Q2q").pack
+ROUTER_PACK = struct.Struct("i4xQ5if").pack
+
+_CACHE = _MAP = _GROUPS = _ROUTER = _P  # host pointers: bytes or byref(struct)
 
 _SIGNATURES = {
     "fp4q_version": (_I, []),
@@ -118,6 +147,15 @@ _SIGNATURES = {
     "fp4q_attention_mxfp4": (_I, [_CACHE, _P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _I64,
                                   ctypes.c_float, _I, _I64, _P, _P, _P, _SZ, _P]),
     "fp4q_attention_mxfp4_workspace_bytes": (_SZ, [_I64] * 8),
+    "fp4q_group_rows": (_I, [_P, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "fp4q_group_rows_workspace_bytes": (_SZ, [_I64] * 2),
+    "fp4q_route_experts": (_I, [_P, _I, _I64, _I64, _I64, _ROUTER, _P, _P, _P, _P, _P, _SZ, _P]),
+    "fp4q_route_experts_workspace_bytes": (_SZ, [_I64] * 3),
+    "fp4q_gemm_mxfp4_grouped": (_I, [_P, _P, _I64, _P, _P, _GROUPS, _I64, _I64, _I64, _I, _I, ctypes.c_float, _I, _P,
+                                     _I64, _P, _SZ, _P]),
+    "fp4q_combine_experts": (_I, [_P, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I, _P, _I64, _P]),
+    "fp4q_lora_add": (_I, [_P, _I, _I64, _P, _I64, _P, _P, _P, _GROUPS, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]),
+    "fp4q_lora_add_workspace_bytes": (_SZ, [_I64] * 5),
     "fp4q_gemm_nvfp4": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _I64, _P, _SZ, _P]),
 }
 

@@ -8,10 +8,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfp4q.so")
 SOURCES = [os.path.join(PKG, "csrc", name)
-           for name in ("fp4q.hip", "fp4q_gemm.hip", "fp4q_kv.hip", "fp4q_attn.hip")]
-HEADERS = [os.path.join(PKG, "csrc", "fp4q_device.h"), os.path.join(PKG, "csrc", "fp4q_kv_host.h"),
-           os.path.join(ROOT, "include", "fp4q.h"), os.path.join(ROOT, "include", "fp4q_gemm.h"),
-           os.path.join(ROOT, "include", "fp4q_kv.h")]
+           for name in ("fp4q.hip", "fp4q_gemm.hip", "fp4q_kv.hip", "fp4q_attn.hip", "fp4q_route.hip", "fp4q_grouped.hip",
+                        "fp4q_lora.hip")]
+HEADERS = ([os.path.join(PKG, "csrc", name)
+            for name in ("fp4q_device.h", "fp4q_mfma.h", "fp4q_kv_host.h", "fp4q_grouped_host.h",
+                         "fp4q_grouped_device.h")] +
+           [os.path.join(ROOT, "include", name)
+            for name in ("fp4q.h", "fp4q_gemm.h", "fp4q_kv.h", "fp4q_grouped.h")])
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,135 @@
+// Argument checks, sizes and index arithmetic of the grouped calls
+// (include/fp4q_grouped.h): plain C++ without HIP, so that a host program can
+// exercise them; the functions marked FP4Q_HD are the ones the kernels run.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#include "fp4q.h"
+#include "fp4q_grouped.h"
+#include "fp4q_kv_host.h"
+
+namespace fp4q {
+
+constexpr int64_t kMaxRowGroups = 2048;
+constexpr int64_t kMaxEntries = (int64_t)1 << 30;
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxTopK = 64;
+constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // workgroups of a launch: with 1024 threads each below 2^32 threads
+
+inline bool grouped_ws_ok(const void *ws, size_t bytes, size_t need) { return ws && bytes >= need && kv_aligned(ws, 16); }
+
+inline fp4q_status_t grouped_check(const fp4q_row_groups_t &g) {
+  if (g.groups < 1 || g.groups > kMaxRowGroups || g.entries < 0 || g.entries > kMaxEntries) return FP4Q_ERR_SHAPE;
+  if (!g.offsets || (g.entries && !g.rows)) return FP4Q_ERR_NULL;
+  if (!kv_aligned(g.offsets, 4) || !kv_aligned(g.rows, 4)) return FP4Q_ERR_ALIGN;
+  return FP4Q_OK;
+}
+
+// Rows of n elements of `size` bytes, ld apart: the last one ends before 2^62
+// bytes from the first.
+inline bool grouped_rows_ok(int64_t rows, int64_t n, int64_t ld, int64_t size) {
+  return n >= 0 && ld >= n && ((__int128)(rows > 0 ? rows - 1 : 0) * ld + n) * size < ((__int128)1 << 62);
+}
+
+// ---------------------------------------------------------------- tiles ----
+
+// Entries lo .. hi - 1 of a group as the kernels see them: its offsets cut to
+// the entries there are.
+struct GroupSpan {
+  int lo, hi;
+  bool bad;
+};
+FP4Q_HD GroupSpan group_span(int o0, int o1, int entries) {
+  GroupSpan s;
+  s.bad = o0 < 0 || o1 < o0 || o1 > entries;
+  s.lo = o0 < 0 ? 0 : (o0 > entries ? entries : o0);
+  s.hi = o1 > entries ? entries : o1;
+  if (s.hi < s.lo) s.hi = s.lo;
+  return s;
+}
+FP4Q_HD int span_tiles(int lo, int hi, int rows) { return (int)(((int64_t)hi - lo + rows - 1) / rows); }
+
+// Row tiles of that many rows that all groups have, at most: each has its
+// whole ones and one that is not full.
+inline int64_t most_tiles(int64_t entries, int64_t groups, int64_t rows) {
+  return entries / rows + (groups < entries ? groups : entries);
+}
+
+inline fp4q_status_t grouped_product_check(const fp4q_row_groups_t &g, int64_t a_rows, int64_t n, int64_t k,
+                                           int64_t gather, int gated, int64_t ldc, int64_t size) {
+  const int64_t most = (int64_t)1 << 31;
+  if (n < 0 || n >= most || k <= 0 || k % 32 || k >= most || (gated && n % 2)) return FP4Q_ERR_SHAPE;
+  if (a_rows < 0 || a_rows >= most || gather < 0 || gather >= most) return FP4Q_ERR_SHAPE;
+  if (gather ? a_rows < (g.entries + gather - 1) / gather : a_rows < g.entries) return FP4Q_ERR_SHAPE;
+  if (!grouped_rows_ok(g.entries, gated ? n / 2 : n, ldc, size)) return FP4Q_ERR_SHAPE;
+  if ((__int128)g.groups * n * (k / 2) >= ((__int128)1 << 62)) return FP4Q_ERR_SHAPE;
+  return FP4Q_OK;
+}
+
+// --------------------------------------------------------------- routing ----
+
+inline fp4q_status_t router_check(const fp4q_router_t &r, int64_t experts) {
+  if (r.score != FP4Q_SOFTMAX && r.score != FP4Q_SIGMOID) return FP4Q_ERR_ARG;
+  if (r.renormalize != 0 && r.renormalize != 1) return FP4Q_ERR_ARG;
+  if (r.group_best != 1 && r.group_best != 2) return FP4Q_ERR_ARG;
+  if (!(fabsf(r.scale) <= 3.4028234e38f)) return FP4Q_ERR_ARG;
+  if (experts < 1 || experts > kMaxExperts) return FP4Q_ERR_SHAPE;
+  if (r.top_k < 1 || r.top_k > kMaxTopK || r.top_k > experts) return FP4Q_ERR_SHAPE;
+  if (r.n_groups < 1 || r.n_groups > 64 || experts % r.n_groups || r.top_groups < 1 || r.top_groups > r.n_groups)
+    return FP4Q_ERR_SHAPE;
+  if (!kv_aligned(r.bias, 4)) return FP4Q_ERR_ALIGN;
+  return FP4Q_OK;
+}
+
+constexpr int kSortChunk = 1024;  // entries that a workgroup places at a time
+constexpr int kSoloTokens = 64;   // up to which one workgroup routes and sorts
+
+// How entries are counted and placed.  Counting block b holds the units
+// (tokens, or entries of ids) [b per, (b + 1) per); placing block p holds
+// `join` counting blocks.
+struct SortPlan {
+  int64_t per, blocks;   // units of a counting block, counting blocks
+  int64_t join, places;  // counting blocks of a placing block, placing blocks
+};
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline SortPlan sort_plan(int64_t units, int64_t per_unit, int64_t least) {
+  SortPlan p;
+  p.per = ceil_div(units, 512);
+  if (p.per < least) p.per = least;
+  p.blocks = ceil_div(units, p.per);
+  p.join = kSortChunk / (p.per * per_unit);
+  if (p.join < 1) p.join = 1;
+  p.places = ceil_div(p.blocks, p.join);
+  return p;
+}
+inline size_t sort_bytes(const SortPlan &p, int64_t groups) { return 256 + (size_t)(p.blocks * (groups + 1) * 4); }
+
+// -------------------------------------------------------------- adapters ----
+
+inline fp4q_status_t lora_check_sizes(int64_t entries, int64_t groups, int64_t n, int64_t k, int64_t rank) {
+  const int64_t most = (int64_t)1 << 31;
+  if (entries < 0 || entries > kMaxEntries || groups < 1 || groups > kMaxRowGroups) return FP4Q_ERR_SHAPE;
+  if (n < 0 || n >= most || k < 8 || k >= most || k % 8 || rank < 8 || rank > 256 || rank % 8) return FP4Q_ERR_SHAPE;
+  return FP4Q_OK;
+}
+
+// few: row tiles of 16, and x A^T split over a workgroup's waves; else row tiles of 64.  splits: of K, over workgroups.
+struct LoraPlan {
+  bool few;
+  int64_t splits;
+};
+inline LoraPlan lora_plan(int64_t entries, int64_t groups, int64_t k) {
+  LoraPlan p;
+  p.few = entries < 64 * groups || entries <= 256;
+  const int64_t tiles = most_tiles(entries, groups, p.few ? 16 : 64);
+  const int64_t steps = ceil_div(k, 32) / (p.few ? 16 : 8);  // at least four steps a wave
+  p.splits = tiles ? 512 / tiles : 1;
+  if (p.splits > steps) p.splits = steps;
+  if (p.splits > 8) p.splits = 8;
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+}  // namespace fp4q

@@ -22,7 +22,8 @@ ScaleSweep, MXFP4 exponent sweep, dequantization), ``hadamard`` (block
 rotation), ``study`` (float64 exhaustive sweeps that pin the lemmas),
 ``focus`` (FOCUS forward quantizer), ``gptq`` (GPTQ with sweep-chosen group
 scales), ``gemm`` (W4A4 products in float64), ``kv`` (key/value cache: rotation,
-append, read, attention in float64).  Import them directly.
+append, read, attention in float64), ``grouped`` (routing to experts, grouped
+products, adapters in float64).  Import them directly.
 
 Parity-unpinned (no value on the pages fixes them): the FP32 evaluation
 order of the per-candidate loss and the reciprocal-multiply form

@@ -27,6 +27,7 @@ struct GroupedArgs {
   Groups groups;
   int a_rows, gather, scatter;
   int n, k, n_out, tiles_n;  // n_out: columns of C
+  int run;                   // tiles in a row that go to one XCD
   float alpha;
   void *c;
   int64_t ldc;
@@ -38,11 +39,12 @@ __device__ __forceinline__ int a_row(const GroupedArgs &a, int p, int e) {
   return a.gather ? (e < 0 ? 0 : e / a.gather) : p;
 }
 
-__device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
+// z / (1 + exp(-z)), the reciprocal by the hardware's (off by one unit at most)
+__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // Any k that is a multiple of 32: 64 rows times 128 rows of B (gated: 64 gates and their 64 ups), registers to a
 // padded LDS double buffer, 128 elements of K a stage, the tail filled with zeros.
-constexpr int kAnyRows = 64, kAnyCols = 128, kAnyThreads = 256, kAnyRowBytes = 80;
+constexpr int kAnyThreads = 256, kAnyRowBytes = 80;
 
 template <typename OutT, bool GATED>
 __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a) {
@@ -154,6 +156,363 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
   Status{a.status, true}.finish(err);
 }
 
+// ---------------------------------------------------------------------------
+// K a multiple of 128: operands move from global memory straight into an LDS ring of NS stages of ROWB code bytes of
+// every row, as in the plain product (fp4q_gemm.hip): one wave computes TM x TN blocks of 32 x 32, WGM x WGN waves a
+// tile; rows are unpadded and swizzled; K step ks takes, in lane half h, the 32-element block h KS + ks of the stage,
+// so that a lane's scale bytes of a stage are one word, of which the instruction selects byte ks.  What differs is
+// where rows come from: a lane loads the entry numbers of the rows that it stages once, before the loop.
+//
+// Gated: block column j of a wave is gates for even j and the ups of the same columns for odd j, so that both meet in
+// a lane's registers.
+//
+// Tiles of one group are taken together, up to kTileGroup row tiles column by column, and runs of `run` tiles go to
+// one XCD (workgroups are dealt round robin over the eight), so that what shares rows or a matrix shares an L2.
+constexpr int kTileGroup = 8;
+
+__device__ __forceinline__ int tile_number(const GroupedArgs &a) {
+  const int local = (int)blockIdx.x / kXcdCount;
+  return (local / a.run * kXcdCount + (int)blockIdx.x % kXcdCount) * a.run + local % a.run;
+}
+// Positions [lo, hi) and column tile of tile number lin, one of group g.
+struct GroupTile {
+  int lo, hi, col;
+};
+__device__ __forceinline__ GroupTile group_tile(const GroupedArgs &a, const TileGroup &g, int rows, int lin) {
+  const int within = lin - g.first * a.tiles_n, chunk = within / (kTileGroup * a.tiles_n);
+  const int left = span_tiles(g.lo, g.hi, rows) - chunk * kTileGroup, deep = left < kTileGroup ? left : kTileGroup;
+  const int r = within - chunk * kTileGroup * a.tiles_n;
+  const int lo = g.lo + (chunk * kTileGroup + r % deep) * rows;
+  return GroupTile{lo, g.hi - lo > rows ? lo + rows : g.hi, r / deep};
+}
+
+template <int ROWB, typename OutT, bool GATED, int WGM, int WGN, int TM, int TN, int NS>
+struct RingShape {
+  static constexpr int WAVES = WGM * WGN, THREADS = 64 * WAVES;
+  static constexpr int BM = WGM * TM * 32, BN = WGN * TN * 32;   // rows of A and of B
+  static constexpr int COLS = GATED ? BN / 2 : BN;               // columns of C
+  static constexpr int CPR = ROWB / 16, KS = ROWB / 32, SPR = ROWB / 16;
+  static constexpr int A_BYTES = BM * ROWB, B_BYTES = BN * ROWB;
+  static constexpr int SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + BM * SPR;
+  static constexpr int STAGE = SB_OFF + BN * SPR;
+};
+
+template <int ROWB, typename OutT, bool GATED, int WGM, int WGN, int TM, int TN, int NS>
+__global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArgs a) {
+  using S = RingShape<ROWB, OutT, GATED, WGM, WGN, TM, TN, NS>;
+  constexpr int WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
+  constexpr int RPL = 1024 / ROWB;  // rows of a 1 KB load
+  constexpr int A_INSTR = BM / RPL / WAVES, B_INSTR = BN / RPL / WAVES;
+  constexpr int SA_INSTR = BM * SPR / 256, SB_INSTR = BN * SPR / 256, SQ = (SA_INSTR + SB_INSTR + WAVES - 1) / WAVES;
+  constexpr int DPR = SPR / 4, RPS = 256 / SPR;  // scale words of a row, rows of a scale load
+  static_assert(A_INSTR * WAVES * RPL == BM && B_INSTR * WAVES * RPL == BN, "code loads must divide evenly");
+  static_assert(SA_INSTR * 256 == BM * SPR && SB_INSTR * 256 == BN * SPR, "scale loads cover whole rows");
+  static_assert(!GATED || TN % 2 == 0, "gates and ups in pairs of block columns");
+  constexpr int LOADS = A_INSTR + B_INSTR + SQ;  // of a wave and stage; a wave without a scale load fills a spare slot
+  constexpr int SPARE = NS * STAGE;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + 256];
+  __shared__ int row_of[BM];  // row of C, -1: not stored
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  const int wm = wave / WGN, wn = wave % WGN, l32 = lane & 31, h = lane >> 5;
+  uint32_t err = 0;
+  if (blockIdx.x == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
+  const int lin = tile_number(a);
+  const TileGroup g = find_group(a.groups, BM, lin / a.tiles_n);
+  if (g.group < 0) {
+    Status{a.status, true}.finish(err);
+    return;
+  }
+  const GroupTile t = group_tile(a, g, BM, lin);
+  const int lo = t.lo, hi = t.hi, n0 = t.col * S::COLS;  // first column of C
+
+  const int64_t kb = a.k / 2, ksc = a.k / 32;
+  const int nst = a.k / (2 * ROWB);
+  const uint8_t *B = a.b + (int64_t)g.group * a.n * kb, *Bs = a.bs + (int64_t)g.group * a.n * ksc;
+  // row of A of tile row i (those past the tile repeat its last one: computed, never stored)
+  auto a_of = [&](int i) {
+    const int p = lo + i < hi ? lo + i : hi - 1;
+    return (int64_t)(a.gather ? a_row(a, p, entry_at(a.groups, p)) : p);
+  };
+  auto b_of = [&](int i) {
+    const int col = GATED ? (i / 64) * 32 + (i & 31) : i;
+    return (int64_t)((n0 + col < a.n_out ? n0 + col : a.n_out - 1) + (GATED && (i & 32) ? a.n_out : 0));
+  };
+  for (int i = tid; i < BM; i += S::THREADS) {
+    const int e = lo + i < hi ? entry_at(a.groups, lo + i) : -1;
+    if (lo + i < hi && e < 0) err = FP4Q_DATA_BAD_GROUP;
+    row_of[i] = e < 0 ? -1 : (a.scatter ? e : lo + i);
+  }
+  const uint8_t *srcA[A_INSTR], *srcB[B_INSTR], *srcS[SQ];
+  int dstS[SQ];
+#pragma unroll
+  for (int i = 0; i < A_INSTR; ++i) {
+    const int row = (wave * A_INSTR + i) * RPL + lane / CPR;
+    srcA[i] = a.a + a_of(row) * kb + 16 * ((lane % CPR) ^ fp4q_gemm::swz<ROWB>(row));
+  }
+#pragma unroll
+  for (int i = 0; i < B_INSTR; ++i) {
+    const int row = (wave * B_INSTR + i) * RPL + lane / CPR;
+    srcB[i] = B + b_of(row) * kb + 16 * ((lane % CPR) ^ fp4q_gemm::swz<ROWB>(row));
+  }
+#pragma unroll
+  for (int j = 0; j < SQ; ++j) {
+    const int q = wave + WAVES * j, rl = lane / DPR, dw = lane % DPR;
+    if (q < SA_INSTR) {
+      srcS[j] = a.as + a_of(RPS * q + rl) * ksc + 4 * dw;
+      dstS[j] = S::SA_OFF + 256 * q;
+    } else if (q < SA_INSTR + SB_INSTR) {
+      srcS[j] = Bs + b_of(RPS * (q - SA_INSTR) + rl) * ksc + 4 * dw;
+      dstS[j] = S::SB_OFF + 256 * (q - SA_INSTR);
+    } else {
+      srcS[j] = Bs + 4 * dw;
+      dstS[j] = -1;
+    }
+  }
+  auto issue = [&](int st, int slot) {
+    uint8_t *base = smem + slot * STAGE;
+#pragma unroll
+    for (int i = 0; i < A_INSTR; ++i)
+      fp4q_gemm::load_lds16(srcA[i] + (int64_t)st * ROWB, base + (wave * A_INSTR + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < B_INSTR; ++i)
+      fp4q_gemm::load_lds16(srcB[i] + (int64_t)st * ROWB, base + S::A_BYTES + (wave * B_INSTR + i) * 1024);
+#pragma unroll
+    for (int j = 0; j < SQ; ++j)
+      fp4q_gemm::load_lds4(srcS[j] + (int64_t)st * SPR, dstS[j] >= 0 ? base + dstS[j] : smem + SPARE);
+  };
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{0};
+  struct Ops {
+    i32x8 a[TM], b[TN];
+    int sa[TM], sb[TN];
+  };
+  auto scale_word = [&](const uint8_t *p) {
+    if constexpr (SPR == 8) return (int)*reinterpret_cast<const uint32_t *>(p + 4 * h);
+    else return (int)*reinterpret_cast<const uint16_t *>(p + 2 * h);
+  };
+  const int lane_sw = fp4q_gemm::swz<ROWB>(l32);  // of every row a lane reads: they differ by multiples of 32
+  auto read_ops = [&](int slot, auto ks_c, Ops &o, const Ops &prev) {
+    constexpr int ks = decltype(ks_c)::value;
+    const uint8_t *base = smem + slot * STAGE;
+    const uint8_t *at = base + l32 * ROWB + 16 * ((h * KS + ks) ^ lane_sw);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(at + (wm * TM + i) * 32 * ROWB);
+      o.a[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      o.sa[i] = ks == 0 ? scale_word(base + S::SA_OFF + SPR * ((wm * TM + i) * 32 + l32)) : prev.sa[i];
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(at + S::A_BYTES + (wn * TN + j) * 32 * ROWB);
+      o.b[j] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      o.sb[j] = ks == 0 ? scale_word(base + S::SB_OFF + SPR * ((wn * TN + j) * 32 + l32)) : prev.sb[j];
+    }
+  };
+  auto mfmas = [&](const Ops &o, auto ks_c) {
+    constexpr int ks = decltype(ks_c)::value;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(o.a[i], o.b[j], acc[i][j], 4, 4, ks, o.sa[i], ks,
+                                                                    o.sb[j]);
+  };
+  const bool live = lo + wm * TM * 32 < hi;  // whether any of this wave's rows is there
+  auto stage_barrier = [&]() {  // keeps LDS accesses on their side, without draining the loads in flight
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  };
+
+  // Stage s sits in slot s % NS; once every wave has read all of it, stage s + NS is issued into its slot (past the
+  // last one the last is loaded again, so that every wait is one constant).
+#pragma unroll
+  for (int s = 0; s < NS; ++s) issue(s < nst ? s : nst - 1, s);
+  fp4q_gemm::wait_lgkmcnt0();  // row_of is written
+  fp4q_gemm::wait_vmcnt<(NS - 1) * LOADS>();
+  stage_barrier();
+  Ops o0, o1;
+  int slot = 0;
+  if (live) read_ops(0, std::integral_constant<int, 0>{}, o0, o1);
+  for (int st = 0; st < nst; ++st) {
+    if (live) {
+      fp4q_gemm::unroll(std::make_integer_sequence<int, KS - 1>{}, [&](auto ks_c) {
+        constexpr int ks = decltype(ks_c)::value;
+        if constexpr (ks % 2 == 0) {
+          read_ops(slot, std::integral_constant<int, ks + 1>{}, o1, o0);
+          mfmas(o0, ks_c);
+        } else {
+          read_ops(slot, std::integral_constant<int, ks + 1>{}, o0, o1);
+          mfmas(o1, ks_c);
+        }
+      });
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fp4q_gemm::wait_lgkmcnt0();                 // this wave's reads of stage st are complete
+    fp4q_gemm::wait_vmcnt<(NS - 2) * LOADS>();  // stage st + 1 has landed
+    stage_barrier();                            // ... for every wave, and nobody reads stage st any more
+    const int next = slot == NS - 1 ? 0 : slot + 1;
+    issue(st + NS < nst ? st + NS : nst - 1, slot);
+    if (live) {
+      read_ops(next, std::integral_constant<int, 0>{}, o0, o1);
+      __builtin_amdgcn_sched_barrier(0);
+      mfmas(o1, std::integral_constant<int, KS - 1>{});
+    }
+    slot = next;
+  }
+  __syncthreads();  // every load has landed, every wave is done reading the ring
+
+  // Each wave writes 32 rows of its columns at a time into its own area (padded by 16 bytes a row) and stores them in
+  // pieces of 16 bytes along the rows of C.
+  constexpr int WCOLS = S::COLS / WGN, VEC = 16 / (int)sizeof(OutT), EROW = WCOLS + VEC;
+  constexpr int LPR = WCOLS / VEC, RPI = 64 / LPR;
+  static_assert(WAVES * 32 * EROW * (int)sizeof(OutT) <= NS * STAGE, "epilogue staging must fit in the ring");
+  OutT *area = reinterpret_cast<OutT *>(smem) + wave * 32 * EROW;
+  OutT *C = (OutT *)a.c;
+  const bool wide = ((uintptr_t)C % 16 == 0) && ((a.ldc * (int64_t)sizeof(OutT)) % 16 == 0);
+  const float alpha = a.alpha;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    constexpr int JS = GATED ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < TN; j += JS)
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        float z0 = alpha * acc[i][j][v], z1 = alpha * acc[i][j][v + 1];
+        if constexpr (GATED) {
+          z0 = silu(z0) * (alpha * acc[i][j + 1][v]);
+          z1 = silu(z1) * (alpha * acc[i][j + 1][v + 1]);
+        }
+        OutT *o = area + (8 * (v >> 2) + 4 * h + (v & 3)) * EROW + j / JS * 32 + l32;  // rows r and r + 1
+        if constexpr (sizeof(OutT) == 4) {
+          o[0] = z0;
+          o[EROW] = z1;
+        } else {
+          const uint32_t p = fp4q_gemm::f32x2_to_bf16x2(z0, z1);
+          o[0] = (uint16_t)p;
+          o[EROW] = (uint16_t)(p >> 16);
+        }
+      }
+#pragma unroll
+    for (int q = 0; q < 32 / RPI; ++q) {
+      const int rr = q * RPI + lane / LPR, c = lane % LPR * VEC;
+      const int row = row_of[(wm * TM + i) * 32 + rr], col = n0 + wn * WCOLS + c;
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(area + rr * EROW + c);
+      if (row >= 0) {
+        OutT *dst = C + (int64_t)row * a.ldc + col;
+        if (wide && col + VEC <= a.n_out) {
+          *reinterpret_cast<i32x4 *>(dst) = v;
+        } else {
+          const OutT *e = reinterpret_cast<const OutT *>(&v);
+#pragma unroll
+          for (int t = 0; t < VEC; ++t)
+            if (col + t < a.n_out) dst[t] = e[t];
+        }
+      }
+    }
+  }
+  Status{a.status, true}.finish(err);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows a group (K a multiple of 128): 16 rows times 32 rows of B (gated: 16 gates and their 16 ups) a workgroup,
+// whose waves share K.  v_mfma_scale_f32_16x16x128_f8f6f4 takes from lane l row l % 16 and the 32 elements at
+// 32 (l / 16) of a step; register v of its accumulator holds row 4 (l / 16) + v, column l % 16.  A wave's codes come
+// straight to registers, kFewSteps steps of 128 elements at a time, all of them asked for before the first is used;
+// the matrix is known before the rows are, so its loads go first.  The waves' sums meet in LDS and are added in order.
+constexpr int kFewSteps = 4, kFewWaves = 8;
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+template <typename OutT, bool GATED>
+__global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs a) {
+  __shared__ f32x4v part[kFewWaves][2][64];
+  const int lane = threadIdx.x & 63, wave = wave_index(), r16 = lane & 15, h = lane >> 4;
+  uint32_t err = 0;
+  if (blockIdx.x == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
+  const int lin = tile_number(a);
+  const TileGroup g = find_group(a.groups, kFewRows16, lin / a.tiles_n);
+  if (g.group < 0) {
+    Status{a.status, true}.finish(err);
+    return;
+  }
+  const GroupTile t = group_tile(a, g, kFewRows16, lin);
+  const int n0 = t.col * (GATED ? kFewCols / 2 : kFewCols);
+  const int64_t kb = a.k / 2, ksc = a.k / 32;
+  const int p = t.lo + r16 < t.hi ? t.lo + r16 : t.hi - 1;
+  const uint8_t *b[2], *bs[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int col = GATED ? n0 + r16 : n0 + 16 * j + r16;
+    const int64_t row = (int64_t)g.group * a.n + (col < a.n_out ? col : a.n_out - 1) + (GATED && j ? a.n_out : 0);
+    b[j] = a.b + row * kb + 16 * h;
+    bs[j] = a.bs + row * ksc;
+  }
+  const int nst = a.k / 128, per = (nst + kFewWaves - 1) / kFewWaves;
+  const int s0 = wave * per, s1 = s0 + per < nst ? s0 + per : nst;
+  f32x4v acc[2] = {f32x4v{0, 0, 0, 0}, f32x4v{0, 0, 0, 0}};
+  const int e = entry_at(a.groups, p);
+  const int64_t ar = a.gather ? a_row(a, p, e) : p;
+  const uint8_t *A = a.a + ar * kb + 16 * h, *As = a.as + ar * ksc;
+  for (int s = s0; s < s1; s += kFewSteps) {
+    i32x4 bc[2][kFewSteps], ac[kFewSteps];
+    uint32_t bw[2][kFewSteps], aw[kFewSteps];
+#pragma unroll
+    for (int q = 0; q < kFewSteps; ++q) {
+      const int st = s + q < s1 ? s + q : s1 - 1;  // past the wave's last step: loaded, and multiplied by zeros
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        bc[j][q] = *reinterpret_cast<const i32x4 *>(b[j] + 64 * (int64_t)st);
+        bw[j][q] = *reinterpret_cast<const uint32_t *>(bs[j] + 4 * (int64_t)st);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kFewSteps; ++q) {
+      const int st = s + q < s1 ? s + q : s1 - 1;
+      ac[q] = *reinterpret_cast<const i32x4 *>(A + 64 * (int64_t)st);
+      aw[q] = *reinterpret_cast<const uint32_t *>(As + 4 * (int64_t)st);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < kFewSteps; ++q) {
+      const bool in = s + q < s1;
+      const i32x8 av = {in ? ac[q][0] : 0, in ? ac[q][1] : 0, in ? ac[q][2] : 0, in ? ac[q][3] : 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const i32x8 bv = {bc[j][q][0], bc[j][q][1], bc[j][q][2], bc[j][q][3], 0, 0, 0, 0};
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[j], 4, 4, 0, (int)(aw[q] >> (8 * h)), 0,
+                                                                  (int)(bw[j][q] >> (8 * h)));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (wave < (GATED ? 1 : 2)) {
+    f32x4v sum[2];
+#pragma unroll
+    for (int j = 0; j < (GATED ? 2 : 1); ++j) {
+      sum[j] = part[0][GATED ? j : wave][lane];
+#pragma unroll
+      for (int w = 1; w < kFewWaves; ++w) sum[j] += part[w][GATED ? j : wave][lane];
+    }
+    const int col = GATED ? n0 + r16 : n0 + 16 * wave + r16;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int q = t.lo + 4 * h + v;
+      const int eq = q < t.hi ? entry_at(a.groups, q) : -1;
+      if (q < t.hi && eq < 0) err = FP4Q_DATA_BAD_GROUP;
+      float z = a.alpha * sum[0][v];
+      if constexpr (GATED) z = silu(z) * (a.alpha * sum[1][v]);
+      if (eq >= 0 && col < a.n_out) store_out((OutT *)a.c + (int64_t)(a.scatter ? eq : q) * a.ldc + col, z);
+    }
+  }
+  Status{a.status, true}.finish(err);
+}
+
 __global__ __launch_bounds__(64) void grouped_status_kernel(uint32_t *status) {
   if (threadIdx.x == 0) Status{status, true}.merge(0u);
 }
@@ -162,6 +521,31 @@ template <typename F>
 void with_type(fp4q_dtype_t t, F &&f) {
   if (t == FP4Q_BF16) f((uint16_t *)nullptr);
   else f((float *)nullptr);
+}
+
+// Launches a kernel; false where it has too many tiles.
+template <typename K>
+bool launch_tiles(K kernel, GroupedArgs &a, const ProductTiles &t, int threads, hipStream_t s) {
+  if (t.workgroups > kMaxTiles) return false;
+  a.tiles_n = (int)ceil_div(a.n, t.cols);
+  a.run = t.run;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)t.workgroups), dim3(threads), 0, s, a);
+  return true;
+}
+
+template <typename O, bool GATED>
+bool launch(GroupedArgs &a, hipStream_t s) {
+  const ProductTiles t = product_tiles(a.groups.entries, a.groups.groups, a.n, a.k);
+  auto go = [&](auto kernel, int threads) { return launch_tiles(kernel, a, t, threads, s); };
+  if (t.kind == kAnyTiles) return go(grouped_any_kernel<O, GATED>, kAnyThreads);
+  if (t.kind == kFewTiles) return go(grouped_few_kernel<O, GATED>, 64 * kFewWaves);
+  if (a.k % 256 == 0) {
+    if (t.rows == 256) return go(grouped_ring_kernel<128, O, GATED, 2, 4, 4, 2, 2>, 512);
+    if (t.rows == 128) return go(grouped_ring_kernel<128, O, GATED, 2, 2, 2, 2, 2>, 256);
+    return go(grouped_ring_kernel<128, O, GATED, 2, 2, 1, 2, 2>, 256);
+  }
+  if (t.rows == 128) return go(grouped_ring_kernel<64, O, GATED, 2, 2, 2, 2, 4>, 256);
+  return go(grouped_ring_kernel<64, O, GATED, 2, 2, 1, 2, 4>, 256);
 }
 
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
@@ -195,17 +579,14 @@ extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const u
   if (!kv_aligned(a_codes, 16) || !kv_aligned(b_codes, 16) || !kv_aligned(c, out_dtype == FP4Q_F32 ? 4 : 2))
     return FP4Q_ERR_ALIGN;
   if (k % 128 == 0 && (!kv_aligned(a_scales, 4) || !kv_aligned(b_scales, 4))) return FP4Q_ERR_ALIGN;
-  GroupedArgs a{a_codes, a_scales, b_codes, b_scales, groups_of(*groups), (int)a_rows, (int)gather, scatter, (int)n, (int)k, (int)(gated ? n / 2 : n), 0,
+  GroupedArgs a{a_codes, a_scales, b_codes, b_scales, groups_of(*groups), (int)a_rows, (int)gather, scatter, (int)n, (int)k, (int)(gated ? n / 2 : n), 0, 1,
                 alpha, c, ldc, status};
-  a.tiles_n = (int)ceil_div(n, kAnyCols);
-  const int64_t tiles = a.tiles_n * most_tiles(groups->entries, groups->groups, kAnyRows);
-  if (tiles > kMaxTiles) return FP4Q_ERR_SHAPE;
+  bool fits = true;
   with_type(out_dtype, [&](auto op) {
     using O = std::remove_pointer_t<decltype(op)>;
-    if (gated)
-      hipLaunchKernelGGL((grouped_any_kernel<O, true>), dim3((unsigned)tiles), dim3(kAnyThreads), 0, s, a);
-    else
-      hipLaunchKernelGGL((grouped_any_kernel<O, false>), dim3((unsigned)tiles), dim3(kAnyThreads), 0, s, a);
+    if (gated) fits = launch<O, true>(a, s);
+    else fits = launch<O, false>(a, s);
   });
+  if (!fits) return FP4Q_ERR_SHAPE;
   return hip_status();
 }

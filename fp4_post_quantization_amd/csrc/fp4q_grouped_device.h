@@ -33,12 +33,12 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// Row tile number `tile` (of `rows` rows): its group, and positions [lo, hi) in the groups' order.  Past the groups'
-// last one: group -1 and the tile's number among those that follow, in lo.
-struct RowTile {
-  int group, lo, hi;
+// The group that row tile number `tile` (of `rows` rows, group after group) belongs to: its positions [lo, hi) in the
+// groups' order, and the number of its first tile.  Past the last one group is -1 and first the number of all tiles.
+struct TileGroup {
+  int group, lo, hi, first;
 };
-__device__ __forceinline__ RowTile find_tile(const Groups &a, int rows, int tile) {
+__device__ __forceinline__ TileGroup find_group(const Groups &a, int rows, int tile) {
   const int lane = threadIdx.x & 63;
   int run = 0;
   for (int g0 = 0; g0 < a.groups; g0 += 64) {
@@ -50,13 +50,23 @@ __device__ __forceinline__ RowTile find_tile(const Groups &a, int rows, int tile
     const int all = __builtin_amdgcn_readlane(upto, 63);
     if (tile < run + all) {
       const int at = __ffsll((unsigned long long)__ballot(run + upto > tile)) - 1;
-      const int lo = __builtin_amdgcn_readlane(s.lo, at), hi = __builtin_amdgcn_readlane(s.hi, at);
-      const int first = lo + (tile - run - __builtin_amdgcn_readlane(upto - mine, at)) * rows;
-      return RowTile{g0 + at, first, hi - first > rows ? first + rows : hi};
+      return TileGroup{g0 + at, __builtin_amdgcn_readlane(s.lo, at), __builtin_amdgcn_readlane(s.hi, at),
+                       run + __builtin_amdgcn_readlane(upto - mine, at)};
     }
     run += all;
   }
-  return RowTile{-1, tile - run, 0};
+  return TileGroup{-1, 0, 0, run};
+}
+
+// The tile itself: positions [lo, hi).  Past the last one: group -1, and its number among those that follow in lo.
+struct RowTile {
+  int group, lo, hi;
+};
+__device__ __forceinline__ RowTile find_tile(const Groups &a, int rows, int tile) {
+  const TileGroup g = find_group(a, rows, tile);
+  if (g.group < 0) return RowTile{-1, tile - g.first, 0};
+  const int lo = g.lo + (tile - g.first) * rows;
+  return RowTile{g.group, lo, g.hi - lo > rows ? lo + rows : g.hi};
 }
 
 // Whether the groups' offsets are not what they should be (one wave).

@@ -68,6 +68,46 @@ inline fp4q_status_t grouped_product_check(const fp4q_row_groups_t &g, int64_t a
   return FP4Q_OK;
 }
 
+constexpr int kXcdCount = 8;
+constexpr int kAnyRows = 64, kAnyCols = 128;
+constexpr int kFewRows16 = 16, kFewCols = 32;
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The kernel of a grouped product, its tiles (rows of A times rows of B), and the tiles in a row that go to one XCD.
+enum ProductKind { kAnyTiles, kFewTiles, kRingTiles };
+struct ProductTiles {
+  ProductKind kind;
+  int rows, cols, run;
+  int64_t workgroups;
+};
+inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, int64_t k) {
+  ProductTiles t;
+  auto tiles = [&](int rows, int cols) { return most_tiles(entries, groups, rows) * ceil_div(n, cols); };
+  if (k % 128) {
+    t = ProductTiles{kAnyTiles, kAnyRows, kAnyCols, 1, tiles(kAnyRows, kAnyCols)};
+    return t;
+  }
+  const int64_t rows = entries / (groups < entries ? groups : (entries ? entries : 1));  // of a group, on average
+  // Measured, us, gate and up products of 4096 x 1536 unless said:
+  // few rows (16 x 32) where all of a call's tiles run at once, two a CU: one token of 8 experts 12.0, in tiles of 64 x
+  // 128 14.5; 16 tokens (3600 tiles) 71 and 53.
+  if (tiles(kFewRows16, kFewCols) <= 512) {
+    t = ProductTiles{kFewTiles, kFewRows16, kFewCols, 4, 0};
+  } else if (rows <= 64) {
+    // 64 rows up to 64 a group: 16 tokens of 128 experts 53, with 128 57; 64 tokens 92 and 103; 512 (32 rows) 113 and
+    // 118; 256 tokens of 8 experts on 3584 columns (64 rows) 22 and 25; 1500 tokens (94 rows) 158 and 150.
+    t = ProductTiles{kRingTiles, 64, 128, 4, 0};
+  } else if (rows >= 192 && k % 256 == 0 && tiles(256, 256) >= 768) {
+    // 256 x 256 needs rows to fill it, and three tiles a CU: 4096 tokens (256 rows) 237, with 128 262; 768 x 4096 186
+    // and 210; 2048 rows on 4096 x 4096 219 and 247; 512 rows on 14336 x 4096 (320 tiles) 282 and 265.
+    t = ProductTiles{kRingTiles, 256, 256, 16, 0};
+  } else {
+    t = ProductTiles{kRingTiles, 128, 128, 4, 0};
+  }
+  t.workgroups = ceil_div(tiles(t.rows, t.cols), t.run * kXcdCount) * t.run * kXcdCount;
+  return t;
+}
+
 // --------------------------------------------------------------- routing ----
 
 inline fp4q_status_t router_check(const fp4q_router_t &r, int64_t experts) {
@@ -84,7 +124,7 @@ inline fp4q_status_t router_check(const fp4q_router_t &r, int64_t experts) {
 }
 
 constexpr int kSortChunk = 1024;  // entries that a workgroup places at a time
-constexpr int kSoloTokens = 64;   // up to which one workgroup routes and sorts
+constexpr int kSoloTokens = 16;   // up to which one workgroup routes and sorts
 
 // How entries are counted and placed.  Counting block b holds the units
 // (tokens, or entries of ids) [b per, (b + 1) per); placing block p holds
@@ -93,18 +133,22 @@ struct SortPlan {
   int64_t per, blocks;   // units of a counting block, counting blocks
   int64_t join, places;  // counting blocks of a placing block, placing blocks
 };
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline SortPlan sort_plan(int64_t units, int64_t per_unit, int64_t least) {
   SortPlan p;
   p.per = ceil_div(units, 512);
   if (p.per < least) p.per = least;
+  if (p.per > 65535 / per_unit) p.per = 65535 / per_unit;  // counts are 16 bits
   p.blocks = ceil_div(units, p.per);
   p.join = kSortChunk / (p.per * per_unit);
   if (p.join < 1) p.join = 1;
   p.places = ceil_div(p.blocks, p.join);
   return p;
 }
-inline size_t sort_bytes(const SortPlan &p, int64_t groups) { return 256 + (size_t)(p.blocks * (groups + 1) * 4); }
+// 16-bit counts of a counting block: of the groups, then of the entries of no group, padded to 16 bytes.
+FP4Q_HD int sort_stride(int groups) { return (groups + 8) & ~7; }
+inline size_t sort_bytes(const SortPlan &p, int64_t groups) {
+  return 256 + (size_t)(p.blocks * sort_stride((int)groups) * 2);
+}
 
 // -------------------------------------------------------------- adapters ----
 
@@ -115,7 +159,8 @@ inline fp4q_status_t lora_check_sizes(int64_t entries, int64_t groups, int64_t n
   return FP4Q_OK;
 }
 
-// few: row tiles of 16, and x A^T split over a workgroup's waves; else row tiles of 64.  splits: of K, over workgroups.
+// few: B meets 16 rows at a time, else 64 (32 in float32 and for ranks beyond 128, which take twice the registers).
+// splits: of K, over workgroups.
 struct LoraPlan {
   bool few;
   int64_t splits;
@@ -123,13 +168,15 @@ struct LoraPlan {
 inline LoraPlan lora_plan(int64_t entries, int64_t groups, int64_t k) {
   LoraPlan p;
   p.few = entries < 64 * groups || entries <= 256;
-  const int64_t tiles = most_tiles(entries, groups, p.few ? 16 : 64);
-  const int64_t steps = ceil_div(k, 32) / (p.few ? 16 : 8);  // at least four steps a wave
-  p.splits = tiles ? 512 / tiles : 1;
+  const int64_t tiles = most_tiles(entries, groups, 16), steps = ceil_div(k, 32) / 16;  // at least two steps a wave
+  p.splits = tiles ? 256 / tiles : 1;
   if (p.splits > steps) p.splits = steps;
   if (p.splits > 8) p.splits = 8;
   if (p.splits < 1) p.splits = 1;
   return p;
+}
+inline int64_t lora_rows(const LoraPlan &p, int64_t rank, int64_t size) {
+  return p.few ? 16 : (size == 4 || rank > 128 ? 32 : 64);
 }
 
 }  // namespace fp4q

@@ -33,40 +33,59 @@ struct SortArgs {
   const int32_t *ids;
   int64_t entries;
   int groups;
-  const uint32_t *counts;  // [blocks][groups + 1], the last column entries of no group
+  const uint16_t *counts;  // [blocks][sort_stride(groups)]
   int blocks, join;
   int64_t per;             // entries of a counting block
   int32_t *offsets, *rows;
 };
 
-// LDS of a placing workgroup: 2 (groups + 1) bases and kSortWaves (groups + 1) 16-bit counts.
-size_t sort_lds(int64_t groups) { return (size_t)((groups + 1) * (8 + 2 * kSortWaves) + 64); }
+// LDS of a placing workgroup: two bases and a 16-bit count for each wave, of every column.
+size_t sort_lds(int64_t groups, int waves) { return (size_t)(sort_stride((int)groups) * (8 + 2 * waves)); }
 
 __device__ __forceinline__ int group_of(int32_t id, int groups) { return (uint32_t)id < (uint32_t)groups ? id : groups; }
 
 // Places the entries [begin, end).  SOLO: they are all there are, and are counted here.
-template <bool SOLO>
+template <bool SOLO, int WAVES>
 __device__ void place_entries(const SortArgs &a, int64_t begin, int64_t end, int first_block, uint8_t *lds) {
-  const int cols = a.groups + 1, tid = threadIdx.x, lane = tid & 63, wave = wave_index();
-  int *base0 = reinterpret_cast<int *>(lds), *base1 = base0 + cols;
-  uint16_t *cnt = reinterpret_cast<uint16_t *>(base1 + cols);  // [wave][cols]
+  constexpr int THREADS = 64 * WAVES;
+  const int cols = a.groups + 1, stride = sort_stride(a.groups), tid = threadIdx.x, lane = tid & 63;
+  const int wave = wave_index();
+  int *base0 = reinterpret_cast<int *>(lds), *base1 = base0 + stride;
+  uint16_t *cnt = reinterpret_cast<uint16_t *>(base1 + stride);  // [wave][stride]
   // base0: entries of the group in the blocks before; base1: in all
-  for (int e = tid; e < cols; e += kSortThreads) base0[e] = base1[e] = 0;
+  for (int e = tid; e < stride; e += THREADS) base0[e] = base1[e] = 0;
   __syncthreads();
   if constexpr (SOLO) {
-    for (int64_t i = begin + tid; i < end; i += kSortThreads) atomicAdd(&base1[group_of(a.ids[i], a.groups)], 1);
-  } else {
-    const int side = kSortThreads / cols > 0 ? kSortThreads / cols : 1;  // blocks read side by side
-    for (int q = tid; q < side * cols; q += kSortThreads) {
-      const int e = q % cols;
-      int before = 0, all = 0;
-      for (int b = q / cols; b < a.blocks; b += side) {
-        const int v = (int)a.counts[(int64_t)b * cols + e];
-        all += v;
-        before += b < first_block ? v : 0;
+    for (int64_t i = begin + tid; i < end; i += THREADS) atomicAdd(&base1[group_of(a.ids[i], a.groups)], 1);
+  } else {  // eight columns a thread, as many blocks side by side as there are threads for, four of them in flight
+    const int eights = stride / 8, side = THREADS / eights > 0 ? THREADS / eights : 1;
+    for (int q = tid; q < side * eights; q += THREADS) {
+      const int c = q % eights;
+      int before[8] = {}, all[8] = {};
+      for (int b0 = q / eights; b0 < a.blocks; b0 += 4 * side) {
+        u32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int b = b0 + i * side < a.blocks ? b0 + i * side : b0;
+          v[i] = *reinterpret_cast<const u32x4 *>(a.counts + (int64_t)b * stride + 8 * c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int b = b0 + i * side;
+          const int in = b < a.blocks, early = b < first_block;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int n = (int)(v[i][j / 2] >> (16 * (j % 2)) & 0xFFFFu);
+            all[j] += in ? n : 0;
+            before[j] += early ? n : 0;
+          }
+        }
       }
-      atomicAdd(&base0[e], before);
-      atomicAdd(&base1[e], all);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        atomicAdd(&base0[8 * c + j], before[j]);
+        atomicAdd(&base1[8 * c + j], all[j]);
+      }
     }
   }
   __syncthreads();
@@ -91,8 +110,8 @@ __device__ void place_entries(const SortArgs &a, int64_t begin, int64_t end, int
   }
   const int bits = 32 - __clz(a.groups);
   int *from = base0, *to = base1;
-  for (int64_t i0 = begin; i0 < end; i0 += kSortThreads) {
-    for (int q = tid; q < kSortWaves * cols; q += kSortThreads) cnt[q] = 0;
+  for (int64_t i0 = begin; i0 < end; i0 += THREADS) {
+    for (int q = tid; q < WAVES * stride / 8; q += THREADS) reinterpret_cast<u32x4 *>(cnt)[q] = u32x4{0, 0, 0, 0};
     __syncthreads();
     const int64_t i = i0 + tid;
     const bool in = i < end;
@@ -103,21 +122,21 @@ __device__ void place_entries(const SortArgs &a, int64_t begin, int64_t end, int
       same &= (g >> b) & 1 ? set : ~set;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (in && rank == 0) cnt[wave * cols + g] = (uint16_t)__popcll(same);
+    if (in && rank == 0) cnt[wave * stride + g] = (uint16_t)__popcll(same);
     __syncthreads();
-    for (int e = tid; e < cols; e += kSortThreads) {
+    for (int e = tid; e < cols; e += THREADS) {
       int run = 0;
 #pragma unroll
-      for (int w = 0; w < kSortWaves; ++w) {
-        const int v = cnt[w * cols + e];
-        cnt[w * cols + e] = (uint16_t)run;
+      for (int w = 0; w < WAVES; ++w) {
+        const int v = cnt[w * stride + e];
+        cnt[w * stride + e] = (uint16_t)run;
         run += v;
       }
       to[e] = from[e] + run;
     }
     __syncthreads();
     if (in) {
-      const int64_t at = (int64_t)from[g] + cnt[wave * cols + g] + rank;
+      const int64_t at = (int64_t)from[g] + cnt[wave * stride + g] + rank;
       if (at >= 0 && at < a.entries) a.rows[at] = (int32_t)i;
     }
     __syncthreads();
@@ -131,11 +150,11 @@ __global__ __launch_bounds__(kSortThreads) void place_kernel(SortArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int first = (int)blockIdx.x * a.join;
   const int64_t begin = first * a.per, want = begin + a.join * a.per;
-  place_entries<false>(a, begin, want < a.entries ? want : a.entries, first, lds);
+  place_entries<false, kSortWaves>(a, begin, want < a.entries ? want : a.entries, first, lds);
 }
 
 // Counts of the ids of a block; reports those past the last group.  solo: all of it by one workgroup.
-__global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a, uint32_t *counts, uint32_t *status) {
+__global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a, uint16_t *counts, uint32_t *status) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int *sum = reinterpret_cast<int *>(lds);
   const int cols = a.groups + 1;
@@ -149,7 +168,8 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a, uint32_
     atomicAdd(&sum[group_of(id, a.groups)], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < cols; e += kSortThreads) counts[(int64_t)blockIdx.x * cols + e] = (uint32_t)sum[e];
+  for (int e = threadIdx.x; e < sort_stride(a.groups); e += kSortThreads)
+    counts[(int64_t)blockIdx.x * sort_stride(a.groups) + e] = e < cols ? (uint16_t)sum[e] : 0;
   Status{status, true}.finish(err);
 }
 
@@ -159,7 +179,7 @@ __global__ __launch_bounds__(kSortThreads) void group_solo_kernel(SortArgs a, ui
   for (int64_t i = threadIdx.x; i < a.entries; i += kSortThreads)
     if (a.ids[i] >= a.groups) err = FP4Q_DATA_BAD_GROUP;
   Status{status, true}.finish(err);
-  place_entries<true>(a, 0, a.entries, 0, lds);
+  place_entries<true, kSortWaves>(a, 0, a.entries, 0, lds);
 }
 
 // ----------------------------------------------------------------- routing ----
@@ -171,7 +191,8 @@ struct RouteArgs {
   float scale;
   float *weights;
   int32_t *chosen;
-  uint32_t *counts, *status;
+  uint16_t *counts;
+  uint32_t *status;
 };
 
 __device__ __forceinline__ float widen1(uint16_t v) { return as_f((uint32_t)v << 16); }
@@ -184,10 +205,33 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float order_value(uint32_t key) { return as_f((key >> 31) ? key & 0x7FFFFFFFu : ~key); }
 
+// The value of a lane that is the same in all lanes' view (a scalar).
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return as_f((uint32_t)__builtin_amdgcn_readlane((int)as_u(v), lane));
+}
+
+// Sum over the wave, in every lane: rows of 16 by shifts, then across rows (lanes shifted in from outside read 0).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_sum_step(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  v = dpp_sum_step<0x111, 0xF>(v);
+  v = dpp_sum_step<0x112, 0xF>(v);
+  v = dpp_sum_step<0x114, 0xF>(v);
+  v = dpp_sum_step<0x118, 0xF>(v);
+  v = dpp_sum_step<0x142, 0xA>(v);
+  v = dpp_sum_step<0x143, 0xC>(v);
+  return lane_value(v, 63);
 }
 
 __device__ __forceinline__ void wave_fence() {
@@ -217,169 +261,176 @@ __device__ uint64_t kept_groups(const RouteArgs &a, const V *pick, int log, int 
   const V mine = a.group_best == 2 && b2 > none ? b1 + b2 : b1;
   int rank = 0;
   for (int h = 0; h < a.n_groups; ++h) {
-    const V v = __shfl(mine, h * lanes);
+    const V v = lane_value(mine, h * lanes);
     rank += v > mine || (v == mine && h < g);
   }
   return __ballot(part == 0 && g < a.n_groups && rank < a.top_groups);
 }
 
-// Routes the tokens [begin, end), one a wave at a time.  SCORED: experts are compared by scores in float64 (with a
-// bias, or the sum of a group's two best); else the logits order them.
-template <int J, typename T, bool SCORED, int WAVES>
-__device__ void route_tokens(const RouteArgs &a, int64_t begin, int64_t end, int *sum, uint8_t *lds_pick, uint32_t &err) {
-  using V = std::conditional_t<SCORED, double, float>;
-  const int lane = threadIdx.x & 63, wave = wave_index();
-  const T *logits = (const T *)a.logits;
-  const int e0 = lane * J;
-  V *pick_lds = reinterpret_cast<V *>(lds_pick) + wave * a.experts;
-  const bool grouped = a.n_groups > 1;
-  const int glog = 32 - __clz(a.n_groups - 1);
+// A lane's experts, what does not change from token to token.
+template <int J>
+struct LaneExperts {
   float bias[J];
-  int bit[J];
+  int bit[J];  // of the expert's group in kept_groups' result
   bool there[J];
+  int log;     // log2 of the groups, rounded up
+};
+
+// Routes token t by the wave.  SCORED: scores matter for the choice (with a bias, or for the sum of a group's two
+// best); else the logits order the experts.
+template <int J, typename T, bool SCORED>
+__device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, const float x[J], const LaneExperts<J> &my,
+                                            int lane, void *lds, int *sum, uint32_t &err) {
+  using V = std::conditional_t<SCORED, double, float>;
+  const float minus_inf = -__builtin_inff();
+  const int e0 = lane * J;
+  const bool biased = SCORED && a.bias;  // choices compare scores, not logits
+  bool bad = false;
+  uint32_t key[J], top = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    there[j] = e0 + j < a.experts;
-    bias[j] = SCORED && a.bias && there[j] ? a.bias[e0 + j] : 0.0f;
-    bit[j] = grouped && there[j] ? (e0 + j) / a.run << (6 - glog) : 0;
+    bad |= !(x[j] < __builtin_inff());
+    key[j] = x[j] > minus_inf ? order_key(x[j]) : 0u;
+    top = key[j] > top ? key[j] : top;
   }
-  const float minus_inf = -__builtin_inff();
-  for (int64_t t = begin + wave; t < end; t += WAVES) {
-    float x[J];
-    uint32_t key[J];
-    bool bad = false;
+  top = wave_max_u32(top);
+  const float most = order_value(top);
+  double total = 0.0;
+  V pick[J];
+  if constexpr (!SCORED) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      x[j] = there[j] ? widen1(logits[t * a.ld + e0 + j]) : minus_inf;
-      bad |= !(x[j] < __builtin_inff());
+    for (int j = 0; j < J; ++j) pick[j] = x[j];
+    if (a.score == FP4Q_SOFTMAX && !a.renormalize) {
+      // float32 exponentials: each is off by a few 2^-24 of itself, and by 2^-24 of its distance from the largest
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) part += key[j] ? __expf(x[j] - most) : 0.0f;
+      total = wave_sum((double)part);
     }
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      key[j] = x[j] > minus_inf ? order_key(x[j]) : 0u;
-      top = key[j] > top ? key[j] : top;
-    }
-    top = wave_max_u32(top);
-    const float most = order_value(top);
-    double score[SCORED ? J : 1], total = 0.0;
-    V pick[J];
-    if constexpr (SCORED) {
-      if (a.score == FP4Q_SOFTMAX) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          score[j] = key[j] ? exp((double)x[j] - (double)most) : 0.0;
-          total += score[j];
-        }
-        total = wave_sum(total);
-#pragma unroll
-        for (int j = 0; j < J; ++j) score[j] = total > 0.0 ? score[j] / total : 0.0;
-      } else {
-#pragma unroll
-        for (int j = 0; j < J; ++j) score[j] = key[j] ? 1.0 / (1.0 + exp(-(double)x[j])) : 0.0;
-      }
+  } else {
+    if (a.score == FP4Q_SOFTMAX) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const double v = score[j] + (double)bias[j];
-        bad |= key[j] && !(v < (double)__builtin_inff());
-        const bool off = !key[j] || !(v > (double)minus_inf);
-        pick[j] = off ? (double)minus_inf : v;
-        key[j] = off ? 0u : (a.bias ? order_key((float)v) : key[j]);
+        pick[j] = key[j] ? exp((double)x[j] - (double)most) : 0.0;
+        total += pick[j];
       }
+      total = wave_sum(total);
+      const double one = total > 0.0 ? 1.0 / total : 0.0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) pick[j] *= one;
     } else {
 #pragma unroll
-      for (int j = 0; j < J; ++j) pick[j] = x[j];
-      if (a.score == FP4Q_SOFTMAX && !a.renormalize) {
-        // float32 exponentials: each is off by a few 2^-24 of itself, and by 2^-24 of its distance from the largest
-        float part = 0.0f;
+      for (int j = 0; j < J; ++j) pick[j] = 1.0 / (1.0 + exp(-(double)x[j]));
+    }
 #pragma unroll
-        for (int j = 0; j < J; ++j) part += key[j] ? __expf(x[j] - most) : 0.0f;
-        total = wave_sum((double)part);
+    for (int j = 0; j < J; ++j) {
+      pick[j] += (V)my.bias[j];
+      bad |= key[j] && !(pick[j] < (V)__builtin_inff());
+      const bool off = !key[j] || !(pick[j] > (V)minus_inf);
+      pick[j] = off ? (V)minus_inf : pick[j];
+      key[j] = off ? 0u : (biased ? order_key((float)pick[j]) : key[j]);
+    }
+  }
+  const bool dropped = __ballot(bad) != 0;
+  if (dropped) err = FP4Q_DATA_NONFINITE_INPUT;
+  if (a.n_groups > 1) {
+    V *room = reinterpret_cast<V *>(lds);
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (my.there[j]) room[e0 + j] = pick[j];
+    wave_fence();
+    const uint64_t kept = kept_groups<V>(a, room, my.log, lane);
+#pragma unroll
+    for (int j = 0; j < J; ++j) key[j] = (kept >> my.bit[j]) & 1 ? key[j] : 0u;
+  }
+  int mine = -1;        // lane i: the token's i-th choice
+  uint32_t my_key = 0;  // and its key
+  for (int i = 0; i < a.k && !dropped; ++i) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int j = 1; j < J; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
       }
-    }
-    const bool dropped = __ballot(bad) != 0;
-    if (dropped) err = FP4Q_DATA_NONFINITE_INPUT;
-    if (grouped) {
-      wave_fence();
+    const uint32_t m = wave_max_u32(best);
+    if (m == 0) break;
+    const uint64_t ties = __ballot(best == m);
+    int from = __ffsll((unsigned long long)ties) - 1;
+    if constexpr (SCORED) {
+      if (biased) {
+        bool twice = false;
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (there[j]) pick_lds[e0 + j] = pick[j];
-      wave_fence();
-      const uint64_t kept = kept_groups<V>(a, pick_lds, glog, lane);
+        for (int j = 0; j < J; ++j) twice |= key[j] == m && at != j;
+        if ((ties & (ties - 1)) || __ballot(twice)) {  // float32 rounds some alike: float64 decides, then the lowest index
+          double high = (double)minus_inf;
 #pragma unroll
-      for (int j = 0; j < J; ++j) key[j] = (kept >> bit[j]) & 1 ? key[j] : 0u;
-    }
-    int my_e = -1;
-    double my_v = 0.0;  // the choice's logit, or its score
-    for (int i = 0; i < a.k && !dropped; ++i) {
-      uint32_t best = key[0];
-      int at = 0;
-#pragma unroll
-      for (int j = 1; j < J; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          at = j;
-        }
-      const uint32_t m = wave_max_u32(best);
-      if (m == 0) break;
-      const uint64_t ties = __ballot(best == m);
-      int from = __ffsll((unsigned long long)ties) - 1;
-      if constexpr (SCORED) {
-        if (a.bias) {
-          int equal = 0;
-#pragma unroll
-          for (int j = 0; j < J; ++j) equal += key[j] == m;
-          if ((ties & (ties - 1)) || __ballot(equal > 1)) {  // the float64 values decide, then the lowest index
-            double mine = (double)minus_inf;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-              if (key[j] == m && pick[j] > mine) {
-                mine = pick[j];
-                at = j;
-              }
-            double most_v = (double)minus_inf;
-            for (uint64_t rest = ties; rest; rest &= rest - 1) {
-              const int l = __ffsll((unsigned long long)rest) - 1;
-              const double v = __shfl(mine, l);
-              if (v > most_v) {
-                most_v = v;
-                from = l;
-              }
+          for (int j = 0; j < J; ++j)
+            if (key[j] == m && pick[j] > high) {
+              high = pick[j];
+              at = j;
+            }
+          double highest = (double)minus_inf;
+          for (uint64_t rest = ties; rest; rest &= rest - 1) {
+            const int l = __ffsll((unsigned long long)rest) - 1;
+            const double v = lane_value(high, l);
+            if (v > highest) {
+              highest = v;
+              from = l;
             }
           }
         }
       }
-      double v = 0.0;
+    }
+    const int e = __builtin_amdgcn_readlane(e0 + at, from);
+    mine = lane == i ? e : mine;
+    my_key = lane == i ? m : my_key;
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (at == j) v = SCORED ? score[SCORED ? j : 0] : (double)x[j];
-      const int e = __builtin_amdgcn_readlane(e0 + at, from);
-      v = __shfl(v, from);
-      if (lane == i) {
-        my_e = e;
-        my_v = v;
-      }
-#pragma unroll
-      for (int j = 0; j < J; ++j) key[j] = lane == from && at == j ? 0u : key[j];
-    }
-    double w = 0.0;
-    if (my_e >= 0) {
-      if constexpr (SCORED) w = my_v;
-      else if (a.score == FP4Q_SIGMOID) w = 1.0 / (1.0 + exp(-my_v));
-      else w = exp(my_v - (double)most) / (a.renormalize ? 1.0 : total);
-    }
-    if (a.renormalize) {
-      const double all = wave_sum(w);
-      w = all > 0.0 ? w / all : 0.0;
-    }
-    if (lane < a.k) {
-      a.weights[t * a.k + lane] = (float)(w * (double)a.scale);
-      a.chosen[t * a.k + lane] = my_e;
-      if (sum) atomicAdd(&sum[my_e < 0 ? a.experts : my_e], 1);
-    }
+    for (int j = 0; j < J; ++j) key[j] = lane == from && at == j ? 0u : key[j];
+  }
+  double w = 0.0;
+  if (mine >= 0) {
+    const double v = biased ? (double)widen1(((const T *)a.logits)[t * a.ld + mine]) : (double)order_value(my_key);
+    if (a.score == FP4Q_SIGMOID) w = 1.0 / (1.0 + exp(-v));
+    else w = exp(v - (double)most) / (a.renormalize ? 1.0 : total);
+  }
+  if (a.renormalize) {
+    const double all = wave_sum(w);
+    w = all > 0.0 ? w / all : 0.0;
+  }
+  if (lane < a.k) {
+    a.weights[t * a.k + lane] = (float)(w * (double)a.scale);
+    a.chosen[t * a.k + lane] = mine;
+    if (sum) atomicAdd(&sum[mine < 0 ? a.experts : mine], 1);
   }
 }
 
-constexpr int kRouteWaves = 4;
+// Routes the tokens [begin, end), one a wave at a time.
+template <int J, typename T, bool SCORED, int WAVES>
+__device__ void route_tokens(const RouteArgs &a, int64_t begin, int64_t end, int *sum, uint8_t *lds_pick, uint32_t &err) {
+  const int lane = threadIdx.x & 63, wave = wave_index();
+  const T *logits = (const T *)a.logits;
+  const int e0 = lane * J;
+  void *room = lds_pick + (size_t)wave * a.experts * (SCORED ? 8 : 4);
+  LaneExperts<J> my;
+  my.log = 32 - __clz(a.n_groups - 1);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    my.there[j] = e0 + j < a.experts;
+    my.bias[j] = SCORED && a.bias && my.there[j] ? a.bias[e0 + j] : 0.0f;
+    my.bit[j] = a.n_groups > 1 && my.there[j] ? (e0 + j) / a.run << (6 - my.log) : 0;
+  }
+  for (int64_t t = begin + wave; t < end; t += WAVES) {
+    float x[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) x[j] = my.there[j] ? widen1(logits[t * a.ld + e0 + j]) : -__builtin_inff();
+    route_token<J, T, SCORED>(a, t, x, my, lane, room, sum, err);
+  }
+}
+
+constexpr int kRouteWaves = 8;
 
 template <int J, typename T, bool SCORED>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
@@ -394,20 +445,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
                                           err);
   __syncthreads();
   if (a.counts)
-    for (int e = threadIdx.x; e < cols; e += 64 * kRouteWaves) a.counts[(int64_t)blockIdx.x * cols + e] = (uint32_t)sum[e];
+    for (int e = threadIdx.x; e < sort_stride(a.experts); e += 64 * kRouteWaves)
+      a.counts[(int64_t)blockIdx.x * sort_stride(a.experts) + e] = e < cols ? (uint16_t)sum[e] : 0;
   Status{a.status, true}.finish(err);
 }
 
 // One workgroup for all tokens, and their entries sorted behind.
 template <int J, typename T, bool SCORED>
-__global__ __launch_bounds__(kSortThreads) void route_solo_kernel(RouteArgs a, SortArgs s) {
+__global__ __launch_bounds__(64 * kRouteWaves) void route_solo_kernel(RouteArgs a, SortArgs s) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   uint32_t err = 0;
-  route_tokens<J, T, SCORED, kSortWaves>(a, 0, a.tokens, nullptr, lds, err);
+  route_tokens<J, T, SCORED, kRouteWaves>(a, 0, a.tokens, nullptr, lds, err);
   Status{a.status, true}.finish(err);
   if (!s.offsets) return;
   __syncthreads();
-  place_entries<true>(s, 0, s.entries, 0, lds);
+  place_entries<true, kRouteWaves>(s, 0, s.entries, 0, lds);
 }
 
 // ------------------------------------------------------------- weighted sum ----
@@ -545,16 +597,16 @@ extern "C" fp4q_status_t fp4q_group_rows(const int32_t *ids, int64_t entries, in
     hipLaunchKernelGGL(no_entries_kernel, dim3(1), dim3(kSortThreads), 0, s, offsets, (int)groups, status);
     return hip_status();
   }
-  uint32_t *counts = (uint32_t *)((char *)workspace + 256);
+  uint16_t *counts = (uint16_t *)((char *)workspace + 256);
   const SortPlan p = sort_plan(entries, 1, kSortChunk);
   const SortArgs a{ids, entries, (int)groups, counts, (int)p.blocks, (int)p.join, p.per, offsets, rows};
   if (solo_group(entries)) {
-    hipLaunchKernelGGL(group_solo_kernel, dim3(1), dim3(kSortThreads), sort_lds(groups), s, a, status);
+    hipLaunchKernelGGL(group_solo_kernel, dim3(1), dim3(kSortThreads), sort_lds(groups, kSortWaves), s, a, status);
     return hip_status();
   }
   hipLaunchKernelGGL(count_kernel, dim3((unsigned)p.blocks), dim3(kSortThreads), (size_t)(groups + 1) * 4, s, a, counts,
                      status);
-  hipLaunchKernelGGL(place_kernel, dim3((unsigned)p.places), dim3(kSortThreads), sort_lds(groups), s, a);
+  hipLaunchKernelGGL(place_kernel, dim3((unsigned)p.places), dim3(kSortThreads), sort_lds(groups, kSortWaves), s, a);
   return hip_status();
 }
 
@@ -590,7 +642,7 @@ extern "C" fp4q_status_t fp4q_route_experts(const void *logits, fp4q_dtype_t dty
   }
   const bool solo = solo_route(tokens, k);
   const SortPlan p = sort_plan(tokens, k, kRouteWaves);
-  uint32_t *counts = solo || !offsets ? nullptr : (uint32_t *)((char *)workspace + 256);
+  uint16_t *counts = solo || !offsets ? nullptr : (uint16_t *)((char *)workspace + 256);
   const RouteArgs a{logits, ld, tokens, p.per, (int)experts, (int)k, (int)router->score, router->n_groups,
                     (int)(experts / router->n_groups), router->top_groups, router->group_best, router->renormalize,
                     router->bias, router->scale, weights, chosen, counts, status};
@@ -604,8 +656,9 @@ extern "C" fp4q_status_t fp4q_route_experts(const void *logits, fp4q_dtype_t dty
       auto go = [&](auto sc) {
         constexpr bool SCORED = decltype(sc)::value;
         if (solo) {
-          const size_t need = sort_lds(experts), lds = pick * kSortWaves > need ? pick * kSortWaves : need;
-          hipLaunchKernelGGL((route_solo_kernel<J, T, SCORED>), dim3(1), dim3(kSortThreads), lds, s, a, e);
+          const size_t need = sort_lds(experts, kRouteWaves);
+          const size_t lds = pick * kRouteWaves > need ? pick * kRouteWaves : need;
+          hipLaunchKernelGGL((route_solo_kernel<J, T, SCORED>), dim3(1), dim3(64 * kRouteWaves), lds, s, a, e);
         } else {
           const size_t lds = (size_t)(experts + 4) / 4 * 16 + pick * kRouteWaves;
           hipLaunchKernelGGL((route_kernel<J, T, SCORED>), dim3((unsigned)p.blocks), dim3(64 * kRouteWaves), lds, s, a);
@@ -616,7 +669,7 @@ extern "C" fp4q_status_t fp4q_route_experts(const void *logits, fp4q_dtype_t dty
     });
   });
   if (counts)
-    hipLaunchKernelGGL(place_kernel, dim3((unsigned)p.places), dim3(kSortThreads), sort_lds(experts), s, e);
+    hipLaunchKernelGGL(place_kernel, dim3((unsigned)p.places), dim3(kSortThreads), sort_lds(experts, kSortWaves), s, e);
   return hip_status();
 }
 

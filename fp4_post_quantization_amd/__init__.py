@@ -23,6 +23,7 @@ HIP kernels.  There is no CPU fallback; a missing library raises.
     lora_add(y, x, a, b, groups, *, scales=None, ...)
 """
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -959,28 +960,62 @@ class ExpertRoute(NamedTuple):
 _SCORES = {"softmax": L.SOFTMAX, "sigmoid": L.SIGMOID}
 
 
-def _sized_ws(ws, device, need):
-    """The caller's workspace, the default one for a status word alone, or a
-    fresh one: calls captured into different graphs share the default one."""
-    if ws is None and need > 256:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    return _ws(ws, device)
+@functools.lru_cache(maxsize=4096)
+def _need(query, *sizes):
+    """A workspace query of the library, which depends on the sizes alone."""
+    return getattr(L.load(), query)(*sizes)
+
+
+def _room(ws, device, index, stream, need):
+    """The caller's workspace, the stream's default one for a status word
+    alone, or a fresh one (calls captured into different graphs share the
+    default one): its address, its bytes and the tensor."""
+    if ws is not None:
+        ws = _ws(ws, device)
+    elif need > 256:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        ws = _WORKSPACES.get((index, stream))
+        if ws is None:
+            ws = workspace(device)
+    return ws.data_ptr(), ws.numel(), ws
+
+
+def _index_of(device):
+    """The number of a tensor's device and the handle of its current stream."""
+    index = device.index
+    return index, (_RAW_STREAM(index) if _RAW_STREAM is not None else _stream(device))
+
+
+def _call(index, call, *args):
+    """call(*args) with the device current."""
+    if _GET_DEVICE() == index:
+        status = call(*args)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args)
+    if status:
+        L.check(status)
+
+
+_FLOATS = {torch.float32: L.F32, torch.bfloat16: L.BF16}
 
 
 def _groups_struct(groups, device):
     """fp4q_row_groups_t, packed, its groups and its entries."""
     offsets, rows = groups
-    for name, t in (("offsets", offsets), ("rows", rows)):
-        if (not isinstance(t, torch.Tensor) or t.dim() != 1 or t.dtype is not torch.int32 or t.device != device
-                or (t.size(0) > 1 and t.stride(0) != 1)):
+    for t in groups:
+        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.device != device
+                or not t.is_contiguous()):
+            name = "offsets" if t is offsets else "rows"
             raise ValueError(f"groups.{name} must be a contiguous int32 vector on {device}")
-    n, entries = offsets.size(0) - 1, rows.size(0)
+    n, entries = offsets.shape[0] - 1, rows.shape[0]
     if n < 1:
         raise ValueError("groups.offsets must have one entry more than there are groups")
     return L.ROW_GROUPS_PACK(offsets.data_ptr(), rows.data_ptr(), n, entries), n, entries
 
 
-def _rows(t, name, device=None, dtypes=(torch.float32, torch.bfloat16)):
+def _rows(t, name, device=None, dtypes=_FLOATS):
     """A [rows, columns] device tensor with dense rows that do not overlap,
     and their stride."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes:
@@ -991,18 +1026,15 @@ def _rows(t, name, device=None, dtypes=(torch.float32, torch.bfloat16)):
     s0, s1 = t.stride()
     if (s1 != 1 and cols > 1) or (rows > 1 and s0 < cols):
         t, s0 = t.contiguous(), cols
-    return t, max(s0, cols) if rows > 1 else cols
+    return t, s0 if rows > 1 and s0 > cols else cols
 
 
-def _result(out, shape, dtype, device):
-    """A fresh result, or the caller's, and the stride of its rows."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
-    if (not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype not in (torch.float32, torch.bfloat16)
-            or out.device != device or (out.stride(1) != 1 and shape[1] > 1)
-            or (shape[0] > 1 and out.stride(0) < shape[1])):
-        raise ValueError(f"out must be a row-major float32 or bfloat16 tensor of shape {tuple(shape)} on {device}")
-    return out, max(out.stride(0), shape[1]) if shape[0] > 1 else shape[1]
+def _result(out, rows, cols, device):
+    """The stride of the rows of a caller's result."""
+    if (not isinstance(out, torch.Tensor) or out.shape != (rows, cols) or out.dtype not in _FLOATS
+            or out.device != device or (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols)):
+        raise ValueError(f"out must be a row-major float32 or bfloat16 tensor of shape ({rows}, {cols}) on {device}")
+    return max(out.stride(0), cols) if rows > 1 else cols
 
 
 def group_rows(ids, n_groups, *, ws=None, check=False):
@@ -1022,9 +1054,10 @@ def group_rows(ids, n_groups, *, ws=None, check=False):
         raise ValueError("n_groups must be positive")
     offsets = torch.empty(n_groups + 1, dtype=torch.int32, device=dev)
     rows = torch.empty(entries, dtype=torch.int32, device=dev)
-    ws = _sized_ws(ws, dev, lib.fp4q_group_rows_workspace_bytes(entries, n_groups))
-    _launch(dev, lib.fp4q_group_rows, ids.data_ptr(), entries, n_groups, offsets.data_ptr(), rows.data_ptr(),
-            ws.data_ptr(), ws.numel())
+    index, stream = _index_of(dev)
+    at, size, ws = _room(ws, dev, index, stream, _need("fp4q_group_rows_workspace_bytes", entries, n_groups))
+    _call(index, lib.fp4q_group_rows, ids.data_ptr(), entries, n_groups, offsets.data_ptr(), rows.data_ptr(), at, size,
+          stream)
     if check:
         _check_data(ws)
     return RowGroups(offsets, rows)
@@ -1057,23 +1090,25 @@ def route_experts(logits, top_k, *, score="softmax", bias=None, n_groups=1, top_
         raise ValueError("top_k must be 1 to the number of experts")
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
+    bias_ptr = 0
     if bias is not None:
         if bias.dtype is not torch.float32 or bias.device != dev or not bias.is_contiguous():
             bias = bias.to(device=dev, dtype=torch.float32).contiguous()
         if bias.shape != (experts,):
             raise ValueError("bias must have one entry per expert")
-    router = L.ROUTER_PACK(_SCORES[score], _ptr(bias) or 0, top_k, int(n_groups), int(top_groups), int(group_best),
-                           bool(renormalize), scale)
-    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
-    chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-    groups = None
+        bias_ptr = bias.data_ptr()
+    router = L.ROUTER_PACK(_SCORES[score], bias_ptr, top_k, n_groups, top_groups, group_best, bool(renormalize), scale)
+    empty, i32 = torch.empty, torch.int32
+    weights = empty(tokens, top_k, dtype=torch.float32, device=dev)
+    chosen = empty(tokens, top_k, dtype=i32, device=dev)
+    groups = offsets_ptr = rows_ptr = None
     if group:
-        groups = RowGroups(torch.empty(experts + 1, dtype=torch.int32, device=dev),
-                           torch.empty(tokens * top_k, dtype=torch.int32, device=dev))
-    ws = _sized_ws(ws, dev, lib.fp4q_route_experts_workspace_bytes(tokens, experts, top_k))
-    _launch(dev, lib.fp4q_route_experts, logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, router,
-            weights.data_ptr(), chosen.data_ptr(), groups.offsets.data_ptr() if group else None,
-            groups.rows.data_ptr() if group else None, ws.data_ptr(), ws.numel())
+        offsets, rows = empty(experts + 1, dtype=i32, device=dev), empty(tokens * top_k, dtype=i32, device=dev)
+        groups, offsets_ptr, rows_ptr = RowGroups(offsets, rows), offsets.data_ptr(), rows.data_ptr()
+    index, stream = _index_of(dev)
+    at, size, ws = _room(ws, dev, index, stream, _need("fp4q_route_experts_workspace_bytes", tokens, experts, top_k))
+    _call(index, lib.fp4q_route_experts, logits.data_ptr(), _FLOATS[logits.dtype], tokens, experts, ld, router,
+          weights.data_ptr(), chosen.data_ptr(), offsets_ptr, rows_ptr, at, size, stream)
     if check:
         _check_data(ws)
     return ExpertRoute(weights, chosen, groups)
@@ -1097,27 +1132,35 @@ def gemm_mxfp4_grouped(a, b, groups, *, gather=0, scatter=False, gated=False, al
     lib = L.load()
     ac, as_ = (a.codes, a.scales) if isinstance(a, MXFP4Result) else a
     bc, bs = (b.codes, b.scales) if isinstance(b, MXFP4Result) else b
-    if ac.dim() != 2 or bc.dim() != 3 or as_.dim() != 2 or bs.dim() != 3:
+    if ac.dim() != 2 or bc.dim() != 3:
         raise ValueError("a must be [rows, K/2] codes, b [groups, N, K/2] codes, with their scales")
     m, kh = ac.shape
     g, n, kh2 = bc.shape
     if kh != kh2:
         raise ValueError(f"K mismatch: A has {2 * kh}, B has {2 * kh2}")
     dev = ac.device
-    ac, as_, bc, bs = (t.contiguous() for t in (ac, as_, bc, bs))
-    _same_device(dev, a_scales=as_, b_codes=bc, b_scales=bs)
-    if any(t.dtype is not torch.uint8 for t in (ac, as_, bc, bs)):
-        raise ValueError("codes and scales must be uint8")
     if as_.shape != (m, kh // 16) or bs.shape != (g, n, kh // 16):
         raise ValueError("scales must be rows x K/32")
+    u8 = torch.uint8
+    if not (ac.dtype is u8 and as_.dtype is u8 and bc.dtype is u8 and bs.dtype is u8):
+        raise ValueError("codes and scales must be uint8")
+    if not (ac.is_cuda and as_.device == dev and bc.device == dev and bs.device == dev):
+        _same_device(dev, a_scales=as_, b_codes=bc, b_scales=bs)
+    if not (ac.is_contiguous() and as_.is_contiguous() and bc.is_contiguous() and bs.is_contiguous()):
+        ac, as_, bc, bs = (t.contiguous() for t in (ac, as_, bc, bs))
     packed, n_groups, entries = _groups_struct(groups, dev)
     if n_groups != g:
         raise ValueError(f"groups has {n_groups} groups, b {g}")
-    out, ldc = _result(out, (entries, n // 2 if gated else n), out_dtype, dev)
-    ws = _ws(ws, dev)
-    _launch(dev, lib.fp4q_gemm_mxfp4_grouped, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(), bs.data_ptr(), packed,
-            n, 2 * kh, int(gather), bool(scatter), bool(gated), alpha, _dtype_code(out), out.data_ptr(), ldc,
-            ws.data_ptr(), ws.numel())
+    cols = n // 2 if gated else n
+    if out is None:
+        out, ldc = torch.empty(entries, cols, dtype=out_dtype, device=dev), cols
+        code = _dtype_code(out)
+    else:
+        ldc, code = _result(out, entries, cols, dev), _FLOATS[out.dtype]
+    index, stream = _index_of(dev)
+    at, size, ws = _room(ws, dev, index, stream, 0)
+    _call(index, lib.fp4q_gemm_mxfp4_grouped, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(), bs.data_ptr(), packed, n,
+          2 * kh, gather, bool(scatter), bool(gated), alpha, code, out.data_ptr(), ldc, at, size, stream)
     if check:
         _check_data(ws)
     return out
@@ -1136,21 +1179,31 @@ def combine_experts(y, weights, experts=None, *, add=None, out_dtype=None, out=N
         raise ValueError("y must be a [tokens, top_k, N] device tensor")
     tokens, k, n = y.shape
     dev = y.device
-    if y.stride(2) != 1 or (tokens > 1 and y.stride(0) != k * y.stride(1)) or (k > 1 and y.stride(1) < n):
-        y = y.contiguous()
-    ld_y = max(n, y.stride(1) if k > 1 else (y.stride(0) if tokens > 1 else n))
+    ld_y = n
+    if not y.is_contiguous():
+        s0, s1, s2 = y.stride()
+        if (s2 != 1 and n > 1) or (tokens > 1 and k > 1 and s0 != k * s1) or (k > 1 and s1 < n) or (tokens > 1 and s0 < n):
+            y = y.contiguous()
+        else:
+            ld_y = s1 if k > 1 else s0
     code = _dtype_code(y)
-    w = _given(weights, (tokens, k), torch.float32, dev, "weights")
+    _given(weights, (tokens, k), torch.float32, dev, "weights")
     if experts is not None:
         _given(experts, (tokens, k), torch.int32, dev, "experts")
-    out, ld_out = _result(out, (tokens, n), out_dtype or y.dtype, dev)
-    ld_add = n
+    if out is None:
+        out, ld_out = torch.empty(tokens, n, dtype=out_dtype or y.dtype, device=dev), n
+        out_code = _dtype_code(out)
+    else:
+        ld_out, out_code = _result(out, tokens, n, dev), _FLOATS[out.dtype]
+    add_ptr, ld_add = None, n
     if add is not None:
         add, ld_add = _rows(add, "add", dev, (out.dtype,))
         if add.shape != (tokens, n):
             raise ValueError("add must be [tokens, N]")
-    _launch(dev, lib.fp4q_combine_experts, y.data_ptr(), code, tokens, k, n, ld_y, w.data_ptr(), _ptr(experts),
-            _ptr(add), ld_add, _dtype_code(out), out.data_ptr(), ld_out)
+        add_ptr = add.data_ptr()
+    index, stream = _index_of(dev)
+    _call(index, lib.fp4q_combine_experts, y.data_ptr(), code, tokens, k, n, ld_y, weights.data_ptr(),
+          None if experts is None else experts.data_ptr(), add_ptr, ld_add, out_code, out.data_ptr(), ld_out, stream)
     return out
 
 
@@ -1180,25 +1233,28 @@ def lora_add(y, x, a, b, groups, *, scales=None, out=None, ws=None, check=False)
     g, rank, k = a.shape
     if x.shape != (rows, k) or b.shape != (g, n, rank):
         raise ValueError("x must be [rows, K], a [groups, rank, K] and b [groups, N, rank]")
-    a, b = a.contiguous(), b.contiguous()
-    _same_device(dev, a=a, b=b, scales=scales)
+    if a.device != dev or b.device != dev:
+        _same_device(dev, a=a, b=b)
+    if not (a.is_contiguous() and b.is_contiguous()):
+        a, b = a.contiguous(), b.contiguous()
     packed, n_groups, entries = _groups_struct(groups, dev)
     if n_groups != g or entries != rows:
         raise ValueError(f"groups must have {g} groups and {rows} entries")
+    scales_ptr = None
     if scales is not None:
-        _given(scales, (g,), torch.float32, dev, "scales")
+        scales_ptr = _given(scales, (g,), torch.float32, dev, "scales").data_ptr()
     if out is None:
-        out, ld_out = _result(None, (rows, n), y.dtype, dev)
+        out, ld_out = torch.empty(rows, n, dtype=y.dtype, device=dev), n
     else:
-        out, ld_out = _result(out, (rows, n), y.dtype, dev)
+        ld_out = _result(out, rows, n, dev)
         if out.dtype != y.dtype:
             raise ValueError("out must have y's type")
     if x.data_ptr() % 16 or (rows > 1 and ld_x % 8):
         x, ld_x = x.clone(memory_format=torch.contiguous_format), k
-    need = lib.fp4q_lora_add_workspace_bytes(rows, g, n, k, rank)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev) if ws is None else _ws(ws, dev)
-    _launch(dev, lib.fp4q_lora_add, y.data_ptr(), _dtype_code(y), ld_y, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(),
-            _ptr(scales), packed, n, k, rank, out.data_ptr(), ld_out, ws.data_ptr(), ws.numel())
+    index, stream = _index_of(dev)
+    at, size, ws = _room(ws, dev, index, stream, _need("fp4q_lora_add_workspace_bytes", rows, g, n, k, rank))
+    _call(index, lib.fp4q_lora_add, y.data_ptr(), _FLOATS[y.dtype], ld_y, x.data_ptr(), ld_x, a.data_ptr(), b.data_ptr(),
+          scales_ptr, packed, n, k, rank, out.data_ptr(), ld_out, at, size, stream)
     if check:
         _check_data(ws)
     return out

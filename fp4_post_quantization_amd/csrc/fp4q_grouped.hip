@@ -157,11 +157,13 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// K a multiple of 128: operands move from global memory straight into an LDS ring of NS stages of ROWB code bytes of
+// K of 256 or more: operands move from global memory straight into an LDS ring of two stages of 128 code bytes of
 // every row, as in the plain product (fp4q_gemm.hip): one wave computes TM x TN blocks of 32 x 32, WGM x WGN waves a
 // tile; rows are unpadded and swizzled; K step ks takes, in lane half h, the 32-element block h KS + ks of the stage,
 // so that a lane's scale bytes of a stage are one word, of which the instruction selects byte ks.  What differs is
 // where rows come from: a lane loads the entry numbers of the rows that it stages once, before the loop.
+// TAIL, where K is no multiple of 256: chunks past a row's end are loaded from zeros, and scales, whose rows need not be
+// aligned, come through registers.
 //
 // Gated: block column j of a wave is gates for even j and the ups of the same columns for odd j, so that both meet in
 // a lane's registers.
@@ -186,8 +188,11 @@ __device__ __forceinline__ GroupTile group_tile(const GroupedArgs &a, const Tile
   return GroupTile{lo, g.hi - lo > rows ? lo + rows : g.hi, r / deep};
 }
 
-template <int ROWB, typename OutT, bool GATED, int WGM, int WGN, int TM, int TN, int NS>
+constexpr int kRowBytes = 128;  // code bytes of a row and stage: 256 elements of K
+
+template <typename OutT, bool GATED, int WGM, int WGN, int TM, int TN>
 struct RingShape {
+  static constexpr int ROWB = kRowBytes;
   static constexpr int WAVES = WGM * WGN, THREADS = 64 * WAVES;
   static constexpr int BM = WGM * TM * 32, BN = WGN * TN * 32;   // rows of A and of B
   static constexpr int COLS = GATED ? BN / 2 : BN;               // columns of C
@@ -197,18 +202,31 @@ struct RingShape {
   static constexpr int STAGE = SB_OFF + BN * SPR;
 };
 
-template <int ROWB, typename OutT, bool GATED, int WGM, int WGN, int TM, int TN, int NS>
+// The E8M0 bytes of blocks 8 st .. 8 st + 7 of a row that has ksc >= 8 of them, at any alignment; 127 past the last.
+__device__ __forceinline__ uint64_t scale_bytes(const uint8_t *row, int ksc, int st) {
+  const int want = 8 * st, at = want + 8 <= ksc ? want : ksc - 8, skip = want - at;  // skip < 8
+  uint64_t v;
+  __builtin_memcpy(&v, row + at, 8);
+  return skip ? v >> (8 * skip) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * skip) : v;
+}
+
+__device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
+
+template <typename OutT, bool GATED, bool TAIL, int WGM, int WGN, int TM, int TN>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArgs a) {
-  using S = RingShape<ROWB, OutT, GATED, WGM, WGN, TM, TN, NS>;
-  constexpr int WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
+  using S = RingShape<OutT, GATED, WGM, WGN, TM, TN>;
+  constexpr int ROWB = kRowBytes, NS = 2, WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
   constexpr int RPL = 1024 / ROWB;  // rows of a 1 KB load
   constexpr int A_INSTR = BM / RPL / WAVES, B_INSTR = BN / RPL / WAVES;
-  constexpr int SA_INSTR = BM * SPR / 256, SB_INSTR = BN * SPR / 256, SQ = (SA_INSTR + SB_INSTR + WAVES - 1) / WAVES;
+  constexpr int SA_INSTR = BM * SPR / 256, SB_INSTR = BN * SPR / 256;
+  constexpr int SQ = TAIL ? 0 : (SA_INSTR + SB_INSTR + WAVES - 1) / WAVES;
+  constexpr int SROWS = (BM + BN + S::THREADS - 1) / S::THREADS;  // TAIL: rows whose scales a thread brings
   constexpr int DPR = SPR / 4, RPS = 256 / SPR;  // scale words of a row, rows of a scale load
   static_assert(A_INSTR * WAVES * RPL == BM && B_INSTR * WAVES * RPL == BN, "code loads must divide evenly");
   static_assert(SA_INSTR * 256 == BM * SPR && SB_INSTR * 256 == BN * SPR, "scale loads cover whole rows");
   static_assert(!GATED || TN % 2 == 0, "gates and ups in pairs of block columns");
-  constexpr int LOADS = A_INSTR + B_INSTR + SQ;  // of a wave and stage; a wave without a scale load fills a spare slot
+  constexpr int LOADS = A_INSTR + B_INSTR + SQ + (TAIL ? SROWS : 0);  // of a wave and stage; one without a scale load
+                                                                     // fills a spare slot
   constexpr int SPARE = NS * STAGE;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + 256];
   __shared__ int row_of[BM];  // row of C, -1: not stored
@@ -227,7 +245,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   const int lo = t.lo, hi = t.hi, n0 = t.col * S::COLS;  // first column of C
 
   const int64_t kb = a.k / 2, ksc = a.k / 32;
-  const int nst = a.k / (2 * ROWB);
+  const int nst = (a.k + 2 * ROWB - 1) / (2 * ROWB);
   const uint8_t *B = a.b + (int64_t)g.group * a.n * kb, *Bs = a.bs + (int64_t)g.group * a.n * ksc;
   // row of A of tile row i (those past the tile repeat its last one: computed, never stored)
   auto a_of = [&](int i) {
@@ -243,17 +261,31 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
     if (lo + i < hi && e < 0) err = FP4Q_DATA_BAD_GROUP;
     row_of[i] = e < 0 ? -1 : (a.scatter ? e : lo + i);
   }
-  const uint8_t *srcA[A_INSTR], *srcB[B_INSTR], *srcS[SQ];
-  int dstS[SQ];
+  const uint8_t *srcA[A_INSTR], *srcB[B_INSTR], *srcS[SQ > 0 ? SQ : 1];
+  int dstS[SQ > 0 ? SQ : 1];
+  // TAIL: the 16-byte chunks that the last stage has of a row, and which of them this lane brings
+  const int last_chunks = (a.k - 2 * ROWB * (nst - 1)) / 32;
+  int chunkA[A_INSTR], chunkB[B_INSTR];
 #pragma unroll
   for (int i = 0; i < A_INSTR; ++i) {
     const int row = (wave * A_INSTR + i) * RPL + lane / CPR;
-    srcA[i] = a.a + a_of(row) * kb + 16 * ((lane % CPR) ^ fp4q_gemm::swz<ROWB>(row));
+    chunkA[i] = (lane % CPR) ^ fp4q_gemm::swz<ROWB>(row);
+    srcA[i] = a.a + a_of(row) * kb + 16 * chunkA[i];
   }
 #pragma unroll
   for (int i = 0; i < B_INSTR; ++i) {
     const int row = (wave * B_INSTR + i) * RPL + lane / CPR;
-    srcB[i] = B + b_of(row) * kb + 16 * ((lane % CPR) ^ fp4q_gemm::swz<ROWB>(row));
+    chunkB[i] = (lane % CPR) ^ fp4q_gemm::swz<ROWB>(row);
+    srcB[i] = B + b_of(row) * kb + 16 * chunkB[i];
+  }
+  // TAIL: scales of rows that need not be aligned come through registers, a row a thread
+  const uint8_t *rowS[SROWS];
+  uint64_t nextS[SROWS];
+#pragma unroll
+  for (int i = 0; i < SROWS; ++i) {
+    const int r = tid + i * S::THREADS;
+    rowS[i] = r < BM ? a.as + a_of(r) * ksc : Bs + b_of(r - BM < BN ? r - BM : BN - 1) * ksc;
+    nextS[i] = 0;
   }
 #pragma unroll
   for (int j = 0; j < SQ; ++j) {
@@ -271,15 +303,32 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   }
   auto issue = [&](int st, int slot) {
     uint8_t *base = smem + slot * STAGE;
+    const int chunks = TAIL && st == nst - 1 ? last_chunks : CPR;
+    auto source = [&](const uint8_t *p, int chunk) {
+      return TAIL && chunk >= chunks ? reinterpret_cast<const uint8_t *>(&kZeroCodes) : p + (int64_t)st * ROWB;
+    };
 #pragma unroll
     for (int i = 0; i < A_INSTR; ++i)
-      fp4q_gemm::load_lds16(srcA[i] + (int64_t)st * ROWB, base + (wave * A_INSTR + i) * 1024);
+      fp4q_gemm::load_lds16(source(srcA[i], chunkA[i]), base + (wave * A_INSTR + i) * 1024);
 #pragma unroll
     for (int i = 0; i < B_INSTR; ++i)
-      fp4q_gemm::load_lds16(srcB[i] + (int64_t)st * ROWB, base + S::A_BYTES + (wave * B_INSTR + i) * 1024);
+      fp4q_gemm::load_lds16(source(srcB[i], chunkB[i]), base + S::A_BYTES + (wave * B_INSTR + i) * 1024);
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int i = 0; i < SROWS; ++i) nextS[i] = scale_bytes(rowS[i], (int)ksc, st);
+    }
 #pragma unroll
     for (int j = 0; j < SQ; ++j)
       fp4q_gemm::load_lds4(srcS[j] + (int64_t)st * SPR, dstS[j] >= 0 ? base + dstS[j] : smem + SPARE);
+  };
+  auto put_scales = [&](int slot) {  // TAIL: of the stage last issued, into its slot
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int i = 0; i < SROWS; ++i) {
+        const int r = tid + i * S::THREADS;
+        if (r < BM + BN) *reinterpret_cast<uint64_t *>(smem + slot * STAGE + S::SA_OFF + 8 * r) = nextS[i];
+      }
+    }
   };
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -328,12 +377,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   };
 
-  // Stage s sits in slot s % NS; once every wave has read all of it, stage s + NS is issued into its slot (past the
+  // Stage s sits in slot s % 2; once every wave has read all of it, stage s + 2 is issued into its slot (past the
   // last one the last is loaded again, so that every wait is one constant).
-#pragma unroll
-  for (int s = 0; s < NS; ++s) issue(s < nst ? s : nst - 1, s);
-  fp4q_gemm::wait_lgkmcnt0();  // row_of is written
-  fp4q_gemm::wait_vmcnt<(NS - 1) * LOADS>();
+  issue(0, 0);
+  put_scales(0);
+  issue(nst > 1 ? 1 : 0, 1);
+  fp4q_gemm::wait_lgkmcnt0();  // row_of and the scales are written
+  fp4q_gemm::wait_vmcnt<LOADS>();
   stage_barrier();
   Ops o0, o1;
   int slot = 0;
@@ -352,11 +402,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
       });
     }
     __builtin_amdgcn_sched_barrier(0);
-    fp4q_gemm::wait_lgkmcnt0();                 // this wave's reads of stage st are complete
-    fp4q_gemm::wait_vmcnt<(NS - 2) * LOADS>();  // stage st + 1 has landed
-    stage_barrier();                            // ... for every wave, and nobody reads stage st any more
-    const int next = slot == NS - 1 ? 0 : slot + 1;
-    issue(st + NS < nst ? st + NS : nst - 1, slot);
+    const int next = slot ^ 1;
+    put_scales(next);
+    fp4q_gemm::wait_lgkmcnt0();  // this wave's reads of stage st are complete, and its scales of st + 1 written
+    fp4q_gemm::wait_vmcnt<0>();  // stage st + 1 has landed
+    stage_barrier();             // ... for every wave, and nobody reads stage st any more
+    issue(st + 2 < nst ? st + 2 : nst - 1, slot);
     if (live) {
       read_ops(next, std::integral_constant<int, 0>{}, o0, o1);
       __builtin_amdgcn_sched_barrier(0);
@@ -539,13 +590,13 @@ bool launch(GroupedArgs &a, hipStream_t s) {
   auto go = [&](auto kernel, int threads) { return launch_tiles(kernel, a, t, threads, s); };
   if (t.kind == kAnyTiles) return go(grouped_any_kernel<O, GATED>, kAnyThreads);
   if (t.kind == kFewTiles) return go(grouped_few_kernel<O, GATED>, 64 * kFewWaves);
-  if (a.k % 256 == 0) {
-    if (t.rows == 256) return go(grouped_ring_kernel<128, O, GATED, 2, 4, 4, 2, 2>, 512);
-    if (t.rows == 128) return go(grouped_ring_kernel<128, O, GATED, 2, 2, 2, 2, 2>, 256);
-    return go(grouped_ring_kernel<128, O, GATED, 2, 2, 1, 2, 2>, 256);
-  }
-  if (t.rows == 128) return go(grouped_ring_kernel<64, O, GATED, 2, 2, 2, 2, 4>, 256);
-  return go(grouped_ring_kernel<64, O, GATED, 2, 2, 1, 2, 4>, 256);
+  auto ring = [&](auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+    if (t.rows == 256) return go(grouped_ring_kernel<O, GATED, TAIL, 2, 4, 4, 2>, 512);
+    if (t.rows == 128) return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 2, 2>, 256);
+    return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 1, 2>, 256);
+  };
+  return a.k % 256 ? ring(std::true_type{}) : ring(std::false_type{});
 }
 
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }

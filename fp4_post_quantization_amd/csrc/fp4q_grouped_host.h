@@ -83,7 +83,7 @@ struct ProductTiles {
 inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, int64_t k) {
   ProductTiles t;
   auto tiles = [&](int rows, int cols) { return most_tiles(entries, groups, rows) * ceil_div(n, cols); };
-  if (k % 128) {
+  if (k < 256) {
     t = ProductTiles{kAnyTiles, kAnyRows, kAnyCols, 1, tiles(kAnyRows, kAnyCols)};
     return t;
   }
@@ -91,13 +91,13 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
   // Measured, us, gate and up products of 4096 x 1536 unless said:
   // few rows (16 x 32) where all of a call's tiles run at once, two a CU: one token of 8 experts 12.0, in tiles of 64 x
   // 128 14.5; 16 tokens (3600 tiles) 71 and 53.
-  if (tiles(kFewRows16, kFewCols) <= 512) {
+  if (k % 128 == 0 && tiles(kFewRows16, kFewCols) <= 512) {
     t = ProductTiles{kFewTiles, kFewRows16, kFewCols, 4, 0};
   } else if (rows <= 64) {
     // 64 rows up to 64 a group: 16 tokens of 128 experts 53, with 128 57; 64 tokens 92 and 103; 512 (32 rows) 113 and
     // 118; 256 tokens of 8 experts on 3584 columns (64 rows) 22 and 25; 1500 tokens (94 rows) 158 and 150.
     t = ProductTiles{kRingTiles, 64, 128, 4, 0};
-  } else if (rows >= 192 && k % 256 == 0 && tiles(256, 256) >= 768) {
+  } else if (rows >= 192 && tiles(256, 256) >= 768) {
     // 256 x 256 needs rows to fill it, and three tiles a CU: 4096 tokens (256 rows) 237, with 128 262; 768 x 4096 186
     // and 210; 2048 rows on 4096 x 4096 219 and 247; 512 rows on 14336 x 4096 (320 tiles) 282 and 265.
     t = ProductTiles{kRingTiles, 256, 256, 16, 0};

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// K of 256 or more: operands move from global memory straight into an LDS ring of two stages of 128 code bytes of
+// K of 256 or more: operands move from global memory straight into an LDS ring of NS stages of 128 code bytes of
 // every row, as in the plain product (fp4q_gemm.hip): one wave computes TM x TN blocks of 32 x 32, WGM x WGN waves a
 // tile; rows are unpadded and swizzled; K step ks takes, in lane half h, the 32-element block h KS + ks of the stage,
 // so that a lane's scale bytes of a stage are one word, of which the instruction selects byte ks.  What differs is
@@ -202,6 +202,22 @@ struct RingShape {
   static constexpr int STAGE = SB_OFF + BN * SPR;
 };
 
+// The accumulators' registers v .. v + 3 (four columns of one row, B's rows being the first operand) to the staging.
+template <typename OutT, bool GATED>
+__device__ __forceinline__ void stage_four(const f32x16 &x, const f32x16 &up, int v, float alpha, OutT *to) {
+  float z[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    z[k] = alpha * x[v + k];
+    if constexpr (GATED) z[k] = silu(z[k]) * (alpha * up[v + k]);
+  }
+  if constexpr (sizeof(OutT) == 4)
+    *reinterpret_cast<f32x4 *>(to) = f32x4{z[0], z[1], z[2], z[3]};
+  else
+    *reinterpret_cast<uint2 *>(to) =
+        uint2{fp4q_gemm::f32x2_to_bf16x2(z[0], z[1]), fp4q_gemm::f32x2_to_bf16x2(z[2], z[3])};
+}
+
 // The E8M0 bytes of blocks 8 st .. 8 st + 7 of a row that has ksc >= 8 of them, at any alignment; 127 past the last.
 __device__ __forceinline__ uint64_t scale_bytes(const uint8_t *row, int ksc, int st) {
   const int want = 8 * st, at = want + 8 <= ksc ? want : ksc - 8, skip = want - at;  // skip < 8
@@ -212,10 +228,11 @@ __device__ __forceinline__ uint64_t scale_bytes(const uint8_t *row, int ksc, int
 
 __device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
 
-template <typename OutT, bool GATED, bool TAIL, int WGM, int WGN, int TM, int TN>
+template <typename OutT, bool GATED, bool TAIL, int NS, int WGM, int WGN, int TM, int TN>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArgs a) {
   using S = RingShape<OutT, GATED, WGM, WGN, TM, TN>;
-  constexpr int ROWB = kRowBytes, NS = 2, WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
+  static_assert(!TAIL || NS == 2, "scales that come through registers are a stage ahead");
+  constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
   constexpr int RPL = 1024 / ROWB;  // rows of a 1 KB load
   constexpr int A_INSTR = BM / RPL / WAVES, B_INSTR = BN / RPL / WAVES;
   constexpr int SA_INSTR = BM * SPR / 256, SB_INSTR = BN * SPR / 256;
@@ -228,8 +245,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   constexpr int LOADS = A_INSTR + B_INSTR + SQ + (TAIL ? SROWS : 0);  // of a wave and stage; one without a scale load
                                                                      // fills a spare slot
   constexpr int SPARE = NS * STAGE;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + 256];
-  __shared__ int row_of[BM];  // row of C, -1: not stored
+  // One array: with two, the compiler tells them apart and then waits for every load into LDS before it reads any of it.
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + 256 + 4 * BM];
+  int *row_of = reinterpret_cast<int *>(smem + NS * STAGE + 256);  // row of C, -1: not stored
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int wm = wave / WGN, wn = wave % WGN, l32 = lane & 31, h = lane >> 5;
@@ -244,24 +262,26 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   const GroupTile t = group_tile(a, g, BM, lin);
   const int lo = t.lo, hi = t.hi, n0 = t.col * S::COLS;  // first column of C
 
-  const int64_t kb = a.k / 2, ksc = a.k / 32;
+  const uint32_t kb = a.k / 2, ksc = a.k / 32;
   const int nst = (a.k + 2 * ROWB - 1) / (2 * ROWB);
   const uint8_t *B = a.b + (int64_t)g.group * a.n * kb, *Bs = a.bs + (int64_t)g.group * a.n * ksc;
   // row of A of tile row i (those past the tile repeat its last one: computed, never stored)
   auto a_of = [&](int i) {
     const int p = lo + i < hi ? lo + i : hi - 1;
-    return (int64_t)(a.gather ? a_row(a, p, entry_at(a.groups, p)) : p);
+    return (uint32_t)(a.gather ? a_row(a, p, entry_at(a.groups, p)) : p);
   };
   auto b_of = [&](int i) {
     const int col = GATED ? (i / 64) * 32 + (i & 31) : i;
-    return (int64_t)((n0 + col < a.n_out ? n0 + col : a.n_out - 1) + (GATED && (i & 32) ? a.n_out : 0));
+    return (uint32_t)((n0 + col < a.n_out ? n0 + col : a.n_out - 1) + (GATED && (i & 32) ? a.n_out : 0));
   };
   for (int i = tid; i < BM; i += S::THREADS) {
     const int e = lo + i < hi ? entry_at(a.groups, lo + i) : -1;
     if (lo + i < hi && e < 0) err = FP4Q_DATA_BAD_GROUP;
     row_of[i] = e < 0 ? -1 : (a.scatter ? e : lo + i);
   }
-  const uint8_t *srcA[A_INSTR], *srcB[B_INSTR], *srcS[SQ > 0 ? SQ : 1];
+  // sources as 32-bit offsets from scalar bases: A and a group's matrix are below 4 GiB
+  uint32_t srcA[A_INSTR], srcB[B_INSTR], srcS[SQ > 0 ? SQ : 1];
+  const uint8_t *baseS[SQ > 0 ? SQ : 1];
   int dstS[SQ > 0 ? SQ : 1];
   // TAIL: the 16-byte chunks that the last stage has of a row, and which of them this lane brings
   const int last_chunks = (a.k - 2 * ROWB * (nst - 1)) / 32;
@@ -270,13 +290,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   for (int i = 0; i < A_INSTR; ++i) {
     const int row = (wave * A_INSTR + i) * RPL + lane / CPR;
     chunkA[i] = (lane % CPR) ^ fp4q_gemm::swz<ROWB>(row);
-    srcA[i] = a.a + a_of(row) * kb + 16 * chunkA[i];
+    srcA[i] = a_of(row) * kb + 16 * chunkA[i];
   }
 #pragma unroll
   for (int i = 0; i < B_INSTR; ++i) {
     const int row = (wave * B_INSTR + i) * RPL + lane / CPR;
     chunkB[i] = (lane % CPR) ^ fp4q_gemm::swz<ROWB>(row);
-    srcB[i] = B + b_of(row) * kb + 16 * chunkB[i];
+    srcB[i] = b_of(row) * kb + 16 * chunkB[i];
   }
   // TAIL: scales of rows that need not be aligned come through registers, a row a thread
   const uint8_t *rowS[SROWS];
@@ -284,42 +304,46 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
 #pragma unroll
   for (int i = 0; i < SROWS; ++i) {
     const int r = tid + i * S::THREADS;
-    rowS[i] = r < BM ? a.as + a_of(r) * ksc : Bs + b_of(r - BM < BN ? r - BM : BN - 1) * ksc;
+    rowS[i] = r < BM ? a.as + (uint64_t)a_of(r) * ksc : Bs + (uint64_t)b_of(r - BM < BN ? r - BM : BN - 1) * ksc;
     nextS[i] = 0;
   }
 #pragma unroll
   for (int j = 0; j < SQ; ++j) {
     const int q = wave + WAVES * j, rl = lane / DPR, dw = lane % DPR;
     if (q < SA_INSTR) {
-      srcS[j] = a.as + a_of(RPS * q + rl) * ksc + 4 * dw;
+      baseS[j] = a.as;
+      srcS[j] = a_of(RPS * q + rl) * ksc + 4 * dw;
       dstS[j] = S::SA_OFF + 256 * q;
     } else if (q < SA_INSTR + SB_INSTR) {
-      srcS[j] = Bs + b_of(RPS * (q - SA_INSTR) + rl) * ksc + 4 * dw;
+      baseS[j] = Bs;
+      srcS[j] = b_of(RPS * (q - SA_INSTR) + rl) * ksc + 4 * dw;
       dstS[j] = S::SB_OFF + 256 * (q - SA_INSTR);
     } else {
-      srcS[j] = Bs + 4 * dw;
+      baseS[j] = Bs;
+      srcS[j] = 4 * dw;
       dstS[j] = -1;
     }
   }
   auto issue = [&](int st, int slot) {
     uint8_t *base = smem + slot * STAGE;
     const int chunks = TAIL && st == nst - 1 ? last_chunks : CPR;
-    auto source = [&](const uint8_t *p, int chunk) {
-      return TAIL && chunk >= chunks ? reinterpret_cast<const uint8_t *>(&kZeroCodes) : p + (int64_t)st * ROWB;
+    const uint8_t *a_st = a.a + (int64_t)st * ROWB, *b_st = B + (int64_t)st * ROWB;
+    auto source = [&](const uint8_t *p, uint32_t off, int chunk) {
+      return TAIL && chunk >= chunks ? reinterpret_cast<const uint8_t *>(&kZeroCodes) : p + off;
     };
 #pragma unroll
     for (int i = 0; i < A_INSTR; ++i)
-      fp4q_gemm::load_lds16(source(srcA[i], chunkA[i]), base + (wave * A_INSTR + i) * 1024);
+      fp4q_gemm::load_lds16(source(a_st, srcA[i], chunkA[i]), base + (wave * A_INSTR + i) * 1024);
 #pragma unroll
     for (int i = 0; i < B_INSTR; ++i)
-      fp4q_gemm::load_lds16(source(srcB[i], chunkB[i]), base + S::A_BYTES + (wave * B_INSTR + i) * 1024);
+      fp4q_gemm::load_lds16(source(b_st, srcB[i], chunkB[i]), base + S::A_BYTES + (wave * B_INSTR + i) * 1024);
     if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < SROWS; ++i) nextS[i] = scale_bytes(rowS[i], (int)ksc, st);
     }
 #pragma unroll
     for (int j = 0; j < SQ; ++j)
-      fp4q_gemm::load_lds4(srcS[j] + (int64_t)st * SPR, dstS[j] >= 0 ? base + dstS[j] : smem + SPARE);
+      fp4q_gemm::load_lds4(baseS[j] + (int64_t)st * SPR + srcS[j], dstS[j] >= 0 ? base + dstS[j] : smem + SPARE);
   };
   auto put_scales = [&](int slot) {  // TAIL: of the stage last issued, into its slot
     if constexpr (TAIL) {
@@ -367,8 +391,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(o.a[i], o.b[j], acc[i][j], 4, 4, ks, o.sa[i], ks,
-                                                                    o.sb[j]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(o.b[j], o.a[i], acc[i][j], 4, 4, ks, o.sb[j], ks,
+                                                                    o.sa[i]);
   };
   const bool live = lo + wm * TM * 32 < hi;  // whether any of this wave's rows is there
   auto stage_barrier = [&]() {  // keeps LDS accesses on their side, without draining the loads in flight
@@ -377,13 +401,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
   };
 
-  // Stage s sits in slot s % 2; once every wave has read all of it, stage s + 2 is issued into its slot (past the
+  // Stage s sits in slot s % NS; once every wave has read all of it, stage s + NS is issued into its slot (past the
   // last one the last is loaded again, so that every wait is one constant).
   issue(0, 0);
   put_scales(0);
-  issue(nst > 1 ? 1 : 0, 1);
+#pragma unroll
+  for (int s = 1; s < NS; ++s) issue(s < nst ? s : nst - 1, s);
   fp4q_gemm::wait_lgkmcnt0();  // row_of and the scales are written
-  fp4q_gemm::wait_vmcnt<LOADS>();
+  fp4q_gemm::wait_vmcnt<(NS - 1) * LOADS>();
   stage_barrier();
   Ops o0, o1;
   int slot = 0;
@@ -394,20 +419,22 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
         constexpr int ks = decltype(ks_c)::value;
         if constexpr (ks % 2 == 0) {
           read_ops(slot, std::integral_constant<int, ks + 1>{}, o1, o0);
+          __builtin_amdgcn_sched_barrier(0);
           mfmas(o0, ks_c);
         } else {
           read_ops(slot, std::integral_constant<int, ks + 1>{}, o0, o1);
+          __builtin_amdgcn_sched_barrier(0);
           mfmas(o1, ks_c);
         }
       });
     }
     __builtin_amdgcn_sched_barrier(0);
-    const int next = slot ^ 1;
+    const int next = slot == NS - 1 ? 0 : slot + 1;
     put_scales(next);
     fp4q_gemm::wait_lgkmcnt0();  // this wave's reads of stage st are complete, and its scales of st + 1 written
-    fp4q_gemm::wait_vmcnt<0>();  // stage st + 1 has landed
-    stage_barrier();             // ... for every wave, and nobody reads stage st any more
-    issue(st + 2 < nst ? st + 2 : nst - 1, slot);
+    fp4q_gemm::wait_vmcnt<(NS - 2) * LOADS>();  // stage st + 1 has landed
+    stage_barrier();                            // ... for every wave, and nobody reads stage st any more
+    issue(st + NS < nst ? st + NS : nst - 1, slot);
     if (live) {
       read_ops(next, std::integral_constant<int, 0>{}, o0, o1);
       __builtin_amdgcn_sched_barrier(0);
@@ -432,22 +459,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
 #pragma unroll
     for (int j = 0; j < TN; j += JS)
 #pragma unroll
-      for (int v = 0; v < 16; v += 2) {
-        float z0 = alpha * acc[i][j][v], z1 = alpha * acc[i][j][v + 1];
-        if constexpr (GATED) {
-          z0 = silu(z0) * (alpha * acc[i][j + 1][v]);
-          z1 = silu(z1) * (alpha * acc[i][j + 1][v + 1]);
-        }
-        OutT *o = area + (8 * (v >> 2) + 4 * h + (v & 3)) * EROW + j / JS * 32 + l32;  // rows r and r + 1
-        if constexpr (sizeof(OutT) == 4) {
-          o[0] = z0;
-          o[EROW] = z1;
-        } else {
-          const uint32_t p = fp4q_gemm::f32x2_to_bf16x2(z0, z1);
-          o[0] = (uint16_t)p;
-          o[EROW] = (uint16_t)(p >> 16);
-        }
-      }
+      for (int v = 0; v < 16; v += 4) stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha, area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
 #pragma unroll
     for (int q = 0; q < 32 / RPI; ++q) {
       const int rr = q * RPI + lane / LPR, c = lane % LPR * VEC;
@@ -564,6 +576,309 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs
   Status{a.status, true}.finish(err);
 }
 
+// ---------------------------------------------------------------------------
+// The ring in tiles of 256 x 256 for many of them (K a multiple of 256, from 512 on; up to kPersistGroups groups): one
+// workgroup a CU walks tiles blockIdx, blockIdx + gridDim, ... and loads the next tile's first stages while it finishes
+// the one before.  Started anew, a tile costs 8 us beside its stages (2.4 us for 256 elements of K): the search for its
+// group, its rows' numbers, the first loads, the stores.  Here the groups' tiles are summed once into LDS, the next
+// tile's rows are asked for when a tile begins, and its loads follow the last ones of the tile without a gap.
+template <typename OutT, bool GATED>
+__global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
+  constexpr int WGN = 4, TM = 4, TN = 2;
+  using S = RingShape<OutT, GATED, 2, WGN, TM, TN>;
+  constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, CPR = S::CPR, KS = S::KS, SPR = S::SPR;
+  constexpr int STAGE = S::STAGE, RPL = 1024 / ROWB, LOADS = BM / RPL / WAVES;  // 1 KB loads of A, and of B, a wave
+  constexpr int RPS = 256 / SPR;  // rows of a scale load: a wave's first is A's, its second B's
+  static_assert(BM == S::BN && BM == RPS * WAVES, "a wave brings the scales of 32 rows of A and of B");
+  constexpr int ROWS_OFF = 2 * STAGE, SUMS_OFF = ROWS_OFF + 2 * 4 * BM, SPANS_OFF = SUMS_OFF + 4 * (kPersistGroups + 2);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[SPANS_OFF + 8 * kPersistGroups];
+  int *row_of = reinterpret_cast<int *>(smem + ROWS_OFF);  // rows of C of this tile and of the next, -1: not stored
+  int *sums = reinterpret_cast<int *>(smem + SUMS_OFF);    // row tiles of the groups before
+  int2 *spans = reinterpret_cast<int2 *>(smem + SPANS_OFF);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
+  const int wm = wave / WGN, wn = wave % WGN, l32 = lane & 31, h = lane >> 5;
+  uint32_t err = 0;
+  if (wave == 0) {
+    int run = 0;
+    bool bad = a.groups.offsets[0] != 0;
+    for (int g0 = 0; g0 < a.groups.groups; g0 += 64) {
+      const int g = g0 + lane;
+      const bool in = g < a.groups.groups;
+      const GroupSpan s = group_span(in ? a.groups.offsets[g] : 0, in ? a.groups.offsets[g + 1] : 0, a.groups.entries);
+      const int mine = in ? span_tiles(s.lo, s.hi, BM) : 0, upto = wave_scan(mine);
+      if (in) {
+        sums[g] = run + upto - mine;
+        spans[g] = int2{s.lo, s.hi};
+      }
+      bad |= s.bad;
+      run += __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (lane == 0) sums[a.groups.groups] = run;
+    if (blockIdx.x == 0 && __ballot(bad)) err = FP4Q_DATA_BAD_GROUP;
+  }
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(sums[a.groups.groups]) * a.tiles_n;
+
+  struct Tile {
+    int lin, group, lo, hi, n0;  // n0: first column of C
+  };
+  auto find = [&](int v) {  // tile of workgroup number v
+    Tile t;
+    const int local = v / kXcdCount;
+    t.lin = __builtin_amdgcn_readfirstlane((local / a.run * kXcdCount + v % kXcdCount) * a.run + local % a.run);
+    t.group = -1;
+    if (t.lin >= total) return t;
+    const int want = t.lin / a.tiles_n;
+    for (int g0 = 0; g0 < a.groups.groups; g0 += 64) {
+      const int g = g0 + lane;
+      const uint64_t hit = __ballot(g < a.groups.groups && sums[g < a.groups.groups ? g + 1 : 0] > want);
+      if (hit) {
+        t.group = g0 + __ffsll((unsigned long long)hit) - 1;
+        break;
+      }
+    }
+    const int2 s = spans[t.group];
+    const TileGroup g{t.group, __builtin_amdgcn_readfirstlane(s.x), __builtin_amdgcn_readfirstlane(s.y),
+                      __builtin_amdgcn_readfirstlane(sums[t.group])};
+    const GroupTile w = group_tile(a, g, BM, t.lin);
+    t.group = __builtin_amdgcn_readfirstlane(t.group);
+    t.lo = __builtin_amdgcn_readfirstlane(w.lo);
+    t.hi = __builtin_amdgcn_readfirstlane(w.hi);
+    t.n0 = __builtin_amdgcn_readfirstlane(w.col * S::COLS);
+    return t;
+  };
+
+  // Rows of A that this lane's loads of a tile take, and (threads below BM) the entry of a tile row.
+  struct Numbers {
+    int a[LOADS], s, entry;
+  };
+  auto numbers = [&](const Tile &t) {
+    Numbers r;
+    auto of = [&](int i) {
+      const int p = t.lo + i < t.hi ? t.lo + i : t.hi - 1;
+      return a.gather ? entry_at(a.groups, p) : p;
+    };
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) r.a[i] = of((wave * LOADS + i) * RPL + lane / CPR);
+    r.s = of(RPS * wave + lane / 2);
+    const int p = t.lo + tid;
+    r.entry = tid < BM && p < t.hi ? entry_at(a.groups, p) : -1;
+    return r;
+  };
+  const uint32_t kb = a.k / 2, ksc = a.k / 32;
+  const int nst = a.k / (2 * ROWB);
+  uint32_t offA[LOADS], offB[LOADS], offAs, offBs;  // of the tile whose stages are being issued
+  const uint8_t *B = nullptr, *Bs = nullptr;
+  auto set_sources = [&](const Tile &t, const Numbers &r, int which) {
+    const int lane = fp4q_gemm::opaque_lane();
+    auto a_of = [&](int n) { return (uint32_t)(a.gather ? (n < 0 ? 0 : n / a.gather) : n); };
+    auto b_of = [&](int i) {
+      const int col = t.n0 + (GATED ? (i / 64) * 32 + (i & 31) : i);
+      return (uint32_t)((col < a.n_out ? col : a.n_out - 1) + (GATED && (i & 32) ? a.n_out : 0));
+    };
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int row = (wave * LOADS + i) * RPL + lane / CPR, chunk = (lane % CPR) ^ fp4q_gemm::swz<ROWB>(row);
+      offA[i] = a_of(r.a[i]) * kb + 16 * chunk;
+      offB[i] = b_of(row) * kb + 16 * chunk;
+    }
+    offAs = a_of(r.s) * ksc + 4 * (lane % 2);
+    offBs = b_of(RPS * wave + lane / 2) * ksc + 4 * (lane % 2);
+    B = a.b + (int64_t)t.group * a.n * kb;
+    Bs = a.bs + (int64_t)t.group * a.n * ksc;
+    if (tid < BM) {
+      const int p = t.lo + tid;
+      if (p < t.hi && r.entry < 0) err = FP4Q_DATA_BAD_GROUP;
+      row_of[which * BM + tid] = r.entry < 0 ? -1 : (a.scatter ? r.entry : p);
+    }
+  };
+  auto issue = [&](int st, int slot) {
+    uint8_t *base = smem + slot * STAGE;
+    const uint8_t *a_st = a.a + (int64_t)st * ROWB, *b_st = B + (int64_t)st * ROWB;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fp4q_gemm::load_lds16(a_st + offA[i], base + (wave * LOADS + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fp4q_gemm::load_lds16(b_st + offB[i], base + S::A_BYTES + (wave * LOADS + i) * 1024);
+    fp4q_gemm::load_lds4(a.as + (int64_t)st * SPR + offAs, base + S::SA_OFF + 256 * wave);
+    fp4q_gemm::load_lds4(Bs + (int64_t)st * SPR + offBs, base + S::SB_OFF + 256 * wave);
+  };
+
+  f32x16 acc[TM][TN];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{0};
+  };
+  struct Ops {
+    i32x8 a[TM], b[TN];
+    int sa[TM], sb[TN];
+  };
+  const int lane_sw = fp4q_gemm::swz<ROWB>(l32);
+  auto read_ops = [&](int slot, auto ks_c, Ops &o, const Ops &prev) {
+    constexpr int ks = decltype(ks_c)::value;
+    const uint8_t *base = smem + slot * STAGE;
+    const uint8_t *at = base + l32 * ROWB + 16 * ((h * KS + ks) ^ lane_sw);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(at + (wm * TM + i) * 32 * ROWB);
+      o.a[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      o.sa[i] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(base + S::SA_OFF + SPR * ((wm * TM + i) * 32 + l32) + 4 * h)
+                        : prev.sa[i];
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(at + S::A_BYTES + (wn * TN + j) * 32 * ROWB);
+      o.b[j] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
+      o.sb[j] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(base + S::SB_OFF + SPR * ((wn * TN + j) * 32 + l32) + 4 * h)
+                        : prev.sb[j];
+    }
+  };
+  auto mfmas = [&](const Ops &o, auto ks_c) {
+    constexpr int ks = decltype(ks_c)::value;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(o.b[j], o.a[i], acc[i][j], 4, 4, ks, o.sb[j], ks,
+                                                                    o.sa[i]);
+  };
+  auto pin = [&]() {  // the MFMAs issued so far are placed here
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) __asm__ volatile("" : "+v"(acc[i][j]));
+  };
+  auto stage_barrier = [&]() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  };
+
+  constexpr int WCOLS = S::COLS / WGN, VEC = 16 / (int)sizeof(OutT), EROW = WCOLS + VEC;
+  constexpr int LPR = WCOLS / VEC, RPI = 64 / LPR;
+  static_assert(WAVES * 32 * EROW * (int)sizeof(OutT) <= STAGE, "epilogue staging must fit in a stage");
+  const bool wide = ((uintptr_t)a.c % 16 == 0) && ((a.ldc * (int64_t)sizeof(OutT)) % 16 == 0);
+  auto epilogue = [&](const Tile &t, int which, uint8_t *room) {
+    const int ln = fp4q_gemm::opaque_lane(), l32 = ln & 31, h = ln >> 5;
+    OutT *area = reinterpret_cast<OutT *>(room) + wave * 32 * EROW;
+    OutT *C = (OutT *)a.c;
+    const float alpha = a.alpha;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      constexpr int JS = GATED ? 2 : 1;
+#pragma unroll
+      for (int j = 0; j < TN; j += JS)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha, area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
+#pragma unroll
+      for (int q = 0; q < 32 / RPI; ++q) {
+        const int rr = q * RPI + ln / LPR, c = ln % LPR * VEC;
+        const int row = row_of[which * BM + (wm * TM + i) * 32 + rr], col = t.n0 + wn * WCOLS + c;
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(area + rr * EROW + c);
+        if (row >= 0) {
+          OutT *dst = C + (int64_t)row * a.ldc + col;
+          if (wide && col + VEC <= a.n_out) {
+            *reinterpret_cast<i32x4 *>(dst) = v;
+          } else {
+            const OutT *e = reinterpret_cast<const OutT *>(&v);
+#pragma unroll
+            for (int x = 0; x < VEC; ++x)
+              if (col + x < a.n_out) dst[x] = e[x];
+          }
+        }
+      }
+    }
+  };
+
+  // The issue stream runs over the stages of all this workgroup's tiles, two ahead of the MFMAs; a tile's stage g sits
+  // in the slot that follows the one before.  Every wait is for all of a wave's loads (and the epilogue's stores).
+  int v = blockIdx.x;
+  Tile cur = find(v), nxt;
+  if (cur.group >= 0) {
+    set_sources(cur, numbers(cur), 0);
+    issue(0, 0);
+    issue(1, 1);
+    fp4q_gemm::wait_lgkmcnt0();
+    fp4q_gemm::wait_vmcnt<2 * LOADS + 2>();
+    stage_barrier();
+    int slot = 0, which = 0;
+    Numbers ahead;
+    auto stage_end = [&]() {
+      __builtin_amdgcn_sched_barrier(0);
+      fp4q_gemm::wait_lgkmcnt0();  // this wave's reads of the stage are complete
+      fp4q_gemm::wait_vmcnt<0>();  // the next one has landed
+      stage_barrier();             // ... for every wave, and nobody reads this one any more
+    };
+    // The stages of a tile, by waves that have rows of it and by those that only load.
+    auto walk = [&](auto live_c) {
+      constexpr bool LIVE = decltype(live_c)::value;
+      Ops o0, o1;
+      if constexpr (LIVE) {
+        clear();
+        read_ops(slot, std::integral_constant<int, 0>{}, o0, o1);
+      }
+      auto body = [&]() {
+        if constexpr (LIVE) {
+          fp4q_gemm::unroll(std::make_integer_sequence<int, KS - 1>{}, [&](auto ks_c) {
+            constexpr int ks = decltype(ks_c)::value;
+            if constexpr (ks % 2 == 0) {
+              read_ops(slot, std::integral_constant<int, ks + 1>{}, o1, o0);
+              __builtin_amdgcn_sched_barrier(0);
+              mfmas(o0, ks_c);
+            } else {
+              read_ops(slot, std::integral_constant<int, ks + 1>{}, o0, o1);
+              __builtin_amdgcn_sched_barrier(0);
+              mfmas(o1, ks_c);
+            }
+          });
+          pin();
+        }
+        stage_end();
+      };
+#pragma nounroll
+      for (int st = 0; st + 1 < nst; ++st) {
+        body();
+        if (st + 2 < nst) {
+          issue(st + 2, slot);
+        } else if (nxt.group >= 0) {  // the next tile's first stage
+          set_sources(nxt, ahead, which ^ 1);
+          issue(0, slot);
+        }
+        slot ^= 1;
+        if constexpr (LIVE) {
+          read_ops(slot, std::integral_constant<int, 0>{}, o0, o1);
+          __builtin_amdgcn_sched_barrier(0);
+          mfmas(o1, std::integral_constant<int, KS - 1>{});
+        }
+      }
+      body();  // the last stage: its slot takes the epilogue's staging before the next tile's second stage
+      if constexpr (LIVE) {
+        mfmas(o1, std::integral_constant<int, KS - 1>{});
+        pin();
+        epilogue(cur, which, smem + slot * STAGE);
+      }
+    };
+#pragma nounroll
+    for (;;) {
+      v += gridDim.x;
+      nxt = find(v);
+      if (nxt.group >= 0) ahead = numbers(nxt);
+      if (cur.lo + wm * TM * 32 < cur.hi) walk(std::true_type{});
+      else walk(std::false_type{});
+      if (nxt.group < 0) break;
+      fp4q_gemm::wait_lgkmcnt0();  // this wave's reads of the staging are complete
+      stage_barrier();             // ... for every wave: the slot may be filled
+      issue(1, slot);
+      slot ^= 1;
+      which ^= 1;
+      cur = nxt;
+    }
+  }
+  Status{a.status, true}.finish(err);
+}
+
 __global__ __launch_bounds__(64) void grouped_status_kernel(uint32_t *status) {
   if (threadIdx.x == 0) Status{status, true}.merge(0u);
 }
@@ -586,15 +901,16 @@ bool launch_tiles(K kernel, GroupedArgs &a, const ProductTiles &t, int threads, 
 
 template <typename O, bool GATED>
 bool launch(GroupedArgs &a, hipStream_t s) {
-  const ProductTiles t = product_tiles(a.groups.entries, a.groups.groups, a.n, a.k);
+  const ProductTiles t = product_tiles(a.groups.entries, a.groups.groups, a.n, a.k, a.a_rows);
   auto go = [&](auto kernel, int threads) { return launch_tiles(kernel, a, t, threads, s); };
+  if (t.kind == kPersistTiles) return go(grouped_persist_kernel<O, GATED>, 512);
   if (t.kind == kAnyTiles) return go(grouped_any_kernel<O, GATED>, kAnyThreads);
   if (t.kind == kFewTiles) return go(grouped_few_kernel<O, GATED>, 64 * kFewWaves);
+  if (t.kind == kDeepTiles) return go(grouped_ring_kernel<O, GATED, false, 3, 2, 2, 1, 2>, 256);
   auto ring = [&](auto tail) {
     constexpr bool TAIL = decltype(tail)::value;
-    if (t.rows == 256) return go(grouped_ring_kernel<O, GATED, TAIL, 2, 4, 4, 2>, 512);
-    if (t.rows == 128) return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 2, 2>, 256);
-    return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 1, 2>, 256);
+    if (t.rows == 128) return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 2, 2, 2>, 256);
+    return go(grouped_ring_kernel<O, GATED, TAIL, 2, 2, 2, 1, 2>, 256);
   };
   return a.k % 256 ? ring(std::true_type{}) : ring(std::false_type{});
 }

@@ -69,21 +69,23 @@ inline fp4q_status_t grouped_product_check(const fp4q_row_groups_t &g, int64_t a
 }
 
 constexpr int kXcdCount = 8;
+constexpr int kPersistGroups = 512;
 constexpr int kAnyRows = 64, kAnyCols = 128;
 constexpr int kFewRows16 = 16, kFewCols = 32;
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The kernel of a grouped product, its tiles (rows of A times rows of B), and the tiles in a row that go to one XCD.
-enum ProductKind { kAnyTiles, kFewTiles, kRingTiles };
+enum ProductKind { kAnyTiles, kFewTiles, kRingTiles, kDeepTiles, kPersistTiles };
 struct ProductTiles {
   ProductKind kind;
   int rows, cols, run;
   int64_t workgroups;
 };
-inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, int64_t k) {
+inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, int64_t k, int64_t a_rows) {
   ProductTiles t;
+  const int64_t far = (int64_t)UINT32_MAX - 4096;  // the ring's kernels take 32-bit offsets into A and into a matrix
   auto tiles = [&](int rows, int cols) { return most_tiles(entries, groups, rows) * ceil_div(n, cols); };
-  if (k < 256) {
+  if (k < 256 || a_rows * (k / 2) > far || n * (k / 2) > far) {
     t = ProductTiles{kAnyTiles, kAnyRows, kAnyCols, 1, tiles(kAnyRows, kAnyCols)};
     return t;
   }
@@ -94,17 +96,27 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
   if (k % 128 == 0 && tiles(kFewRows16, kFewCols) <= 512) {
     t = ProductTiles{kFewTiles, kFewRows16, kFewCols, 4, 0};
   } else if (rows <= 64) {
-    // 64 rows up to 64 a group: 16 tokens of 128 experts 53, with 128 57; 64 tokens 92 and 103; 512 (32 rows) 113 and
-    // 118; 256 tokens of 8 experts on 3584 columns (64 rows) 22 and 25; 1500 tokens (94 rows) 158 and 150.
-    t = ProductTiles{kRingTiles, 64, 128, 4, 0};
-  } else if (rows >= 192 && tiles(256, 256) >= 768) {
-    // 256 x 256 needs rows to fill it, and three tiles a CU: 4096 tokens (256 rows) 237, with 128 262; 768 x 4096 186
-    // and 210; 2048 rows on 4096 x 4096 219 and 247; 512 rows on 14336 x 4096 (320 tiles) 282 and 265.
-    t = ProductTiles{kRingTiles, 256, 256, 16, 0};
+    // 64 rows up to 64 a group: 16 tokens of 128 experts 51, with 128 52; 64 tokens 91 and 100; 512 (32 rows) 115 and
+    // 117; 1000 (62 rows) 130 and 130; 1500 (94 rows) 155 and 142.  Two stages more in flight where K has many, at two
+    // workgroups a CU instead of three: 46, 91, 110 and 129; 64 tokens of 8 experts on 14336 x 4096 46 and 41; 1000
+    // tokens on 768 x 4096 73 and 84.
+    t = ProductTiles{k % 256 == 0 && k >= 4096 ? kDeepTiles : kRingTiles, 64, 128, 4, 0};
   } else {
-    t = ProductTiles{kRingTiles, 128, 128, 4, 0};
+    const int64_t live = groups < entries ? groups : entries;
+    auto rounds = [&](int64_t r, int64_t c, int64_t at_once) {  // every group's last tile half full
+      return ceil_div((entries / r + live / 2) * ceil_div(n, c), at_once);
+    };
+    // 256 x 256, one a CU, where it takes fewer rounds of 1.55 times the length than 128 x 128, two a CU: 2500 tokens of
+    // 128 experts (156 rows) 165 and 183; 4096 tokens (256) 212 and 262; 768 x 4096 154 and 196; 2048 rows on 4096 x 4096
+    // 200 and 243; 512 rows on 4096 x 4096 (two rounds, the second a quarter full) 75 and 68; 94 rows 157 and 142.
+    if (k % 256 == 0 && k >= 512 && groups <= kPersistGroups &&
+        155 * rounds(256, 256, 256) <= 100 * rounds(128, 128, 512))
+      t = ProductTiles{kPersistTiles, 256, 256, 16, 0};
+    else
+      t = ProductTiles{kRingTiles, 128, 128, 4, 0};
   }
   t.workgroups = ceil_div(tiles(t.rows, t.cols), t.run * kXcdCount) * t.run * kXcdCount;
+  if (t.kind == kPersistTiles && t.workgroups > kCus && t.workgroups <= kMaxTiles) t.workgroups = kCus;
   return t;
 }
 

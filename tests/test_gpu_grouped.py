@@ -237,6 +237,8 @@ PRODUCTS = [  # tokens, groups, top_k, k, n
     (1, 8, 2, 512, 256), (3, 60, 4, 704, 40), (16, 128, 8, 1024, 96), (17, 4, 1, 4096, 200), (64, 8, 2, 2048, 512),
     (100, 3, 2, 256, 130), (130, 16, 4, 1056, 66), (257, 5, 2, 128, 260), (300, 2, 1, 1536, 384), (700, 2, 2, 768, 320),
     (40, 200, 3, 32, 34), (9, 1, 1, 8192, 64), (1500, 6, 2, 640, 256), (33, 2, 2, 14336, 48),
+    (100, 16, 4, 1024, 520), (64, 16, 4, 4096, 520), (90, 40, 6, 4608, 258), (500, 4, 1, 2048, 640),
+    (4096, 6, 2, 512, 4000), (2900, 20, 3, 768, 4096), (3000, 3, 3, 1280, 3602),
 ]
 
 
@@ -281,7 +283,8 @@ def test_grouped_product_matches_the_plain_one():
     assert torch.allclose(got, fq.gemm_mxfp4(a, w), rtol=1e-5, atol=1e-3)
 
 
-@pytest.mark.parametrize("tokens,k,n", [(12, 1024, 128), (400, 512, 256), (90, 96, 64)])
+@pytest.mark.parametrize("tokens,k,n", [(12, 1024, 128), (400, 512, 256), (90, 96, 64), (90, 4096, 2000),
+                                        (4096, 512, 4096)])
 def test_grouped_product_keeps_nan_to_its_row_and_column(tokens, k, n):
     fq = _fq()
     rng = np.random.default_rng(8)
@@ -299,7 +302,8 @@ def test_grouped_product_keeps_nan_to_its_row_and_column(tokens, k, n):
     assert np.array_equal(_np(got)[~nan], _np(ref)[~nan])
 
 
-@pytest.mark.parametrize("tokens,k,n", [(20, 1024, 96), (500, 512, 256), (90, 96, 64)])
+@pytest.mark.parametrize("tokens,k,n", [(20, 1024, 96), (500, 512, 256), (90, 96, 64), (90, 4096, 2000),
+                                        (5000, 512, 4096)])
 def test_grouped_product_with_bad_groups_stays_inside(tokens, k, n):
     """Offsets and rows out of range are reported and not followed; guards around C stay."""
     fq = _fq()

@@ -7,6 +7,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -222,6 +223,10 @@ extern "C" void plan(int64_t units, int64_t per_unit, int64_t least, int64_t *o)
   SortPlan p = sort_plan(units, per_unit, least);
   o[0] = p.per; o[1] = p.blocks; o[2] = p.join; o[3] = p.places;
 }
+extern "C" void product(int64_t entries, int64_t groups, int64_t n, int64_t k, int64_t *o) {
+  ProductTiles t = product_tiles(entries, groups, n, k, entries);
+  o[0] = t.kind; o[1] = t.rows; o[2] = t.cols; o[3] = t.run; o[4] = t.workgroups;
+}
 extern "C" int64_t splits(int64_t entries, int64_t groups, int64_t k) { return lora_plan(entries, groups, k).splits; }
 """
 
@@ -236,7 +241,7 @@ def host(tmp_path_factory):
                    check=True)
     lib = ctypes.CDLL(str(so))
     P, I = ctypes.c_void_p, ctypes.c_int64
-    lib.span.argtypes, lib.plan.argtypes = [I, I, I, I, P], [I, I, I, P]
+    lib.span.argtypes, lib.plan.argtypes, lib.product.argtypes = [I, I, I, I, P], [I, I, I, P], [I, I, I, I, P]
     for f in (lib.most, lib.splits):
         f.argtypes, f.restype = [I, I, I], I
     return lib
@@ -282,3 +287,51 @@ def test_adapter_splits_keep_whole_steps(host):
         for groups in (1, 5, 100):
             for k in (8, 64, 1024, 4096, 14336):
                 assert 1 <= host.splits(entries, groups, k) <= 8
+
+
+def _tiles(host, *sizes):
+    o = np.zeros(5, np.int64)
+    host.product(*sizes, o.ctypes.data)
+    return dict(zip(("kind", "rows", "cols", "run", "workgroups"), o.tolist()))
+
+
+ANY, FEW, RING, DEEP, PERSIST = range(5)
+
+
+def test_product_tiles_cover_the_rows(host):
+    """Every launch but the persistent one has a workgroup for each tile there can be, in whole runs for every XCD."""
+    rng = np.random.default_rng(4)
+    for _ in range(2000):
+        groups = int(rng.integers(1, 300))
+        entries = int(np.exp(rng.uniform(0, 12)))
+        n, k = int(rng.integers(1, 9000)), 32 * int(rng.integers(1, 500))
+        t = _tiles(host, entries, groups, n, k)
+        most = host.most(entries, groups, t["rows"]) * -(-n // t["cols"])
+        assert t["workgroups"] % (8 * t["run"] if t["kind"] in (FEW, RING, DEEP) else 1) == 0
+        assert t["workgroups"] >= (min(most, 256) if t["kind"] == PERSIST else most)
+        assert k >= 256 or t["kind"] == ANY
+        assert t["kind"] not in (DEEP, PERSIST) or k % 256 == 0
+        assert t["kind"] != PERSIST or (k >= 512 and groups <= 512 and t["workgroups"] % 8 == 0)
+        assert t["kind"] != FEW or k % 128 == 0
+
+
+def test_products_past_32_bit_offsets_and_launches(host):
+    """Operands of 4 GiB and more go to the kernel with 64-bit addresses; more tiles than a launch has are counted."""
+    assert _tiles(host, 1 << 20, 4, 4096, 8192)["kind"] == ANY       # 2^20 rows of 4096 bytes
+    assert _tiles(host, 1 << 19, 4, 4096, 8192)["kind"] == PERSIST
+    assert _tiles(host, 4096, 4, 1 << 21, 4096)["kind"] == ANY       # a matrix of 2^32 bytes
+    assert _tiles(host, 1 << 22, 2, 1 << 20, 512)["workgroups"] > 1 << 22
+
+
+def test_product_sizes_of_the_gpu_tests_reach_every_kernel(host):
+    sys.path.insert(0, os.path.join(ROOT, "tests"))
+    from test_gpu_grouped import PRODUCTS
+    seen = set()
+    for tokens, groups, top_k, k, n in PRODUCTS:
+        t = _tiles(host, tokens * top_k, groups, n, k)
+        tail = t["kind"] == RING and k % 256 != 0
+        several = t["kind"] == PERSIST and (tokens * top_k // 256) * (n // 256) > 256  # tiles, at least
+        seen.add((t["kind"], t["rows"], tail, several))
+    assert seen >= {(ANY, 64, False, False), (FEW, 16, False, False), (RING, 64, False, False), (RING, 64, True, False),
+                    (RING, 128, False, False), (RING, 128, True, False), (DEEP, 64, False, False),
+                    (PERSIST, 256, False, True)}

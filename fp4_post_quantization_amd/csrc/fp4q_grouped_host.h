@@ -171,7 +171,8 @@ inline fp4q_status_t lora_check_sizes(int64_t entries, int64_t groups, int64_t n
   return FP4Q_OK;
 }
 
-// few: B meets 16 rows at a time, else 64 (32 in float32 and for ranks beyond 128, which take twice the registers).
+// few: B meets 16 rows at a time, else 64 (8191 rows, rank 64, N 14336: 119 us, with 32 134), but 32 in float32 and for
+// ranks beyond 64, which take twice the registers and LDS (4000 rows, rank 128, N 4096: 39 us, with 64 41).
 // splits: of K, over workgroups.
 struct LoraPlan {
   bool few;
@@ -180,7 +181,7 @@ struct LoraPlan {
 inline LoraPlan lora_plan(int64_t entries, int64_t groups, int64_t k) {
   LoraPlan p;
   p.few = entries < 64 * groups || entries <= 256;
-  const int64_t tiles = most_tiles(entries, groups, 16), steps = ceil_div(k, 32) / 16;  // at least two steps a wave
+  const int64_t tiles = most_tiles(entries, groups, 16), steps = ceil_div(k, 32) / 16;  // at least two stages of 64 a wave
   p.splits = tiles ? 256 / tiles : 1;
   if (p.splits > steps) p.splits = steps;
   if (p.splits > 8) p.splits = 8;
@@ -188,7 +189,7 @@ inline LoraPlan lora_plan(int64_t entries, int64_t groups, int64_t k) {
   return p;
 }
 inline int64_t lora_rows(const LoraPlan &p, int64_t rank, int64_t size) {
-  return p.few ? 16 : (size == 4 || rank > 128 ? 32 : 64);
+  return p.few ? 16 : (size == 4 || rank > 64 ? 32 : 64);
 }
 
 }  // namespace fp4q

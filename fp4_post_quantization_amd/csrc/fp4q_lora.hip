@@ -4,18 +4,25 @@
 // lane l takes row l % 16 and the 8 elements of K at 8 (l / 16), and register
 // v of its accumulator holds row 4 (l / 16) + v, column l % 16).
 //
-//   shrink  u = s x A^T: 16 rows a workgroup, K shared by its four waves, and
-//           where there are few rows by several workgroups.  Their sums meet
-//           in LDS.  A row's u is taken on as bfloat16 parts, each the leading
-//           bits of what the ones before leave: three hold float32's 24 bits
-//           exactly.  For a bfloat16 result two do, the second rounded: they
-//           are off by 2^-17 of u, 2^-9 of the result's own half step.
+//   shrink  u = s x A^T: 16 or 32 rows a workgroup, K shared by its four waves,
+//           and where there are few rows by several workgroups.  Their sums
+//           meet in LDS.  A row's u is taken on as bfloat16 parts, each the
+//           leading bits of what the ones before leave: three hold float32's 24
+//           bits exactly.  For a bfloat16 result two do, the second rounded:
+//           they are off by 2^-17 of u, 2^-9 of the result's own half step.
 //           Workgroups that share K write float32 sums instead.
 //   expand  y + u B^T, 256 columns a workgroup, 64 a wave, which keeps its part
-//           of B in registers for up to 64 rows.  B's rows are the first
-//           operand and u's the second, so a lane ends with several consecutive
-//           columns of one row, which it adds to y and stores without any
-//           exchange.
+//           of B in registers for up to 64 rows.  Column 4 q + i of the wave's
+//           64 is column q of tile i, so that a lane ends with four consecutive
+//           columns of a row and 16 lanes with all 64, which they add to y and
+//           store without any exchange.
+//
+// Both read through LDS what the matrix core wants by rows: a load of 16 bytes a
+// lane takes 16 cycles where its first 16 lanes read one run of memory, and 64
+// where they read 16 rows (8191 rows, rank 64, K 4096: shrink 31 us so, 21 by
+// LDS; expand to 14336 columns 115 with y and out in the operand's layout too, 97
+// now; 64 requests on 32 adapters, rank 64, N 4096: 9.6 -> 5.0).  Then y and out
+// bound it for many rows (the latter at 4.8 TB/s), B and two launches for few.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -75,81 +82,114 @@ __host__ __device__ __forceinline__ int64_t part_size(int64_t entries, int rank)
 }
 
 // RT tiles of 16 ranks, MR of 16 rows, WAVES that share K; PARTS bfloat16 parts, or 0: float32 sums of a share of K.
-// All workgroups of a group read the same A at about the same time, which is what bounds this kernel for many rows
-// (A's rows lie a power of two apart and meet in few channels of the L2): two row tiles halve it.
-template <int RT, int MR, int WAVES, int PARTS>
+//
+// A wave copies 64 elements of K of its rows of x and of A at a time to its own part of the LDS, NS such stages in
+// flight, and reads its operands there: a load of 16 bytes a lane straight into the operand's layout has 16 rows in its
+// first 16 lanes, and such a load takes the 64 cycles of 64 lines.  16-byte piece p of row r lies at p ^ (r / 2 % 8) of
+// its 128 bytes, so that 16 rows read at once fall on all banks.
+template <int RT, int MR, int WAVES, int NS, int PARTS>
 __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(LoraArgs a) {
-  constexpr int STEPS = RT <= 4 ? 4 : (RT == 8 ? 2 : 1);  // steps of K whose loads are in flight together
-  __shared__ f32x4 part[WAVES][RT * MR][64];
+  constexpr int LOADS = 2 * (MR + RT), STAGE = 1024 * LOADS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * NS * STAGE];
+  static_assert(RT * MR <= NS * LOADS, "the waves' sums lie where their stages were");
   const int lane = threadIdx.x & 63, wave = wave_index(), r16 = lane & 15, h = lane >> 4;
   uint32_t err = 0;
   const RowTile t = find_tile(a.groups, 16 * MR, (int)blockIdx.x);
   if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
   if (t.group >= 0) {
-    const uint16_t *x[MR];
+    const int row8 = lane >> 3;  // of the eight rows of a load
+    int64_t x[2 * MR];
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      const int row = t.lo + 16 * m + r16;
+    for (int j = 0; j < 2 * MR; ++j) {
+      const int row = t.lo + 8 * j + row8;
       int e = entry_at(a.groups, row < t.hi ? row : t.hi - 1);
       if (e < 0) {
         err = FP4Q_DATA_BAD_GROUP;
         e = 0;
       }
-      x[m] = a.x + e * a.ld_x + 8 * h;
+      x[j] = e * a.ld_x;
     }
-    const uint16_t *w = a.a + (int64_t)t.group * a.rank * a.k + 8 * h;
-    int64_t at[RT];
+    const uint16_t *w = a.a + ((int64_t)t.group * a.rank + row8) * a.k;
+    const int eights = a.rank / 8, piece = 8 * ((lane & 7) ^ (row8 >> 1));
+    const int stages = (a.k + 63) / 64, shares = a.splits * WAVES;
+    const int share = (int)blockIdx.y * WAVES + wave, per = (stages + shares - 1) / shares;
+    const int s0 = share * per, s1 = s0 + per < stages ? s0 + per : stages;
+    uint8_t *mine = lds + wave * NS * STAGE;
+    auto load = [&](int s, int slot) {
+      int at[2];  // elements past the end of K: the row's first ones
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = 16 * i + r16;
-      at[i] = (int64_t)(r < a.rank ? r : a.rank - 1) * a.k;
-    }
-    const int steps = (a.k + 31) / 32, shares = a.splits * WAVES;
-    const int share = (int)blockIdx.y * WAVES + wave, per = (steps + shares - 1) / shares;
-    const int s0 = share * per, s1 = s0 + per < steps ? s0 + per : steps;
+      for (int i = 0; i < 2; ++i) {
+        const int k = 64 * s + (piece ^ (32 * i));
+        at[i] = k < a.k ? k : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * MR; ++j) fp4q_gemm::load_lds16(a.x + x[j] + at[j & 1], mine + slot * STAGE + 1024 * j);
+#pragma unroll
+      for (int j = 0; j < 2 * RT; ++j)  // past the rank: its last rows, whose columns are not stored
+        fp4q_gemm::load_lds16(w + (int64_t)(8 * (j < eights ? j : eights - 1)) * a.k + at[j & 1],
+                              mine + slot * STAGE + 1024 * (2 * MR + j));
+    };
     f32x4 acc[RT][MR];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int m = 0; m < MR; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
-    for (int s = s0; s < s1; s += STEPS) {
-      bf16x8 xv[STEPS][MR], wv[STEPS][RT];
 #pragma unroll
-      for (int q = 0; q < STEPS; ++q) {
-        // past the wave's share or the end of K: an earlier piece of the row, which then meets zeros
-        const int k0 = 32 * (s + q < s1 ? s + q : s1 - 1), off = k0 + 8 * h < a.k ? k0 : -8 * h;
-#pragma unroll
-        for (int m = 0; m < MR; ++m) xv[q][m] = load_bf16x8(x[m] + off);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) wv[q][i] = load_bf16x8(w + at[i] + off);
-      }
+    for (int s = 0; s < NS; ++s)
+      if (s0 + s < s1) load(s0 + s, s);
+    int slot = 0;
+    for (int s = s0; s < s1; ++s) {
+      if (NS > 1 && s + NS <= s1) fp4q_gemm::wait_vmcnt<(NS - 1) * LOADS>();
+      else fp4q_gemm::wait_vmcnt<0>();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_sched_barrier(0);
+      bf16x8 xv[2][MR], wv[2][RT];
+      const uint8_t *from = mine + slot * STAGE + r16 * 128;
 #pragma unroll
-      for (int q = 0; q < STEPS; ++q) {
-        const bool in = s + q < s1 && 32 * (s + q) + 8 * h < a.k;
-        const bf16x8 z = zero_bf16x8();
-        bf16x8 xq[MR];
+      for (int q = 0; q < 2; ++q) {
+        const uint8_t *at = from + 16 * ((4 * q + h) ^ (r16 >> 1));
 #pragma unroll
-        for (int m = 0; m < MR; ++m) xq[m] = in ? xv[q][m] : z;
+        for (int m = 0; m < MR; ++m) xv[q][m] = *reinterpret_cast<const bf16x8 *>(at + 2048 * m);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const bf16x8 wq = in ? wv[q][i] : z;
+        for (int i = 0; i < RT; ++i) wv[q][i] = *reinterpret_cast<const bf16x8 *>(at + 2048 * (MR + i));
+      }
+      if (64 * s + 64 > a.k) {
 #pragma unroll
-          for (int m = 0; m < MR; ++m)
-            acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xq[m], wq, acc[i][m], 0, 0, 0);
+        for (int q = 0; q < 2; ++q) {
+          const bool in = 64 * s + 32 * q + 8 * h < a.k;
+          const bf16x8 z = zero_bf16x8();
+#pragma unroll
+          for (int m = 0; m < MR; ++m) xv[q][m] = in ? xv[q][m] : z;
+#pragma unroll
+          for (int i = 0; i < RT; ++i) wv[q][i] = in ? wv[q][i] : z;
         }
       }
+      fp4q_gemm::wait_lgkmcnt0();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_sched_barrier(0);
+      if (s + NS < s1) load(s + NS, slot);
+      slot = slot == NS - 1 ? 0 : slot + 1;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int m = 0; m < MR; ++m)
+            acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[q][m], wv[q][i], acc[i][m], 0, 0, 0);
     }
+    // the waves' sums [wave][tile][lane], in the part of the LDS that the wave itself used
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);
+    constexpr int WAVE_PART = NS * STAGE / 16;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int m = 0; m < MR; ++m) part[wave][i * MR + m][lane] = acc[i][m];
+      for (int m = 0; m < MR; ++m) part[wave * WAVE_PART + (i * MR + m) * 64 + lane] = acc[i][m];
     __syncthreads();
     const float scale = PARTS && a.scales ? a.scales[t.group] : 1.0f;
     for (int i = wave; i < RT * MR; i += WAVES) {
-      f32x4 sum = part[0][i][lane];
+      f32x4 sum = part[i * 64 + lane];
 #pragma unroll
-      for (int q = 1; q < WAVES; ++q) sum += part[q][i][lane];
+      for (int q = 1; q < WAVES; ++q) sum += part[q * WAVE_PART + i * 64 + lane];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int to = t.lo + 16 * (i % MR) + 4 * h + v, r = 16 * (i / MR) + r16;
@@ -170,53 +210,39 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(LoraArgs a) {
     Status{a.status, true}.report(err);
 }
 
-// A lane's 16 columns of a wave's 64, in runs of 16 bytes whose neighbours the lanes of the same row have: register v
-// of tile i of lane quarter h holds column 16 i + 4 h + v in float32, 32 (i / 2) + 8 h + 4 (i % 2) + v in bfloat16.
+// Four consecutive values of a row.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 template <typename O>
-__device__ __forceinline__ int column_of(int i, int h) {
-  return sizeof(O) == 4 ? 16 * i + 4 * h : 32 * (i >> 1) + 8 * h + 4 * (i & 1);
-}
-struct LaneRow {
-  u32x4 q[4];  // 16 float32, or in the first two 16 bfloat16
+struct Four;
+template <>
+struct Four<float> {
+  f32x4 v;
+  __device__ __forceinline__ float at(int i) const { return v[i]; }
 };
-template <typename O>
-__device__ __forceinline__ LaneRow load_lane(const O *p, int h) {
-  LaneRow r;
-#pragma unroll
-  for (int i = 0; i < 16 / (16 / (int)sizeof(O)); ++i)
-    r.q[i] = *reinterpret_cast<const u32x4 *>(p + column_of<O>(sizeof(O) == 4 ? i : 2 * i, h));
-  return r;
+template <>
+struct Four<uint16_t> {
+  u32x2 v;
+  __device__ __forceinline__ float at(int i) const { return as_f(i % 2 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16); }
+};
+__device__ __forceinline__ void store_four(float *p, const float z[4]) {
+  *reinterpret_cast<f32x4 *>(p) = f32x4{z[0], z[1], z[2], z[3]};
 }
-__device__ __forceinline__ float lane_item(const LaneRow &r, float *, int k) { return as_f(r.q[k / 4][k % 4]); }
-__device__ __forceinline__ float lane_item(const LaneRow &r, uint16_t *, int k) {
-  const uint32_t w = r.q[k / 8][k / 2 % 4];
-  return k % 2 ? as_f(w & 0xFFFF0000u) : as_f(w << 16);
-}
-__device__ __forceinline__ void store_lane(float *p, int h, const float z[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<f32x4 *>(p + column_of<float>(i, h)) = f32x4{z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]};
-}
-__device__ __forceinline__ void store_lane(uint16_t *p, int h, const float z[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    u32x4 w;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = fp4q_gemm::f32x2_to_bf16x2(z[8 * i + 2 * j], z[8 * i + 2 * j + 1]);
-    *reinterpret_cast<u32x4 *>(p + column_of<uint16_t>(2 * i, h)) = w;
-  }
+__device__ __forceinline__ void store_four(uint16_t *p, const float z[4]) {
+  *reinterpret_cast<u32x2 *>(p) = u32x2{fp4q_gemm::f32x2_to_bf16x2(z[0], z[1]), fp4q_gemm::f32x2_to_bf16x2(z[2], z[3])};
 }
 __device__ __forceinline__ float load1(const uint16_t *p) { return as_f((uint32_t)*p << 16); }
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 
 // RK steps of 32 ranks; ROWS rows (a multiple of 16) a workgroup.  SUMS: u is float32 sums of several workgroups, added
-// and split here; else its parts, one run of memory, go straight to LDS.  Everything that a wave reads is asked for at
-// once: its rows of y, u, and its columns of B.
+// and split here; else its parts, one run of memory, go straight to LDS.  So do a wave's 64 columns of B, up to 128 ranks
+// at a time, on their way to its registers, and everything that a wave reads is asked for at once.
 template <int RK, int ROWS, bool SUMS, typename O>
 __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
   constexpr int PARTS = sizeof(O) == 4 ? 3 : 2, TILES = ROWS / 16;
   constexpr int PART_BYTES = (ROWS * (32 * RK + 8) * 2 + 1023) / 1024 * 1024;  // LDS of a part, at most
-  __shared__ __attribute__((aligned(1024))) uint8_t u_lds[SUMS ? 16 : PARTS * PART_BYTES];
+  constexpr int MOST_B = ROWS == 16 ? 4 : 2, BK = RK < MOST_B ? RK : MOST_B;  // steps of B a round
+  constexpr int B_BYTES = 4096 * BK;                                          // LDS of a wave's
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[PARTS * PART_BYTES + kLoraWaves * B_BYTES];
   const int lane = threadIdx.x & 63, wave = wave_index(), r16 = lane & 15, h = lane >> 4;
   RowTile t = find_tile(a.groups, ROWS, (int)(blockIdx.x / a.tiles_n));
   const bool rest = t.group < 0;  // rows of no group
@@ -228,54 +254,109 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
     t.lo = (int)first;
     t.hi = a.groups.entries - t.lo > ROWS ? t.lo + ROWS : a.groups.entries;
   }
-  const int stride = part_stride(a.rank);
-  if (!SUMS && !rest) {
-    const int pieces = (ROWS * stride * 2 + 1023) / 1024;  // of 1 KB
+  const int n0 = (int)(blockIdx.x % a.tiles_n) * 64 * kLoraWaves + 64 * wave;
+  const bool live = n0 < a.n;
+  // Slot c / (4 BK) of a wave's part of LDS holds column 4 q + i of tile i, q = slot % 16, whose 16-byte pieces lie so
+  // that the 16 columns read at once fall on all banks; pieces past the rank are its last one again, and not used.
+  auto shuffle = [](int q) { return BK == 1 ? q >> 2 & 3 : (BK == 2 ? q >> 1 & 7 : q); };
+  uint8_t *b_lds = lds + PARTS * PART_BYTES + wave * B_BYTES;
+  const uint16_t *w = a.b + ((int64_t)t.group * a.n + n0) * a.rank;
+  auto load_b = [&](int round) {
+    const int most = a.n - 1 - n0, pieces = a.rank / 8;
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-      const uint8_t *src = (const uint8_t *)a.u + 2 * (q * part_size(a.groups.entries, a.rank) + (int64_t)t.lo * stride);
-      for (int c = wave; c < pieces; c += kLoraWaves) {
-        // the last piece ends with the tile's rows: lanes past them load its first bytes again
-        const int at = 1024 * c + 16 * lane;
-        fp4q_gemm::load_lds16(src + (at < ROWS * stride * 2 ? at : 0), u_lds + q * PART_BYTES + 1024 * c);
+    for (int j = 0; j < 4 * BK; ++j) {
+      const int slot = 16 / BK * j + lane / (4 * BK), q = slot & 15, col = 4 * q + (slot >> 4);
+      const int piece = 4 * BK * round + ((lane & (4 * BK - 1)) ^ shuffle(q));
+      fp4q_gemm::load_lds16(w + (col < most ? col : most) * a.rank + 8 * (piece < pieces ? piece : pieces - 1),
+                            b_lds + 1024 * j);
+    }
+  };
+  if (live && !rest) load_b(0);
+  // this lane's rows of tile m, 4 h + v of its 16, and its columns, 4 r16 + i of the wave's 64
+  const int row0 = t.lo + lane, here = entry_at(a.groups, row0 < t.hi ? row0 : t.hi - 1);
+  const int stride = part_stride(a.rank);
+  if (!rest) {
+    if constexpr (SUMS) {
+      const float scale = a.scales ? a.scales[t.group] : 1.0f;
+      const int fours = (t.hi - t.lo) * a.rank / 4;
+      for (int c = threadIdx.x; c < fours; c += kLoraThreads) {
+        const float *at = (const float *)a.u + (int64_t)t.lo * a.rank + 4 * c;
+        f32x4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < a.splits) v[q] = *reinterpret_cast<const f32x4 *>(at + (int64_t)q * a.groups.entries * a.rank);
+        f32x4 sum = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+          if (q < a.splits) sum += v[q];
+        uint16_t z[4][PARTS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts_of<PARTS>(sum[i] * scale, z[i]);
+        const int row = (int)((uint32_t)(4 * c) / (uint32_t)a.rank), to = 2 * (4 * c + 8 * row);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+          *reinterpret_cast<u32x2 *>(lds + i * PART_BYTES + to) =
+              u32x2{z[0][i] | (uint32_t)z[1][i] << 16, z[2][i] | (uint32_t)z[3][i] << 16};
+      }
+    } else {
+      const int pieces = (ROWS * stride * 2 + 1023) / 1024;  // of 1 KB
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        const uint8_t *src =
+            (const uint8_t *)a.u + 2 * (q * part_size(a.groups.entries, a.rank) + (int64_t)t.lo * stride);
+        for (int c = wave; c < pieces; c += kLoraWaves) {
+          // the last piece ends with the tile's rows: lanes past them load its first bytes again
+          const int at = 1024 * c + 16 * lane;
+          fp4q_gemm::load_lds16(src + (at < ROWS * stride * 2 ? at : 0), lds + q * PART_BYTES + 1024 * c);
+        }
       }
     }
   }
-  const int n0 = (int)(blockIdx.x % a.tiles_n) * 64 * kLoraWaves + 64 * wave;
-  const bool live = n0 < a.n, whole = a.wide && n0 + 64 <= a.n;
-  int entry[TILES];  // of this lane's row in each 16; -1: none
+  int entry[TILES][4];
 #pragma unroll
-  for (int i = 0; i < TILES; ++i) {
-    const int row = t.lo + 16 * i + r16;
-    entry[i] = entry_at(a.groups, row < t.hi ? row : t.hi - 1);
-    if (row >= t.hi) entry[i] |= -2147483647 - 1;  // read again, not stored
-  }
-  const O *y = (const O *)a.y + n0;
-  O *out = (O *)a.out + n0;
-  auto row_of = [&](int i) { return entry[i] == -1 ? 0 : entry[i] & 2147483647; };
-  LaneRow old[TILES];
+  for (int m = 0; m < TILES; ++m)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) entry[m][v] = __shfl(here, 16 * m + 4 * h + v);
+  const int c0 = n0 + 4 * r16;
+  const bool whole = a.wide && c0 + 4 <= a.n;
+  const O *y = (const O *)a.y + c0;
+  O *out = (O *)a.out + c0;
+  Four<O> old[TILES][4];
   if (whole) {
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) old[i] = load_lane(y + (int64_t)row_of(i) * a.ld_y, h);
+    for (int m = 0; m < TILES; ++m)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        old[m][v].v = *reinterpret_cast<const decltype(Four<O>::v) *>(y + (entry[m][v] < 0 ? 0 : entry[m][v]) * a.ld_y);
   }
-  bf16x8 b[4][RK];
-  float scale = 1.0f;
+  __syncthreads();  // u and B have landed
+  if (!live) return;
   bool in[RK];  // whether this lane's piece of a step lies within the rank
 #pragma unroll
   for (int s = 0; s < RK; ++s) in[s] = 32 * s + 8 * h < a.rank;
+  bf16x8 b[4][RK];
   if (!rest) {
-    if (SUMS && a.scales) scale = a.scales[t.group];
-    const uint16_t *w = a.b + (int64_t)t.group * a.n * a.rank;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = n0 + column_of<O>(i, r16 >> 2) + (r16 & 3);
-      const uint16_t *row = w + (int64_t)(col < a.n ? col : a.n - 1) * a.rank + 8 * h;
+    for (int round = 0; round < RK / BK; ++round) {
 #pragma unroll
-      for (int s = 0; s < RK; ++s) b[i][s] = in[s] ? load_bf16x8(row + 32 * s) : zero_bf16x8();
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int s = 0; s < BK; ++s) {
+          const bf16x8 z = *reinterpret_cast<const bf16x8 *>(b_lds + (16 * i + r16) * 64 * BK +
+                                                             16 * ((4 * s + h) ^ shuffle(r16)));
+          b[i][BK * round + s] = in[BK * round + s] ? z : zero_bf16x8();
+        }
+      if (round + 1 < RK / BK) {
+        fp4q_gemm::wait_lgkmcnt0();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_sched_barrier(0);
+        load_b(round + 1);
+        fp4q_gemm::wait_vmcnt<0>();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
-  if constexpr (!SUMS) __syncthreads();  // u has landed
-  if (!live) return;
 #pragma unroll
   for (int m = 0; m < TILES; ++m) {
     if (t.lo + 16 * m >= t.hi) break;
@@ -286,58 +367,32 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
 #pragma unroll
       for (int s = 0; s < RK; ++s) {
         bf16x8 u[PARTS];
-        if constexpr (SUMS) {
-          const int row = t.lo + 16 * m + r16, p = row < t.hi ? row : t.hi - 1;
-          float v[8];
+        // past the rank: the next row's numbers or the padding, which are no numbers of this row
+        const uint8_t *at = lds + ((16 * m + r16) * stride + 32 * s + 8 * h) * 2;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-          if (in[s])
-            for (int q = 0; q < a.splits; ++q) {
-              const f32x4 *at = reinterpret_cast<const f32x4 *>(
-                  (const float *)a.u + ((int64_t)q * a.groups.entries + p) * a.rank + 32 * s + 8 * h);
-              const f32x4 u0 = at[0], u1 = at[1];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                v[j] += u0[j];
-                v[4 + j] += u1[j];
-              }
-            }
-          uint32_t w[PARTS][4];
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            uint16_t q0[PARTS], q1[PARTS];
-            parts_of<PARTS>(v[j] * scale, q0);
-            parts_of<PARTS>(v[j + 1] * scale, q1);
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) w[i][j / 2] = q0[i] | (uint32_t)q1[i] << 16;
-          }
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i) u[i] = __builtin_bit_cast(bf16x8, u32x4{w[i][0], w[i][1], w[i][2], w[i][3]});
-        } else {
-          // past the rank: the next row's numbers or the padding, which are no numbers of this row
-          const uint8_t *at = u_lds + ((16 * m + r16) * stride + 32 * s + 8 * h) * 2;
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i)
-            u[i] = in[s] ? *reinterpret_cast<const bf16x8 *>(at + i * PART_BYTES) : zero_bf16x8();
-        }
+        for (int i = 0; i < PARTS; ++i)
+          u[i] = in[s] ? *reinterpret_cast<const bf16x8 *>(at + i * PART_BYTES) : zero_bf16x8();
 #pragma unroll
         for (int q = PARTS - 1; q >= 0; --q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][s], u[q], acc[i], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[q], b[i][s], acc[i], 0, 0, 0);
       }
     }
-    O *to = out + (int64_t)row_of(m) * a.ld_out;
-    if (whole) {
-      float z[16];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) z[k] = lane_item(old[m], (O *)nullptr, k) + acc[k / 4][k % 4];
-      if (entry[m] >= 0) store_lane(to, h, z);
-    } else {
-      const O *from = y + (int64_t)row_of(m) * a.ld_y;
+    for (int v = 0; v < 4; ++v) {
+      const int e = entry[m][v];
+      if (e < 0 || t.lo + 16 * m + 4 * h + v >= t.hi) continue;
+      O *to = out + e * a.ld_out;
+      if (whole) {
+        float z[4];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int c = column_of<O>(k / 4, h) + k % 4;
-        if (entry[m] >= 0 && n0 + c < a.n) fp4q_gemm::store_out(to + c, load1(from + c) + acc[k / 4][k % 4]);
+        for (int i = 0; i < 4; ++i) z[i] = old[m][v].at(i) + acc[i][v];
+        store_four(to, z);
+      } else {
+        const O *from = y + e * a.ld_y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c0 + i < a.n) fp4q_gemm::store_out(to + i, load1(from + i) + acc[i][v]);
       }
     }
   }
@@ -388,7 +443,7 @@ extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_
     return FP4Q_ERR_ALIGN;
   if (out == y && ld_out != ld_y) return FP4Q_ERR_ARG;
   const LoraPlan p = lora_plan(entries, groups->groups, k);
-  const bool wide = kv_aligned(y, 16) && kv_aligned(out, 16) && ld_y * size % 16 == 0 && ld_out * size % 16 == 0;
+  const bool wide = kv_aligned(y, 4 * size) && kv_aligned(out, 4 * size) && ld_y % 4 == 0 && ld_out % 4 == 0;
   const LoraArgs l{y, (const uint16_t *)x, (const uint16_t *)a, (const uint16_t *)b, scales, out, ld_y, ld_x, ld_out,
                    groups_of(*groups), (int)n, (int)k, (int)rank, (int)p.splits, (int)ceil_div(n, 64 * kLoraWaves),
                    out == y, wide, (char *)workspace + 256, status};
@@ -398,9 +453,10 @@ extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_
   const int64_t shrink_tiles = most_tiles(entries, groups->groups, 16 * mr);
   if (tiles > kMaxTiles || shrink_tiles > kMaxTiles) return FP4Q_ERR_SHAPE;
   auto shrink = [&](auto rt) {
-    constexpr int RT = decltype(rt)::value, W = RT == 16 ? 4 : 8, MR = RT <= 4 ? 2 : 1;
-    auto kernel = p.splits > 1 ? shrink_kernel<RT, 1, W, 0>
-                               : (dtype == FP4Q_F32 ? shrink_kernel<RT, MR, W, 3> : shrink_kernel<RT, MR, W, 2>);
+    constexpr int RT = decltype(rt)::value, MR = RT <= 4 ? 2 : 1;
+    constexpr int W = 4, NS = RT <= 2 ? 4 : (RT == 4 ? 3 : (RT == 8 ? 2 : 1)), SPLIT_NS = RT <= 4 ? 2 : 1;
+    auto kernel = p.splits > 1 ? shrink_kernel<RT, 1, W, SPLIT_NS, 0>
+                               : (dtype == FP4Q_F32 ? shrink_kernel<RT, MR, W, NS, 3> : shrink_kernel<RT, MR, W, NS, 2>);
     hipLaunchKernelGGL(kernel, dim3((unsigned)shrink_tiles, (unsigned)p.splits), dim3(64 * W), 0, s, l);
   };
   if (rank <= 16) shrink(std::integral_constant<int, 1>{});
@@ -412,7 +468,7 @@ extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_
     constexpr int RK = decltype(rk)::value;
     auto go = [&](auto op) {
       using O = std::remove_pointer_t<decltype(op)>;
-      constexpr int MOST = sizeof(O) == 4 || RK == 8 ? 32 : 64;
+      constexpr int MOST = sizeof(O) == 4 || RK >= 4 ? 32 : 64;
       auto kernel = p.splits > 1 ? (rows == 16 ? expand_kernel<RK, 16, true, O> : expand_kernel<RK, MOST, true, O>)
                                  : (rows == 16 ? expand_kernel<RK, 16, false, O> : expand_kernel<RK, MOST, false, O>);
       hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kLoraThreads), 0, s, l);

@@ -1003,6 +1003,8 @@ _FLOATS = {torch.float32: L.F32, torch.bfloat16: L.BF16}
 
 def _groups_struct(groups, device):
     """fp4q_row_groups_t, packed, its groups and its entries."""
+    if not isinstance(groups, tuple) or len(groups) != 2:
+        raise ValueError("groups must be RowGroups")
     offsets, rows = groups
     for t in groups:
         if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.device != device
@@ -1092,6 +1094,8 @@ def route_experts(logits, top_k, *, score="softmax", bias=None, n_groups=1, top_
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     bias_ptr = 0
     if bias is not None:
+        if not isinstance(bias, torch.Tensor):
+            raise ValueError("bias must be a tensor of one entry per expert")
         if bias.dtype is not torch.float32 or bias.device != dev or not bias.is_contiguous():
             bias = bias.to(device=dev, dtype=torch.float32).contiguous()
         if bias.shape != (experts,):

@@ -41,7 +41,8 @@ extern "C" {
  *           rows[offsets[g + 1] - 1]; offsets[0] is 0, and they do not decrease.
  *   rows    [entries]  the entries' numbers, each once: by group, ascending
  *           within a group, those of no group last (also ascending).
- *   groups  1 .. 65536;  entries  0 .. 2^30. */
+ *   groups  1 .. 2048;  entries  0 .. 2^30.
+ * Rows of results of an entry that is listed twice are unspecified. */
 typedef struct fp4q_row_groups {
   const int32_t *offsets, *rows;
   int64_t groups, entries;
@@ -137,7 +138,9 @@ fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const uint8_t *a_s
  *            be out itself.
  *   out, out_dtype  [tokens] rows of n, ld_out apart; it must not overlap y.
  * float32 sums in the order of j, add last, rounded once.  top_k 1 .. 64.
- * Pointers aligned to their type. */
+ * Pointers aligned to their type.  Where the rows of y, add and out are all
+ * 16-byte aligned and n is a multiple of 8, a call of 2^24 or more pieces of
+ * 2048 columns, else of 256, is refused with FP4Q_ERR_SHAPE. */
 fp4q_status_t fp4q_combine_experts(const void *y, fp4q_dtype_t dtype, int64_t tokens, int64_t top_k, int64_t n,
                                    int64_t ld_y, const float *weights, const int32_t *chosen, const void *add,
                                    int64_t ld_add, fp4q_dtype_t out_dtype, void *out, int64_t ld_out, void *stream);
@@ -159,7 +162,8 @@ fp4q_status_t fp4q_combine_experts(const void *y, fp4q_dtype_t dtype, int64_t to
  * its 24 bits, for a bfloat16 result as two that are off by 2^-17 of it; one
  * rounding at the end.  Elements of b that are not finite
  * give infinities or NaN in their column.  The order of a sum depends on the
- * sizes alone. */
+ * sizes alone.  A call of more than 2^22 tiles (of 16 rows or more and 256
+ * columns) is refused with FP4Q_ERR_SHAPE. */
 fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_t ld_y, const void *x, int64_t ld_x,
                             const void *a, const void *b, const float *scales, const fp4q_row_groups_t *groups,
                             int64_t n, int64_t k, int64_t rank, void *out, int64_t ld_out, void *workspace,

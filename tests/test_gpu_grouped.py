@@ -335,6 +335,28 @@ def test_grouped_product_with_bad_groups_stays_inside(tokens, k, n):
             assert (big[:64] == 3.0).all() and (big[64 + entries:] == 3.0).all()
 
 
+@pytest.mark.parametrize("rows,groups,k,n", [(2 ** 21 + 77, 2, 4096, 32), (300, 3, 4096, 2 ** 20 - 24)])
+def test_grouped_product_past_4_gib(rows, groups, k, n):
+    """Rows of A, and matrices of B, that begin more than 2^32 bytes from the first."""
+    fq = _fq()
+    g = torch.Generator(device=DEV).manual_seed(3)
+    held = lambda r: (torch.randint(0, 256, (r, k // 2), generator=g, dtype=torch.uint8, device=DEV),
+                      torch.randint(122, 129, (r, k // 32), generator=g, dtype=torch.uint8, device=DEV))
+    a, b = held(rows), held(groups * n)
+    ids = (torch.arange(rows, device=DEV) % groups).int()
+    gr = fq.group_rows(ids, groups)
+    out = fq.gemm_mxfp4_grouped(a, (b[0].view(groups, n, -1), b[1].view(groups, n, -1)), gr, gather=1, scatter=True,
+                                out_dtype=torch.bfloat16, check=True)
+    pick = sorted({0, 1, 2, 150, rows // 2, rows - 2, rows - 1})
+    cols = sorted({0, 1, 17, n // 2, n - 2, n - 1})
+    hat = lambda t, i: GM.decode_mxfp4_64(_np(t[0][i]), _np(t[1][i]))
+    ah = hat(a, pick)
+    for i, e in enumerate(pick):
+        bh = hat(b, [int(ids[e]) * n + c for c in cols])
+        ref, mag = bh @ ah[i], np.abs(bh) @ np.abs(ah[i])
+        _within(out[e, cols], ref, _product_tol(ref[None], mag[None], k, False)[1][0], torch.bfloat16)
+
+
 def test_grouped_product_empty():
     fq = _fq()
     z = torch.zeros(0, dtype=torch.int32, device=DEV)
@@ -379,6 +401,8 @@ LORA = [  # rows, adapters, rank, k, n, none
     (1, 1, 16, 512, 256, 0.0), (1, 3, 8, 40, 7, 1.0), (5, 3, 8, 1000, 100, 0.4), (64, 32, 16, 4096, 512, 0.2),
     (64, 1, 64, 1024, 300, 0.0), (200, 3, 24, 2040, 130, 0.3), (300, 2, 128, 256, 640, 0.1), (1000, 5, 40, 768, 264, 0.2),
     (700, 1, 256, 512, 72, 0.0), (2000, 7, 16, 128, 1000, 0.5), (90, 100, 200, 64, 64, 0.2),
+    # K shared by several workgroups whose rows the second kernel takes many at a time
+    (700, 1, 64, 2048, 200, 0.1), (300, 1, 128, 4088, 96, 0.0), (400, 1, 208, 2040, 70, 0.3), (500, 2, 8, 1600, 516, 0.2),
 ]
 
 
@@ -409,6 +433,33 @@ def test_lora_add(rows, adapters, rank, k, n, none, dtype):
     view.copy_(yd)
     same = fq.lora_add(view, xd, ad, bd, gr, scales=sc.to(DEV), out=view, check=True)
     assert same is view and torch.equal(view, got) and (big[:, 0] == 5.0).all() and (big[:, n + 1:] == 5.0).all()
+
+
+def test_strided_broadcast_and_unaligned_operands():
+    """Views that the calls read in place or copy: the result of dense ones."""
+    fq = _fq()
+    g = torch.Generator().manual_seed(12)
+    w, ids = torch.rand(9, 3, generator=g).to(DEV), torch.randint(-1, 4, (9, 3), generator=g, dtype=torch.int32).to(DEV)
+    big = torch.randn(9, 3, 80, generator=g).to(DEV)
+    for y in (big[:, :, 3:43], big[:, :, 8:72], big.transpose(0, 1).contiguous().transpose(0, 1), big[:, :1].expand(9, 3, 80),
+              big[..., ::2]):
+        assert torch.equal(fq.combine_experts(y, w, ids), fq.combine_experts(y.contiguous(), w, ids))
+    assert torch.equal(fq.combine_experts(big[:, :1, :40], w[:, :1].contiguous()),
+                       fq.combine_experts(big[:, :1, :40].contiguous(), w[:, :1].contiguous()))
+    x = torch.randn(300, 201, generator=g).bfloat16().to(DEV)
+    a, b = torch.randn(2, 16, 128, generator=g).bfloat16().to(DEV), torch.randn(2, 96, 16, generator=g).bfloat16().to(DEV)
+    gr = fq.group_rows((torch.arange(300, device=DEV) % 3 - 1).int(), 2)
+    y = torch.randn(96, generator=g).to(DEV)
+    for v in (x[:, 1:129], x[:, 8:136], x[:1, :128].expand(300, 128), x[:, :128].t().contiguous().t()):
+        got = fq.lora_add(y.expand(300, 96), v, a, b, gr, check=True)
+        assert torch.equal(got, fq.lora_add(y.repeat(300, 1), v.contiguous(), a, b, gr))
+    codes = torch.randint(0, 256, (40, 96), generator=g, dtype=torch.uint8).to(DEV)
+    scales = torch.randint(122, 129, (40, 8), generator=g, dtype=torch.uint8).to(DEV)
+    m = (torch.randint(0, 256, (2, 24, 64), generator=g, dtype=torch.uint8).to(DEV),
+         torch.randint(122, 129, (2, 24, 4), generator=g, dtype=torch.uint8).to(DEV))
+    gr = fq.group_rows((torch.arange(40, device=DEV) % 2).int(), 2)
+    got = fq.gemm_mxfp4_grouped((codes[:, 16:80], scales[:, 2:6]), m, gr, check=True)
+    assert torch.equal(got, fq.gemm_mxfp4_grouped((codes[:, 16:80].contiguous(), scales[:, 2:6].contiguous()), m, gr))
 
 
 def test_lora_add_keeps_non_finite_rows_to_themselves():
@@ -567,7 +618,8 @@ def test_refusals_of_the_binding_on_device_tensors():
     x = torch.zeros(6, 64, device=DEV)
     gr = fq.RowGroups(torch.tensor([0, 3, 6], dtype=torch.int32, device=DEV),
                       torch.arange(6, dtype=torch.int32, device=DEV))
-    for bad in (dict(top_k=0), dict(top_k=65), dict(top_k=2, score="relu"), dict(top_k=2, bias=torch.zeros(3, device=DEV))):
+    for bad in (dict(top_k=0), dict(top_k=65), dict(top_k=2, score="relu"), dict(top_k=2, bias=torch.zeros(3, device=DEV)),
+                dict(top_k=2, bias=[0.0] * 64)):
         with pytest.raises(ValueError):
             fq.route_experts(x, **bad)
     with pytest.raises(ValueError):
@@ -582,6 +634,9 @@ def test_refusals_of_the_binding_on_device_tensors():
     a = fq.quantize_mxfp4(x)
     b = (torch.zeros(2, 32, 32, dtype=torch.uint8, device=DEV), torch.zeros(2, 32, 2, dtype=torch.uint8, device=DEV))
     fq.gemm_mxfp4_grouped(a, b, gr, check=True)
+    for bad in (None, gr.rows, (gr.offsets.long(), gr.rows), (gr.offsets, gr.rows.cpu()), (gr.offsets, gr.rows[::2])):
+        with pytest.raises(ValueError):
+            fq.gemm_mxfp4_grouped(a, b, bad)
     for bad in ((b[0][:1], b[1][:1]), (b[0], b[1][:1]), (b[0][:, :, :16].contiguous(), b[1]), (b[0].int(), b[1])):
         with pytest.raises(ValueError):
             fq.gemm_mxfp4_grouped(a, bad, gr)

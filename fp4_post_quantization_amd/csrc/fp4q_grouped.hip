@@ -1,7 +1,14 @@
 // Grouped MXFP4 products: every entry's row times its group's matrix
 // (include/fp4q_grouped.h), on gfx950's scaled FP4 matrix cores.
 //
-// A tile is rows of one group times columns of its matrix.
+// A tile is rows of one group times columns of its matrix.  Few rows a group are
+// bound by the matrices' bytes: 16 tokens of 128 experts, 8 each, gate and up
+// rows of 4096 x 1536 read 276 MB in 44 us (6.2 TB/s, part of it from the last
+// level cache).  Many are bound by the steps of the LDS ring, as in the plain
+// product, and by rows that fill no tile: 4096 tokens (256 rows a group on
+// average, 1.5 tiles of 256) 204 us, 2.0 PFLOP/s of the entries' products and 3
+// of the tiles'; 8192 tokens of 8 experts, two each, on 4096 x 4096 199 us, 2.8
+// PFLOP/s.  product_tiles() chooses the kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -43,7 +50,9 @@ __device__ __forceinline__ int a_row(const GroupedArgs &a, int p, int e) {
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // Any k that is a multiple of 32: 64 rows times 128 rows of B (gated: 64 gates and their 64 ups), registers to a
-// padded LDS double buffer, 128 elements of K a stage, the tail filled with zeros.
+// padded LDS double buffer, 128 elements of K a stage, the tail filled with zeros.  For K below 256, which the ring's
+// stages do not fit, and for matrices or rows of A past 4 GiB, whose offsets it does not hold (2^21 rows of K 4096 on
+// N 32: reading A bounds it there as well).
 constexpr int kAnyThreads = 256, kAnyRowBytes = 80;
 
 template <typename OutT, bool GATED>
@@ -162,8 +171,8 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
 // tile; rows are unpadded and swizzled; K step ks takes, in lane half h, the 32-element block h KS + ks of the stage,
 // so that a lane's scale bytes of a stage are one word, of which the instruction selects byte ks.  What differs is
 // where rows come from: a lane loads the entry numbers of the rows that it stages once, before the loop.
-// TAIL, where K is no multiple of 256: chunks past a row's end are loaded from zeros, and scales, whose rows need not be
-// aligned, come through registers.
+// TAIL, where K is no multiple of 256: chunks past a row's end are loaded from zeros, and scales, whose rows need not
+// be aligned, come through registers.
 //
 // Gated: block column j of a wave is gates for even j and the ups of the same columns for odd j, so that both meet in
 // a lane's registers.
@@ -232,7 +241,8 @@ template <typename OutT, bool GATED, bool TAIL, int NS, int WGM, int WGN, int TM
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArgs a) {
   using S = RingShape<OutT, GATED, WGM, WGN, TM, TN>;
   static_assert(!TAIL || NS == 2, "scales that come through registers are a stage ahead");
-  constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, BN = S::BN, CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
+  constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, BN = S::BN;
+  constexpr int CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
   constexpr int RPL = 1024 / ROWB;  // rows of a 1 KB load
   constexpr int A_INSTR = BM / RPL / WAVES, B_INSTR = BN / RPL / WAVES;
   constexpr int SA_INSTR = BM * SPR / 256, SB_INSTR = BN * SPR / 256;
@@ -245,7 +255,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
   constexpr int LOADS = A_INSTR + B_INSTR + SQ + (TAIL ? SROWS : 0);  // of a wave and stage; one without a scale load
                                                                      // fills a spare slot
   constexpr int SPARE = NS * STAGE;
-  // One array: with two, the compiler tells them apart and then waits for every load into LDS before it reads any of it.
+  // One array: with two, the compiler tells them apart and then waits for every load into LDS before it reads any.
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * STAGE + 256 + 4 * BM];
   int *row_of = reinterpret_cast<int *>(smem + NS * STAGE + 256);  // row of C, -1: not stored
 
@@ -459,7 +469,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
 #pragma unroll
     for (int j = 0; j < TN; j += JS)
 #pragma unroll
-      for (int v = 0; v < 16; v += 4) stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha, area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
+      for (int v = 0; v < 16; v += 4)
+        stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha,
+                                area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
 #pragma unroll
     for (int q = 0; q < 32 / RPI; ++q) {
       const int rr = q * RPI + lane / LPR, c = lane % LPR * VEC;
@@ -699,7 +711,8 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) fp4q_gemm::load_lds16(a_st + offA[i], base + (wave * LOADS + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) fp4q_gemm::load_lds16(b_st + offB[i], base + S::A_BYTES + (wave * LOADS + i) * 1024);
+    for (int i = 0; i < LOADS; ++i)
+      fp4q_gemm::load_lds16(b_st + offB[i], base + S::A_BYTES + (wave * LOADS + i) * 1024);
     fp4q_gemm::load_lds4(a.as + (int64_t)st * SPR + offAs, base + S::SA_OFF + 256 * wave);
     fp4q_gemm::load_lds4(Bs + (int64_t)st * SPR + offBs, base + S::SB_OFF + 256 * wave);
   };
@@ -724,15 +737,15 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
     for (int i = 0; i < TM; ++i) {
       const i32x4 v = *reinterpret_cast<const i32x4 *>(at + (wm * TM + i) * 32 * ROWB);
       o.a[i] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-      o.sa[i] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(base + S::SA_OFF + SPR * ((wm * TM + i) * 32 + l32) + 4 * h)
-                        : prev.sa[i];
+      const uint8_t *scales = base + S::SA_OFF + SPR * ((wm * TM + i) * 32 + l32) + 4 * h;
+      o.sa[i] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(scales) : prev.sa[i];
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const i32x4 v = *reinterpret_cast<const i32x4 *>(at + S::A_BYTES + (wn * TN + j) * 32 * ROWB);
       o.b[j] = i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0};
-      o.sb[j] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(base + S::SB_OFF + SPR * ((wn * TN + j) * 32 + l32) + 4 * h)
-                        : prev.sb[j];
+      const uint8_t *scales = base + S::SB_OFF + SPR * ((wn * TN + j) * 32 + l32) + 4 * h;
+      o.sb[j] = ks == 0 ? (int)*reinterpret_cast<const uint32_t *>(scales) : prev.sb[j];
     }
   };
   auto mfmas = [&](const Ops &o, auto ks_c) {
@@ -771,7 +784,9 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
 #pragma unroll
       for (int j = 0; j < TN; j += JS)
 #pragma unroll
-        for (int v = 0; v < 16; v += 4) stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha, area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
+        for (int v = 0; v < 16; v += 4)
+        stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha,
+                                area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
 #pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
         const int rr = q * RPI + ln / LPR, c = ln % LPR * VEC;
@@ -946,8 +961,8 @@ extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const u
   if (!kv_aligned(a_codes, 16) || !kv_aligned(b_codes, 16) || !kv_aligned(c, out_dtype == FP4Q_F32 ? 4 : 2))
     return FP4Q_ERR_ALIGN;
   if (k % 128 == 0 && (!kv_aligned(a_scales, 4) || !kv_aligned(b_scales, 4))) return FP4Q_ERR_ALIGN;
-  GroupedArgs a{a_codes, a_scales, b_codes, b_scales, groups_of(*groups), (int)a_rows, (int)gather, scatter, (int)n, (int)k, (int)(gated ? n / 2 : n), 0, 1,
-                alpha, c, ldc, status};
+  GroupedArgs a{a_codes, a_scales, b_codes, b_scales, groups_of(*groups), (int)a_rows, (int)gather, scatter, (int)n,
+                (int)k, (int)(gated ? n / 2 : n), 0, 1, alpha, c, ldc, status};
   bool fits = true;
   with_type(out_dtype, [&](auto op) {
     using O = std::remove_pointer_t<decltype(op)>;

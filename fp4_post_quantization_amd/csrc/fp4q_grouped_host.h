@@ -18,7 +18,9 @@ constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopK = 64;
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;  // workgroups of a launch: with 1024 threads each below 2^32 threads
 
-inline bool grouped_ws_ok(const void *ws, size_t bytes, size_t need) { return ws && bytes >= need && kv_aligned(ws, 16); }
+inline bool grouped_ws_ok(const void *ws, size_t bytes, size_t need) {
+  return ws && bytes >= need && kv_aligned(ws, 16);
+}
 
 inline fp4q_status_t grouped_check(const fp4q_row_groups_t &g) {
   if (g.groups < 1 || g.groups > kMaxRowGroups || g.entries < 0 || g.entries > kMaxEntries) return FP4Q_ERR_SHAPE;
@@ -85,6 +87,10 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
   ProductTiles t;
   const int64_t far = (int64_t)UINT32_MAX - 4096;  // the ring's kernels take 32-bit offsets into A and into a matrix
   auto tiles = [&](int rows, int cols) { return most_tiles(entries, groups, rows) * ceil_div(n, cols); };
+  // Tiles in a row to one XCD: 16 where there are many (2000 tokens of 64 experts, 704 x 2048, in runs of 4 49 us, of
+  // 16 45; 16 tokens of 128 experts 44.5 and 43.8), 4 where long runs would leave XCDs without any (one token, in runs
+  // of 64: 25 us instead of 18).
+  auto run = [&](int rows) { return tiles(rows, 128) >= 512 ? 16 : 4; };
   if (k < 256 || a_rows * (k / 2) > far || n * (k / 2) > far) {
     t = ProductTiles{kAnyTiles, kAnyRows, kAnyCols, 1, tiles(kAnyRows, kAnyCols)};
     return t;
@@ -100,20 +106,20 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
     // 117; 1000 (62 rows) 130 and 130; 1500 (94 rows) 155 and 142.  Two stages more in flight where K has many, at two
     // workgroups a CU instead of three: 46, 91, 110 and 129; 64 tokens of 8 experts on 14336 x 4096 46 and 41; 1000
     // tokens on 768 x 4096 73 and 84.
-    t = ProductTiles{k % 256 == 0 && k >= 4096 ? kDeepTiles : kRingTiles, 64, 128, 4, 0};
+    t = ProductTiles{k % 256 == 0 && k >= 4096 ? kDeepTiles : kRingTiles, 64, 128, run(64), 0};
   } else {
     const int64_t live = groups < entries ? groups : entries;
     auto rounds = [&](int64_t r, int64_t c, int64_t at_once) {  // every group's last tile half full
       return ceil_div((entries / r + live / 2) * ceil_div(n, c), at_once);
     };
-    // 256 x 256, one a CU, where it takes fewer rounds of 1.55 times the length than 128 x 128, two a CU: 2500 tokens of
-    // 128 experts (156 rows) 165 and 183; 4096 tokens (256) 212 and 262; 768 x 4096 154 and 196; 2048 rows on 4096 x 4096
-    // 200 and 243; 512 rows on 4096 x 4096 (two rounds, the second a quarter full) 75 and 68; 94 rows 157 and 142.
+    // 256 x 256, one a CU, where it takes fewer rounds of 1.55 times the length than 128 x 128, two a CU: 2500 tokens
+    // of 128 experts (156 rows) 165 and 183; 4096 tokens (256) 212 and 262; 768 x 4096 154 and 196; 2048 rows on 4096 x
+    // 4096 200 and 243; 512 rows on 4096 x 4096 (two rounds, the second a quarter full) 75 and 68; 94 rows 157 and 142.
     if (k % 256 == 0 && k >= 512 && groups <= kPersistGroups &&
         155 * rounds(256, 256, 256) <= 100 * rounds(128, 128, 512))
       t = ProductTiles{kPersistTiles, 256, 256, 16, 0};
     else
-      t = ProductTiles{kRingTiles, 128, 128, 4, 0};
+      t = ProductTiles{kRingTiles, 128, 128, run(128), 0};
   }
   t.workgroups = ceil_div(tiles(t.rows, t.cols), t.run * kXcdCount) * t.run * kXcdCount;
   if (t.kind == kPersistTiles && t.workgroups > kCus && t.workgroups <= kMaxTiles) t.workgroups = kCus;
@@ -181,7 +187,8 @@ struct LoraPlan {
 inline LoraPlan lora_plan(int64_t entries, int64_t groups, int64_t k) {
   LoraPlan p;
   p.few = entries < 64 * groups || entries <= 256;
-  const int64_t tiles = most_tiles(entries, groups, 16), steps = ceil_div(k, 32) / 16;  // at least two stages of 64 a wave
+  const int64_t tiles = most_tiles(entries, groups, 16);
+  const int64_t steps = ceil_div(k, 32) / 16;  // at least two stages of 64 a wave
   p.splits = tiles ? 256 / tiles : 1;
   if (p.splits > steps) p.splits = steps;
   if (p.splits > 8) p.splits = 8;

@@ -233,9 +233,10 @@ __device__ __forceinline__ void store_four(uint16_t *p, const float z[4]) {
 __device__ __forceinline__ float load1(const uint16_t *p) { return as_f((uint32_t)*p << 16); }
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 
-// RK steps of 32 ranks; ROWS rows (a multiple of 16) a workgroup.  SUMS: u is float32 sums of several workgroups, added
-// and split here; else its parts, one run of memory, go straight to LDS.  So do a wave's 64 columns of B, up to 128 ranks
-// at a time, on their way to its registers, and everything that a wave reads is asked for at once.
+// RK steps of 32 ranks; ROWS rows (a multiple of 16) a workgroup.  SUMS: u is float32 sums of several workgroups,
+// added and split here; else its parts, one run of memory, go straight to LDS.  So do a wave's 64 columns of B, up to
+// 128 ranks (64 beside many rows, whose u takes the room) at a time, on their way to its registers, and everything that
+// a wave reads is asked for at once.
 template <int RK, int ROWS, bool SUMS, typename O>
 __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
   constexpr int PARTS = sizeof(O) == 4 ? 3 : 2, TILES = ROWS / 16;
@@ -456,7 +457,8 @@ extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_
     constexpr int RT = decltype(rt)::value, MR = RT <= 4 ? 2 : 1;
     constexpr int W = 4, NS = RT <= 2 ? 4 : (RT == 4 ? 3 : (RT == 8 ? 2 : 1)), SPLIT_NS = RT <= 4 ? 2 : 1;
     auto kernel = p.splits > 1 ? shrink_kernel<RT, 1, W, SPLIT_NS, 0>
-                               : (dtype == FP4Q_F32 ? shrink_kernel<RT, MR, W, NS, 3> : shrink_kernel<RT, MR, W, NS, 2>);
+                 : dtype == FP4Q_F32 ? shrink_kernel<RT, MR, W, NS, 3>
+                                     : shrink_kernel<RT, MR, W, NS, 2>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)shrink_tiles, (unsigned)p.splits), dim3(64 * W), 0, s, l);
   };
   if (rank <= 16) shrink(std::integral_constant<int, 1>{});

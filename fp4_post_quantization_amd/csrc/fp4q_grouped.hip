@@ -590,8 +590,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs
 
 // ---------------------------------------------------------------------------
 // The ring in tiles of 256 x 256 for many of them (K a multiple of 256, from 512 on; up to kPersistGroups groups): one
-// workgroup a CU walks tiles blockIdx, blockIdx + gridDim, ... and loads the next tile's first stages while it finishes
-// the one before.  Started anew, a tile costs 8 us beside its stages (2.4 us for 256 elements of K): the search for its
+// workgroup a CU walks tiles gridDim apart, and loads the next tile's first stages while it finishes the one before.
+// Started anew, a tile costs 8 us beside its stages (2.4 us for 256 elements of K): the search for its
 // group, its rows' numbers, the first loads, the stores.  Here the groups' tiles are summed once into LDS, the next
 // tile's rows are asked for when a tile begins, and its loads follow the last ones of the tile without a gap.
 template <typename OutT, bool GATED>
@@ -785,8 +785,8 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
       for (int j = 0; j < TN; j += JS)
 #pragma unroll
         for (int v = 0; v < 16; v += 4)
-        stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha,
-                                area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
+          stage_four<OutT, GATED>(acc[i][j], acc[i][j + JS - 1], v, alpha,
+                                  area + l32 * EROW + j / JS * 32 + 2 * v + 4 * h);
 #pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
         const int rr = q * RPI + ln / LPR, c = ln % LPR * VEC;
@@ -809,8 +809,15 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
 
   // The issue stream runs over the stages of all this workgroup's tiles, two ahead of the MFMAs; a tile's stage g sits
   // in the slot that follows the one before.  Every wait is for all of a wave's loads (and the epilogue's stores).
-  int v = blockIdx.x;
-  Tile cur = find(v), nxt;
+  // A workgroup moves on by one within its XCD from one of its tiles to the next: where groups have two row tiles, a whole
+  // one and a remainder (which takes half as long), it would else get the same kind every time (272 rows a group 248 us,
+  // so 227; 256 on average 210 and 207).
+  int walked = 0;
+  auto number = [&](int i) {
+    const int b = (int)blockIdx.x, eighth = (int)gridDim.x / kXcdCount;
+    return i * (int)gridDim.x + (b / kXcdCount + i) % eighth * kXcdCount + b % kXcdCount;
+  };
+  Tile cur = find(number(0)), nxt;
   if (cur.group >= 0) {
     set_sources(cur, numbers(cur), 0);
     issue(0, 0);
@@ -877,8 +884,7 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
     };
 #pragma nounroll
     for (;;) {
-      v += gridDim.x;
-      nxt = find(v);
+      nxt = find(number(++walked));
       if (nxt.group >= 0) ahead = numbers(nxt);
       if (cur.lo + wm * TM * 32 < cur.hi) walk(std::true_type{});
       else walk(std::false_type{});

@@ -3,11 +3,11 @@
 //
 // A tile is rows of one group times columns of its matrix.  Few rows a group are
 // bound by the matrices' bytes: 16 tokens of 128 experts, 8 each, gate and up
-// rows of 4096 x 1536 read 276 MB in 44 us (6.2 TB/s, part of it from the last
+// rows of 4096 x 1536 read 276 MB in 43 us (6.4 TB/s, part of it from the last
 // level cache).  Many are bound by the steps of the LDS ring, as in the plain
 // product, and by rows that fill no tile: 4096 tokens (256 rows a group on
-// average, 1.5 tiles of 256) 204 us, 2.0 PFLOP/s of the entries' products and 3
-// of the tiles'; 8192 tokens of 8 experts, two each, on 4096 x 4096 199 us, 2.8
+// average, 1.5 tiles of 256) 201 us, 2.0 PFLOP/s of the entries' products and 3
+// of the tiles'; 8192 tokens of 8 experts, two each, on 4096 x 4096 195 us, 2.8
 // PFLOP/s.  product_tiles() chooses the kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

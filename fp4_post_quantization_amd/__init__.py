@@ -1007,8 +1007,8 @@ def _groups_struct(groups, device):
         raise ValueError("groups must be RowGroups")
     offsets, rows = groups
     for t in groups:
-        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.device != device
-                or not t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.ndim == 1 and t.device == device
+                and t.is_contiguous()):
             name = "offsets" if t is offsets else "rows"
             raise ValueError(f"groups.{name} must be a contiguous int32 vector on {device}")
     n, entries = offsets.shape[0] - 1, rows.shape[0]
@@ -1020,11 +1020,13 @@ def _groups_struct(groups, device):
 def _rows(t, name, device=None, dtypes=_FLOATS):
     """A [rows, columns] device tensor with dense rows that do not overlap,
     and their stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in dtypes:
+    if not isinstance(t, torch.Tensor) or t.ndim != 2 or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} is on {t.device}, must be on {device or 'a GPU'}")
     rows, cols = t.shape
+    if t.is_contiguous():
+        return t, cols
     s0, s1 = t.stride()
     if (s1 != 1 and cols > 1) or (rows > 1 and s0 < cols):
         t, s0 = t.contiguous(), cols

@@ -142,7 +142,13 @@ inline fp4q_status_t router_check(const fp4q_router_t &r, int64_t experts) {
 }
 
 constexpr int kSortChunk = 1024;  // entries that a workgroup places at a time
-constexpr int kSoloTokens = 16;   // up to which one workgroup routes and sorts
+
+// Tokens up to which one workgroup routes and sorts (one launch, which from Python saves 4 us of a call): 24 of 64 experts
+// 8.4 us on the GPU, in two launches 9.9, and where scores are compared (with a bias, in groups) 12.6 and 11.5; of 128
+// 10.2 and 10.4, scores 17.0 and 13.1; of 256 11.7 and 11.4.  16 of 128 with scores 12.8 and 13.1, of 256 16.4 and 15.2.
+inline int64_t solo_tokens(int64_t experts, bool scored) {
+  return experts <= 64 || (!scored && experts <= 256) ? 24 : 16;
+}
 
 // How entries are counted and placed.  Counting block b holds the units
 // (tokens, or entries of ids) [b per, (b + 1) per); placing block p holds

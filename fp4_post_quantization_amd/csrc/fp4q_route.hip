@@ -584,7 +584,9 @@ void with_lanes(int64_t experts, F &&f) {
 
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
 
-bool solo_route(int64_t tokens, int64_t top_k) { return tokens <= kSoloTokens && tokens * top_k <= kSortChunk; }
+bool solo_route(int64_t tokens, int64_t experts, int64_t top_k, bool scored) {
+  return tokens <= solo_tokens(experts, scored) && tokens * top_k <= kSortChunk;
+}
 bool solo_group(int64_t entries) { return entries <= 2 * kSortChunk; }
 
 }  // namespace
@@ -627,7 +629,9 @@ extern "C" size_t fp4q_route_experts_workspace_bytes(int64_t tokens, int64_t exp
   if (tokens < 0 || experts < 1 || experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK ||
       tokens > kMaxEntries / top_k)
     return 0;
-  return tokens == 0 || solo_route(tokens, top_k) ? 256 : sort_bytes(sort_plan(tokens, top_k, kRouteWaves), experts);
+  return tokens == 0 || solo_route(tokens, experts, top_k, true)
+             ? 256
+             : sort_bytes(sort_plan(tokens, top_k, kRouteWaves), experts);
 }
 
 extern "C" fp4q_status_t fp4q_route_experts(const void *logits, fp4q_dtype_t dtype, int64_t tokens, int64_t experts,
@@ -653,14 +657,14 @@ extern "C" fp4q_status_t fp4q_route_experts(const void *logits, fp4q_dtype_t dty
     hipLaunchKernelGGL(no_entries_kernel, dim3(1), dim3(kSortThreads), 0, s, offsets, (int)experts, status);
     return hip_status();
   }
-  const bool solo = solo_route(tokens, k);
+  const bool scored = router->bias || (router->n_groups > 1 && router->group_best == 2);
+  const bool solo = solo_route(tokens, experts, k, scored);
   const SortPlan p = sort_plan(tokens, k, kRouteWaves);
   uint16_t *counts = solo || !offsets ? nullptr : (uint16_t *)((char *)workspace + 256);
   const RouteArgs a{logits, ld, tokens, p.per, (int)experts, (int)k, (int)router->score, router->n_groups,
                     (int)(experts / router->n_groups), router->top_groups, router->group_best, router->renormalize,
                     router->bias, router->scale, weights, chosen, counts, status};
   const SortArgs e{chosen, tokens * k, (int)experts, counts, (int)p.blocks, (int)p.join, p.per * k, offsets, rows};
-  const bool scored = router->bias || (router->n_groups > 1 && router->group_best == 2);
   const size_t pick = router->n_groups > 1 ? (size_t)experts * (scored ? 8 : 4) : 0;  // LDS of a wave
   with_lanes(experts, [&](auto jc) {
     constexpr int J = decltype(jc)::value;

@@ -96,6 +96,18 @@ def test_route_within_groups(experts, n_groups, top_groups, k):
             _check_route(x, k, **kw)
 
 
+@pytest.mark.parametrize("experts", [60, 64, 65, 256, 300])
+def test_route_where_one_workgroup_ends(experts):
+    """Tokens around the numbers up to which one workgroup routes and sorts."""
+    g = torch.Generator().manual_seed(experts)
+    bias = (0.1 * torch.randn(experts, generator=g)).to(DEV)
+    for tokens in (8, 16, 17, 24, 25):
+        x = (1.5 * torch.randn(tokens, experts, generator=g)).to(DEV)
+        for k in (6, 50):
+            _check_route(x, k)
+            _check_route(x, k, score="sigmoid", bias=bias)
+
+
 def test_route_ties_take_the_lowest_index():
     """Equal logits (both zeros among them), equal scores with a bias, equal groups."""
     g = torch.Generator().manual_seed(3)

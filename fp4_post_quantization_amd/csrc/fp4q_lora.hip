@@ -6,10 +6,12 @@
 //
 //   shrink  u = s x A^T: 16 or 32 rows a workgroup, K shared by its four waves,
 //           and where there are few rows by several workgroups.  Their sums
-//           meet in LDS.  A row's u is taken on as bfloat16 parts, each the
-//           leading bits of what the ones before leave: three hold float32's 24
-//           bits exactly.  For a bfloat16 result two do, the second rounded:
-//           they are off by 2^-17 of u, 2^-9 of the result's own half step.
+//           meet in LDS.  A row's u is taken on as three bfloat16 parts, each
+//           the leading bits of what the ones before leave, which hold float32's
+//           24 bits exactly, whatever the result's type: where terms of u B^T,
+//           or y and u B^T, cancel, a bfloat16 result shows them too.  (Two
+//           parts, off by up to 2^-16 of u: 120 us instead of 130 for 8191 rows,
+//           rank 64, K 4096, 14336 columns.)
 //           Workgroups that share K write float32 sums instead.
 //   expand  y + u B^T, 256 columns a workgroup, 64 a wave, which keeps its part
 //           of B in registers for up to 64 rows.  Column 4 q + i of the wave's
@@ -49,7 +51,7 @@ struct LoraArgs {
   Groups groups;
   int n, k, rank, splits, tiles_n;
   bool in_place, wide;
-  void *u;  // one split: bfloat16 [parts][entries][rank]; else float32 [splits][entries][rank], without the scale
+  void *u;  // one split: bfloat16 [kParts][entries][rank]; else float32 [splits][entries][rank], without the scale
   uint32_t *status;
 };
 
@@ -60,16 +62,16 @@ __device__ __forceinline__ bf16x8 zero_bf16x8() { return __builtin_bit_cast(bf16
 
 constexpr int kLoraWaves = 4, kLoraThreads = 64 * kLoraWaves;
 
+constexpr int kParts = 3;
+
 // The leading bits of z that bfloat16 holds (cut off, so that nothing overflows and the rest is exact); infinities and
 // NaN, whose first bit is set, go into the first part alone.
-template <int PARTS>
-__device__ __forceinline__ void parts_of(float z, uint16_t p[PARTS]) {
+__device__ __forceinline__ void parts_of(float z, uint16_t p[kParts]) {
   const bool finite = __builtin_fabsf(z) < __builtin_inff();
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
+  for (int i = 0; i < kParts; ++i) {
     const uint32_t top = as_u(z) & 0xFFFF0000u;
-    const uint32_t part = PARTS == 2 && i == 1 ? (uint32_t)fp4q_gemm::f32_to_bf16_rne(z) << 16 : top;
-    p[i] = (uint16_t)((finite ? part : (i ? 0u : top | (z != z ? 0x400000u : 0u))) >> 16);
+    p[i] = (uint16_t)((finite ? top : (i ? 0u : top | (z != z ? 0x400000u : 0u))) >> 16);
     z -= as_f(top);
   }
 }
@@ -81,13 +83,13 @@ __host__ __device__ __forceinline__ int64_t part_size(int64_t entries, int rank)
   return (entries + 64) * part_stride(rank);
 }
 
-// RT tiles of 16 ranks, MR of 16 rows, WAVES that share K; PARTS bfloat16 parts, or 0: float32 sums of a share of K.
+// RT tiles of 16 ranks, MR of 16 rows, WAVES that share K; SUMS: float32 sums of a share of K, else u's parts.
 //
 // A wave copies 64 elements of K of its rows of x and of A at a time to its own part of the LDS, NS such stages in
 // flight, and reads its operands there: a load of 16 bytes a lane straight into the operand's layout has 16 rows in its
 // first 16 lanes, and such a load takes the 64 cycles of 64 lines.  16-byte piece p of row r lies at p ^ (r / 2 % 8) of
 // its 128 bytes, so that 16 rows read at once fall on all banks.
-template <int RT, int MR, int WAVES, int NS, int PARTS>
+template <int RT, int MR, int WAVES, int NS, bool SUMS>
 __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(LoraArgs a) {
   constexpr int LOADS = 2 * (MR + RT), STAGE = 1024 * LOADS;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[WAVES * NS * STAGE];
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(LoraArgs a) {
 #pragma unroll
       for (int m = 0; m < MR; ++m) part[wave * WAVE_PART + (i * MR + m) * 64 + lane] = acc[i][m];
     __syncthreads();
-    const float scale = PARTS && a.scales ? a.scales[t.group] : 1.0f;
+    const float scale = !SUMS && a.scales ? a.scales[t.group] : 1.0f;
     for (int i = wave; i < RT * MR; i += WAVES) {
       f32x4 sum = part[i * 64 + lane];
 #pragma unroll
@@ -194,13 +196,13 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(LoraArgs a) {
       for (int v = 0; v < 4; ++v) {
         const int to = t.lo + 16 * (i % MR) + 4 * h + v, r = 16 * (i / MR) + r16;
         if (to >= t.hi || r >= a.rank) continue;
-        if constexpr (PARTS == 0) {
+        if constexpr (SUMS) {
           ((float *)a.u)[((int64_t)blockIdx.y * a.groups.entries + to) * a.rank + r] = sum[v];
         } else {
-          uint16_t q[PARTS];
-          parts_of<PARTS>(sum[v] * scale, q);
+          uint16_t q[kParts];
+          parts_of(sum[v] * scale, q);
 #pragma unroll
-          for (int j = 0; j < PARTS; ++j)
+          for (int j = 0; j < kParts; ++j)
             ((uint16_t *)a.u)[j * part_size(a.groups.entries, a.rank) + (int64_t)to * part_stride(a.rank) + r] = q[j];
         }
       }
@@ -235,15 +237,20 @@ __device__ __forceinline__ float load1(const float *p) { return *p; }
 
 // RK steps of 32 ranks; ROWS rows (a multiple of 16) a workgroup.  SUMS: u is float32 sums of several workgroups,
 // added and split here; else its parts, one run of memory, go straight to LDS.  So do a wave's 64 columns of B, up to
-// 128 ranks (64 beside many rows, whose u takes the room) at a time, on their way to its registers, and everything that
-// a wave reads is asked for at once.
+// 128 ranks (64 beside many rows, whose u takes the room) at a time, on their way to its registers; but for TURNS
+// everything that a wave reads is asked for at once.
 template <int RK, int ROWS, bool SUMS, typename O>
 __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
-  constexpr int PARTS = sizeof(O) == 4 ? 3 : 2, TILES = ROWS / 16;
+  constexpr int TILES = ROWS / 16;
   constexpr int PART_BYTES = (ROWS * (32 * RK + 8) * 2 + 1023) / 1024 * 1024;  // LDS of a part, at most
   constexpr int MOST_B = ROWS == 16 ? 4 : 2, BK = RK < MOST_B ? RK : MOST_B;  // steps of B a round
   constexpr int B_BYTES = 4096 * BK;                                          // LDS of a wave's
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[PARTS * PART_BYTES + kLoraWaves * B_BYTES];
+  constexpr int U_BYTES = kParts * PART_BYTES, ALL_B = kLoraWaves * B_BYTES;
+  // Where three workgroups would not fit a CU's LDS with both, u takes B's place once B is in registers: 8191 rows of
+  // rank 64 on 14336 columns 139 -> 130 us, 2000 of rank 256 on 4096 64 -> 54.  For few rows, which a second trip to
+  // memory would cost more, and where they fit (rank 16: 36.6 us, in turns 37.7) both are asked for at once.
+  constexpr bool TURNS = ROWS > 16 && U_BYTES + ALL_B > 53 * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[!TURNS ? U_BYTES + ALL_B : (U_BYTES > ALL_B ? U_BYTES : ALL_B)];
   const int lane = threadIdx.x & 63, wave = wave_index(), r16 = lane & 15, h = lane >> 4;
   RowTile t = find_tile(a.groups, ROWS, (int)(blockIdx.x / a.tiles_n));
   const bool rest = t.group < 0;  // rows of no group
@@ -260,7 +267,7 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
   // Slot c / (4 BK) of a wave's part of LDS holds column 4 q + i of tile i, q = slot % 16, whose 16-byte pieces lie so
   // that the 16 columns read at once fall on all banks; pieces past the rank are its last one again, and not used.
   auto shuffle = [](int q) { return BK == 1 ? q >> 2 & 3 : (BK == 2 ? q >> 1 & 7 : q); };
-  uint8_t *b_lds = lds + PARTS * PART_BYTES + wave * B_BYTES;
+  uint8_t *b_lds = lds + (TURNS ? 0 : U_BYTES) + wave * B_BYTES;
   const uint16_t *w = a.b + ((int64_t)t.group * a.n + n0) * a.rank;
   auto load_b = [&](int round) {
     const int most = a.n - 1 - n0, pieces = a.rank / 8;
@@ -272,71 +279,11 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
                             b_lds + 1024 * j);
     }
   };
-  if (live && !rest) load_b(0);
-  // this lane's rows of tile m, 4 h + v of its 16, and its columns, 4 r16 + i of the wave's 64
-  const int row0 = t.lo + lane, here = entry_at(a.groups, row0 < t.hi ? row0 : t.hi - 1);
-  const int stride = part_stride(a.rank);
-  if (!rest) {
-    if constexpr (SUMS) {
-      const float scale = a.scales ? a.scales[t.group] : 1.0f;
-      const int fours = (t.hi - t.lo) * a.rank / 4;
-      for (int c = threadIdx.x; c < fours; c += kLoraThreads) {
-        const float *at = (const float *)a.u + (int64_t)t.lo * a.rank + 4 * c;
-        f32x4 v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < a.splits) v[q] = *reinterpret_cast<const f32x4 *>(at + (int64_t)q * a.groups.entries * a.rank);
-        f32x4 sum = v[0];
-#pragma unroll
-        for (int q = 1; q < 8; ++q)
-          if (q < a.splits) sum += v[q];
-        uint16_t z[4][PARTS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) parts_of<PARTS>(sum[i] * scale, z[i]);
-        const int row = (int)((uint32_t)(4 * c) / (uint32_t)a.rank), to = 2 * (4 * c + 8 * row);
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-          *reinterpret_cast<u32x2 *>(lds + i * PART_BYTES + to) =
-              u32x2{z[0][i] | (uint32_t)z[1][i] << 16, z[2][i] | (uint32_t)z[3][i] << 16};
-      }
-    } else {
-      const int pieces = (ROWS * stride * 2 + 1023) / 1024;  // of 1 KB
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        const uint8_t *src =
-            (const uint8_t *)a.u + 2 * (q * part_size(a.groups.entries, a.rank) + (int64_t)t.lo * stride);
-        for (int c = wave; c < pieces; c += kLoraWaves) {
-          // the last piece ends with the tile's rows: lanes past them load its first bytes again
-          const int at = 1024 * c + 16 * lane;
-          fp4q_gemm::load_lds16(src + (at < ROWS * stride * 2 ? at : 0), lds + q * PART_BYTES + 1024 * c);
-        }
-      }
-    }
-  }
-  int entry[TILES][4];
-#pragma unroll
-  for (int m = 0; m < TILES; ++m)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) entry[m][v] = __shfl(here, 16 * m + 4 * h + v);
-  const int c0 = n0 + 4 * r16;
-  const bool whole = a.wide && c0 + 4 <= a.n;
-  const O *y = (const O *)a.y + c0;
-  O *out = (O *)a.out + c0;
-  Four<O> old[TILES][4];
-  if (whole) {
-#pragma unroll
-    for (int m = 0; m < TILES; ++m)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        old[m][v].v = *reinterpret_cast<const decltype(Four<O>::v) *>(y + (entry[m][v] < 0 ? 0 : entry[m][v]) * a.ld_y);
-  }
-  __syncthreads();  // u and B have landed
-  if (!live) return;
   bool in[RK];  // whether this lane's piece of a step lies within the rank
 #pragma unroll
   for (int s = 0; s < RK; ++s) in[s] = 32 * s + 8 * h < a.rank;
   bf16x8 b[4][RK];
-  if (!rest) {
+  auto read_b = [&]() {
 #pragma unroll
     for (int round = 0; round < RK / BK; ++round) {
 #pragma unroll
@@ -357,6 +304,81 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+  };
+  // this lane's rows of tile m, 4 h + v of its 16, and its columns, 4 r16 + i of the wave's 64; the rows' numbers are
+  // waited for before B is asked for, whose loads they would else wait for too
+  const int row0 = t.lo + lane, here = entry_at(a.groups, row0 < t.hi ? row0 : t.hi - 1);
+  int entry[TILES][4];
+#pragma unroll
+  for (int m = 0; m < TILES; ++m)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) entry[m][v] = __shfl(here, 16 * m + 4 * h + v);
+  __builtin_amdgcn_sched_barrier(0);
+  if (live && !rest) load_b(0);
+  const int stride = part_stride(a.rank);
+  if constexpr (TURNS) {
+    if (live && !rest) {
+      fp4q_gemm::wait_vmcnt<0>();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_sched_barrier(0);
+      read_b();
+      fp4q_gemm::wait_lgkmcnt0();
+    }
+    __syncthreads();
+  }
+  if (!rest) {
+    if constexpr (SUMS) {
+      const float scale = a.scales ? a.scales[t.group] : 1.0f;
+      const int fours = (t.hi - t.lo) * a.rank / 4;
+      for (int c = threadIdx.x; c < fours; c += kLoraThreads) {
+        const float *at = (const float *)a.u + (int64_t)t.lo * a.rank + 4 * c;
+        f32x4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < a.splits) v[q] = *reinterpret_cast<const f32x4 *>(at + (int64_t)q * a.groups.entries * a.rank);
+        f32x4 sum = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+          if (q < a.splits) sum += v[q];
+        uint16_t z[4][kParts];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts_of(sum[i] * scale, z[i]);
+        const int row = (int)((uint32_t)(4 * c) / (uint32_t)a.rank), to = 2 * (4 * c + 8 * row);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          *reinterpret_cast<u32x2 *>(lds + i * PART_BYTES + to) =
+              u32x2{z[0][i] | (uint32_t)z[1][i] << 16, z[2][i] | (uint32_t)z[3][i] << 16};
+      }
+    } else {
+      const int pieces = (ROWS * stride * 2 + 1023) / 1024;  // of 1 KB
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) {
+        const uint8_t *src =
+            (const uint8_t *)a.u + 2 * (q * part_size(a.groups.entries, a.rank) + (int64_t)t.lo * stride);
+        for (int c = wave; c < pieces; c += kLoraWaves) {
+          // the last piece ends with the tile's rows: lanes past them load its first bytes again
+          const int at = 1024 * c + 16 * lane;
+          fp4q_gemm::load_lds16(src + (at < ROWS * stride * 2 ? at : 0), lds + q * PART_BYTES + 1024 * c);
+        }
+      }
+    }
+  }
+  const int c0 = n0 + 4 * r16;
+  const bool whole = a.wide && c0 + 4 <= a.n;
+  const O *y = (const O *)a.y + c0;
+  O *out = (O *)a.out + c0;
+  Four<O> old[TILES][4];
+  if (whole) {
+#pragma unroll
+    for (int m = 0; m < TILES; ++m)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        old[m][v].v = *reinterpret_cast<const decltype(Four<O>::v) *>(y + (entry[m][v] < 0 ? 0 : entry[m][v]) * a.ld_y);
+  }
+  __syncthreads();  // u and B have landed
+  if (!live) return;
+  if constexpr (!TURNS) {
+    if (!rest) read_b();
   }
 #pragma unroll
   for (int m = 0; m < TILES; ++m) {
@@ -367,14 +389,14 @@ __global__ __launch_bounds__(kLoraThreads) void expand_kernel(LoraArgs a) {
     if (!rest) {
 #pragma unroll
       for (int s = 0; s < RK; ++s) {
-        bf16x8 u[PARTS];
+        bf16x8 u[kParts];
         // past the rank: the next row's numbers or the padding, which are no numbers of this row
         const uint8_t *at = lds + ((16 * m + r16) * stride + 32 * s + 8 * h) * 2;
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i)
+        for (int i = 0; i < kParts; ++i)
           u[i] = in[s] ? *reinterpret_cast<const bf16x8 *>(at + i * PART_BYTES) : zero_bf16x8();
 #pragma unroll
-        for (int q = PARTS - 1; q >= 0; --q)
+        for (int q = kParts - 1; q >= 0; --q)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[q], b[i][s], acc[i], 0, 0, 0);
       }
@@ -414,7 +436,7 @@ extern "C" size_t fp4q_lora_add_workspace_bytes(int64_t entries, int64_t groups,
   if (lora_check_sizes(entries, groups, n, k, rank) != FP4Q_OK) return 0;
   const LoraPlan p = lora_plan(entries, groups, k);
   if (p.splits > 1) return 256 + (size_t)(p.splits * entries * rank * 4);
-  return 256 + (size_t)(3 * part_size(entries, (int)rank) * 2);
+  return 256 + (size_t)(kParts * part_size(entries, (int)rank) * 2);
 }
 
 extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_t ld_y, const void *x, int64_t ld_x,
@@ -456,9 +478,7 @@ extern "C" fp4q_status_t fp4q_lora_add(const void *y, fp4q_dtype_t dtype, int64_
   auto shrink = [&](auto rt) {
     constexpr int RT = decltype(rt)::value, MR = RT <= 4 ? 2 : 1;
     constexpr int W = 4, NS = RT <= 2 ? 4 : (RT == 4 ? 3 : (RT == 8 ? 2 : 1)), SPLIT_NS = RT <= 4 ? 2 : 1;
-    auto kernel = p.splits > 1 ? shrink_kernel<RT, 1, W, SPLIT_NS, 0>
-                 : dtype == FP4Q_F32 ? shrink_kernel<RT, MR, W, NS, 3>
-                                     : shrink_kernel<RT, MR, W, NS, 2>;
+    auto kernel = p.splits > 1 ? shrink_kernel<RT, 1, W, SPLIT_NS, true> : shrink_kernel<RT, MR, W, NS, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)shrink_tiles, (unsigned)p.splits), dim3(64 * W), 0, s, l);
   };
   if (rank <= 16) shrink(std::integral_constant<int, 1>{});

@@ -159,8 +159,7 @@ fp4q_status_t fp4q_combine_experts(const void *y, fp4q_dtype_t dtype, int64_t to
  *
  * Arithmetic: products are exact; x A^T is summed in float32, multiplied by
  * the scale, and enters the second product as three bfloat16 parts that hold
- * its 24 bits, for a bfloat16 result as two that are off by 2^-17 of it; one
- * rounding at the end.  Elements of b that are not finite
+ * its 24 bits; one rounding at the end.  Elements of b that are not finite
  * give infinities or NaN in their column.  The order of a sum depends on the
  * sizes alone.  A call of more than 2^22 tiles (of 16 rows or more and 256
  * columns) is refused with FP4Q_ERR_SHAPE. */

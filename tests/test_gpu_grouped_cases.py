@@ -1,0 +1,68 @@
+"""Cases of the grouped calls where a result depends on the last bits, on rows
+of no group, or on a group far down the list, against the CPU oracle
+(oracle/grouped.py).  u = 2^-24 is float32's half step, h a half step of the
+result's type.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import gemm as GM
+from oracle import grouped as GR
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+def _fq():
+    import fp4_post_quantization_amd as fq
+    return fq
+
+
+def _np(t):
+    return t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def _within(got, ref, tol, dtype=torch.float32):
+    # half a step of the result: relative, and below the normal range absolute
+    tol = tol + HALF[dtype] * np.abs(ref) + (2.0 ** -150 if dtype == torch.float32 else 2.0 ** -134)
+    err = np.abs(_np(got) - ref)
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.size, float(np.nanmax(err / np.maximum(tol, 1e-300))))
+
+
+def _dev(*ts):
+    return tuple(torch.from_numpy(np.ascontiguousarray(t)).to(DEV) for t in ts)
+
+
+# -------------------------------------------------------------- adapters ----
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,adapters,rank,k,n", [
+    (20, 3, 8, 40, 36), (20, 2, 64, 4096, 36), (700, 2, 64, 40, 300), (700, 1, 128, 40, 72), (600, 2, 200, 40, 68),
+    (300, 1, 128, 2048, 40), (9000, 2, 16, 40, 36),
+])
+def test_adapters_that_cancel_the_projection(rows, adapters, rank, k, n, dtype):
+    """y is close to -s (x A^T) B^T, so that what is left shows every bit of x A^T: its sum in float32, the scale, then
+    products of its 24 bits.  One rank carries all of it, x and A are positive: the steps' bound is
+    (k / 32 + 35 + 3 rank / 32) u of s (x A^T) |B|^T."""
+    fq = _fq()
+    g = torch.Generator().manual_seed(rows + rank)
+    ids = torch.randint(0, adapters, (rows,), generator=g, dtype=torch.int32)
+    x = (0.1 + torch.rand(rows, k, generator=g)).bfloat16()
+    a = (0.1 + torch.rand(adapters, rank, k, generator=g)).bfloat16()
+    b = torch.zeros(adapters, n, rank)
+    b[:, :, rank - 3] = torch.randn(adapters, n, generator=g)
+    b = b.bfloat16()
+    sc = torch.rand(adapters, generator=g) + 0.5
+    off, order = GR.group_rows(ids.numpy(), adapters)
+    away, _ = GR.lora(np.zeros((rows, n)), _np(x), _np(a), _np(b), off, order, _np(sc))
+    y = torch.from_numpy(-away).to(dtype)
+    ref, mag = GR.lora(_np(y), _np(x), _np(a), _np(b), off, order, _np(sc))
+    yd, xd, ad, bd, sd = (t.to(DEV) for t in (y, x, a, b, sc))
+    got = fq.lora_add(yd, xd, ad, bd, fq.group_rows(ids.to(DEV), adapters), scales=sd, check=True)
+    _within(got, ref, (k / 32 + 35 + 3 * rank / 32) * U * mag + U * np.abs(_np(y)), dtype)

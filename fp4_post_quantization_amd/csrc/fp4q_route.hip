@@ -306,11 +306,9 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, const
 #pragma unroll
     for (int j = 0; j < J; ++j) pick[j] = x[j];
     if (a.score == FP4Q_SOFTMAX && !a.renormalize) {
-      // float32 exponentials: each is off by a few 2^-24 of itself, and by 2^-24 of its distance from the largest
-      float part = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) part += key[j] ? __expf(x[j] - most) : 0.0f;
-      total = wave_sum((double)part);
+      for (int j = 0; j < J; ++j) total += exp(key[j] ? (double)x[j] - (double)most : (double)minus_inf);
+      total = wave_sum(total);
     }
   } else {
     if (a.score == FP4Q_SOFTMAX) {

@@ -66,3 +66,26 @@ def test_adapters_that_cancel_the_projection(rows, adapters, rank, k, n, dtype):
     yd, xd, ad, bd, sd = (t.to(DEV) for t in (y, x, a, b, sc))
     got = fq.lora_add(yd, xd, ad, bd, fq.group_rows(ids.to(DEV), adapters), scales=sd, check=True)
     _within(got, ref, (k / 32 + 35 + 3 * rank / 32) * U * mag + U * np.abs(_np(y)), dtype)
+
+
+# --------------------------------------------------------------- routing ----
+@pytest.mark.parametrize("experts,k", [(60, 4), (128, 8), (256, 8), (500, 6), (1024, 16)])
+@pytest.mark.parametrize("tokens", [1, 20, 301])
+def test_softmax_weights_are_rounded_once(experts, k, tokens):
+    """A softmax that is not renormalised: float64 (its own steps below one u), rounded once; and the same bits with a
+    bias of zeros, which changes no choice."""
+    fq = _fq()
+    g = torch.Generator().manual_seed(experts + tokens)
+    for spread in (0.02, 1.5, 6.0):
+        x = spread * torch.randn(tokens, experts, generator=g)
+        x[torch.rand(x.shape, generator=g) < 0.1] = -math.inf
+        for t in (x, x.bfloat16()):
+            d = t.to(DEV)
+            r = fq.route_experts(d, k, renormalize=False, scale=2.5, check=True)
+            w, ids, _ = GR.route(_np(t), k, renormalize=False, scale=2.5)
+            np.testing.assert_array_equal(_np(r.experts), ids)
+            _within(r.weights, w, U * np.abs(w))
+            if t.dtype == torch.float32:  # without equal logits, whose order a bias leaves to float64 scores
+                z = fq.route_experts(d, k, renormalize=False, scale=2.5, bias=torch.zeros(experts, device=DEV))
+                same = (z.experts == r.experts).all(1)
+                assert same.float().mean() > 0.9 and torch.equal(z.weights[same], r.weights[same])

@@ -46,8 +46,22 @@ __device__ __forceinline__ int a_row(const GroupedArgs &a, int p, int e) {
   return a.gather ? (e < 0 ? 0 : e / a.gather) : p;
 }
 
-// z / (1 + exp(-z)), the reciprocal by the hardware's (off by one unit at most)
-__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// z / (1 + exp(-z)) to 7 units of 2^-24, for z < 0 as z exp(z) / (1 + exp(z)), so that nothing leaves float32's range
+// before the result does.  exp(-|z|) is 2^(i + f) with i = round(-|z| log2 e) and f from two parts of log2 e, so that
+// the error of the product does not grow with |z| (from 200 on it is 0 all the same); 1 / (1 + exp(-|z|)) is the
+// hardware's, off by one unit, after one Newton step.  -inf gives NaN, as the quotient does.  (The hardware's exponential
+// and reciprocal of 1 + exp(-z) alone: off by |z| units, and 0 from z = -87 on where float32 reaches to -92; 4096 tokens of
+// 128 experts, gates and ups of 4096 x 1536, 212 us instead of 221.)
+__device__ __forceinline__ float silu(float z) {
+  constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;
+  const float a = __builtin_fminf(__builtin_fabsf(z), 200.0f);
+  const float i = __builtin_rintf(-a * kLog2e);
+  const float f = __builtin_fmaf(-a, kLog2eRest, __builtin_fmaf(-a, kLog2e, -i));
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)i), d = 1.0f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  return (z < 0.0f ? z * e : z) * r;
+}
 
 // Any k that is a multiple of 32: 64 rows times 128 rows of B (gated: 64 gates and their 64 ups), registers to a
 // padded LDS double buffer, 128 elements of K a stage, the tail filled with zeros.  For K below 256, which the ring's

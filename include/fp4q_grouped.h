@@ -110,7 +110,7 @@ size_t fp4q_route_experts_workspace_bytes(int64_t tokens, int64_t experts, int64
  *            entry e's.
  *   gated    1: n is even, and of the n products the first half are gates:
  *            C has n / 2 columns, silu(gate) * up, with silu(z) =
- *            z / (1 + exp(-z)) in float32.
+ *            z / (1 + exp(-z)) in float32, off by at most 7 * 2^-24 of it.
  *   c, ldc, out_dtype  [groups->entries] rows of n (n / 2) columns,
  *            FP4Q_F32 or FP4Q_BF16; it must not overlap the inputs.
  *   workspace  fp4q_workspace_bytes() bytes (status word).

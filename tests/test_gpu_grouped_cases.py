@@ -89,3 +89,41 @@ def test_softmax_weights_are_rounded_once(experts, k, tokens):
                 z = fq.route_experts(d, k, renormalize=False, scale=2.5, bias=torch.zeros(experts, device=DEV))
                 same = (z.experts == r.experts).all(1)
                 assert same.float().mean() > 0.9 and torch.equal(z.weights[same], r.weights[same])
+
+
+# ------------------------------------------------------ grouped products ----
+_E2M1 = [0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def _single(values, k):
+    """MXFP4 rows of k whose first element is the value (an E2M1 number times a power of two), the rest zero."""
+    codes, scales = np.zeros((len(values), k // 2), np.uint8), np.full((len(values), k // 32), 127, np.uint8)
+    for i, v in enumerate(values):
+        e = next(e for e in range(-8, 12) if abs(v) / 2.0 ** e in _E2M1)
+        codes[i, 0] = _E2M1.index(abs(v) / 2.0 ** e) + 1 | (8 if v < 0 else 0)
+        scales[i, 0] = 127 + e
+    return codes, scales
+
+
+@pytest.mark.parametrize("rows,k", [(7, 32), (7, 512), (700, 320), (700, 512)])
+@pytest.mark.parametrize("alpha", [1.0, 0.9371, 0.0371, -1.3])
+def test_gates_to_float32(rows, k, alpha):
+    """silu(z) * up for z = alpha a b exactly known: z spans -125 .. 125, where exp(-z) leaves float32's range and
+    silu(z), down to -92, does not.  silu: exp(-|z|) off by 2.4 u (its instruction by one unit), which z < 0 takes in
+    full, then a product, a sum, a reciprocal and a product, one u each: 6.4 u; the product with up is the result's
+    half step.  Below float32's normal range its steps count."""
+    fq = _fq()
+    gates = [s * v * 2.0 ** e for e in range(-5, 5) for v in _E2M1 for s in (1, -1)]
+    n = len(gates)
+    bc, bs = _single(gates + [1.0] * n, k)
+    av = [(1.0, 1.5, 0.5, 1.0)[i % 4] for i in range(rows)]
+    ac, as_ = _single(av, k)
+    off, order = _dev(np.array([0, rows], np.int32), np.arange(rows, dtype=np.int32))
+    got = fq.gemm_mxfp4_grouped(_dev(ac, as_), _dev(bc[None], bs[None]), fq.RowGroups(off, order), gated=True, alpha=alpha,
+                                check=True)
+    al = np.float32(alpha)
+    z = (al * np.outer(av, gates).astype(np.float32)).astype(np.float64)
+    up = (al * np.array(av, np.float32)[:, None]).astype(np.float64)
+    e = np.exp(-np.abs(z))
+    ref = np.where(z < 0, z * e, z) / (1.0 + e) * up
+    _within(got, ref, 6.4 * U * np.abs(ref) + 2.0 ** -140)

@@ -1133,8 +1133,8 @@ def gemm_mxfp4_grouped(a, b, groups, *, gather=0, scatter=False, gated=False, al
     gates, the result [entries, N/2] is silu(gate) * up.
 
     Returns [entries, N] (gated: N/2) in float32 or bfloat16; rows of entries
-    of no group are left as they are in a given out (unspecified in a fresh
-    one).  check: synchronize and raise on data errors."""
+    of no group are left as they are in a given out, and zeros in a fresh one.
+    check: synchronize and raise on data errors."""
     lib = L.load()
     ac, as_ = (a.codes, a.scales) if isinstance(a, MXFP4Result) else a
     bc, bs = (b.codes, b.scales) if isinstance(b, MXFP4Result) else b
@@ -1160,13 +1160,13 @@ def gemm_mxfp4_grouped(a, b, groups, *, gather=0, scatter=False, gated=False, al
     cols = n // 2 if gated else n
     if out is None:
         out, ldc = torch.empty(entries, cols, dtype=out_dtype, device=dev), cols
-        code = _dtype_code(out)
+        code, call = _dtype_code(out), lib.fp4q_gemm_mxfp4_grouped_zeroed
     else:
-        ldc, code = _result(out, entries, cols, dev), _FLOATS[out.dtype]
+        ldc, code, call = _result(out, entries, cols, dev), _FLOATS[out.dtype], lib.fp4q_gemm_mxfp4_grouped
     index, stream = _index_of(dev)
     at, size, ws = _room(ws, dev, index, stream, 0)
-    _call(index, lib.fp4q_gemm_mxfp4_grouped, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(), bs.data_ptr(), packed, n,
-          2 * kh, gather, bool(scatter), bool(gated), alpha, code, out.data_ptr(), ldc, at, size, stream)
+    _call(index, call, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(), bs.data_ptr(), packed, n, 2 * kh, gather,
+          bool(scatter), bool(gated), alpha, code, out.data_ptr(), ldc, at, size, stream)
     if check:
         _check_data(ws)
     return out

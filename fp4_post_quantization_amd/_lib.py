@@ -68,6 +68,7 @@ GROUPED_EXPORTS = (
     "fp4q_route_experts",
     "fp4q_route_experts_workspace_bytes",
     "fp4q_gemm_mxfp4_grouped",
+    "fp4q_gemm_mxfp4_grouped_zeroed",
     "fp4q_combine_experts",
     "fp4q_lora_add",
     "fp4q_lora_add_workspace_bytes",
@@ -153,6 +154,8 @@ _SIGNATURES = {
     "fp4q_route_experts_workspace_bytes": (_SZ, [_I64] * 3),
     "fp4q_gemm_mxfp4_grouped": (_I, [_P, _P, _I64, _P, _P, _GROUPS, _I64, _I64, _I64, _I, _I, ctypes.c_float, _I, _P,
                                      _I64, _P, _SZ, _P]),
+    "fp4q_gemm_mxfp4_grouped_zeroed": (_I, [_P, _P, _I64, _P, _P, _GROUPS, _I64, _I64, _I64, _I, _I, ctypes.c_float, _I,
+                                            _P, _I64, _P, _SZ, _P]),
     "fp4q_combine_experts": (_I, [_P, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I, _P, _I64, _P]),
     "fp4q_lora_add": (_I, [_P, _I, _I64, _P, _I64, _P, _P, _P, _GROUPS, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]),
     "fp4q_lora_add_workspace_bytes": (_SZ, [_I64] * 5),

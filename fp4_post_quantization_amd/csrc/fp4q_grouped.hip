@@ -39,11 +39,31 @@ struct GroupedArgs {
   void *c;
   int64_t ldc;
   uint32_t *status;
+  bool zeroed;  // rows of C of entries of no group become zeros
 };
 
 // The row of A of position p, whose entry is e.
 __device__ __forceinline__ int a_row(const GroupedArgs &a, int p, int e) {
   return a.gather ? (e < 0 ? 0 : e / a.gather) : p;
+}
+
+// Zeros in the rows of C of entries of no group, a row a workgroup of whatever kernel at a time: they are read like any
+// other by what quantizes or sums C next.  (A call with none of them: one load a workgroup, 12.3 us instead of 12.0 for
+// one token of 8 experts; 333 tokens of which every seventh is padding 18.5 instead of 17.9.)
+template <typename OutT>
+__device__ __forceinline__ void zero_rest(const GroupedArgs &a) {
+  constexpr int VEC = 16 / (int)sizeof(OutT);
+  const int last = a.groups.offsets[a.groups.groups], from = last < 0 ? 0 : last;
+  const bool wide = ((uintptr_t)a.c % 16 == 0) && ((a.ldc * (int64_t)sizeof(OutT)) % 16 == 0);
+  const int whole = wide ? a.n_out / VEC * VEC : 0;
+  for (int64_t p = (int64_t)from + blockIdx.x; p < a.groups.entries; p += gridDim.x) {
+    const int row = a.scatter ? entry_at(a.groups, (int)p) : (int)p;
+    if (row < 0) continue;
+    OutT *c = (OutT *)a.c + (int64_t)row * a.ldc;
+    for (int i = threadIdx.x * VEC; i < whole; i += blockDim.x * VEC)
+      *reinterpret_cast<u32x4 *>(c + i) = u32x4{0, 0, 0, 0};
+    for (int i = whole + threadIdx.x; i < a.n_out; i += blockDim.x) c[i] = OutT(0);
+  }
 }
 
 // z / (1 + exp(-z)) to 7 units of 2^-24, for z < 0 as z exp(z) / (1 + exp(z)), so that nothing leaves float32's range
@@ -76,6 +96,7 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
   __shared__ int row_of[kAnyRows];  // row of C, -1: not stored
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int wm = wave & 1, wn = wave >> 1, l32 = lane & 31, h = lane >> 5;
+  if (a.zeroed) zero_rest<OutT>(a);
   uint32_t err = 0;
   if (blockIdx.x == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
   const RowTile t = find_tile(a.groups, kAnyRows, (int)(blockIdx.x / a.tiles_n));
@@ -275,6 +296,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int wm = wave / WGN, wn = wave % WGN, l32 = lane & 31, h = lane >> 5;
+  if (a.zeroed) zero_rest<OutT>(a);
   uint32_t err = 0;
   if (blockIdx.x == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
   const int lin = tile_number(a);
@@ -520,6 +542,7 @@ template <typename OutT, bool GATED>
 __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs a) {
   __shared__ f32x4v part[kFewWaves][2][64];
   const int lane = threadIdx.x & 63, wave = wave_index(), r16 = lane & 15, h = lane >> 4;
+  if (a.zeroed) zero_rest<OutT>(a);
   uint32_t err = 0;
   if (blockIdx.x == 0 && wave == 0 && offsets_bad(a.groups)) err = FP4Q_DATA_BAD_GROUP;
   const int lin = tile_number(a);
@@ -624,6 +647,7 @@ __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_index();
   const int wm = wave / WGN, wn = wave % WGN, l32 = lane & 31, h = lane >> 5;
+  if (a.zeroed) zero_rest<OutT>(a);
   uint32_t err = 0;
   if (wave == 0) {
     int run = 0;
@@ -952,17 +976,11 @@ bool launch(GroupedArgs &a, hipStream_t s) {
 
 fp4q_status_t hip_status() { return hipGetLastError() == hipSuccess ? FP4Q_OK : FP4Q_ERR_HIP; }
 
-}  // namespace
-}  // namespace fp4q
-
-using namespace fp4q;
-
-extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows,
-                                                 const uint8_t *b_codes, const uint8_t *b_scales,
-                                                 const fp4q_row_groups_t *groups, int64_t n, int64_t k,
-                                                 int64_t gather, int scatter, int gated, float alpha,
-                                                 fp4q_dtype_t out_dtype, void *c, int64_t ldc, void *workspace,
-                                                 size_t workspace_bytes, void *stream) {
+// The calls of the header; zeroed: rows of C of entries of no group become zeros.
+fp4q_status_t grouped_call(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows, const uint8_t *b_codes,
+                           const uint8_t *b_scales, const fp4q_row_groups_t *groups, int64_t n, int64_t k,
+                           int64_t gather, int scatter, int gated, float alpha, fp4q_dtype_t out_dtype, void *c,
+                           int64_t ldc, void *workspace, size_t workspace_bytes, void *stream, bool zeroed) {
   if (!groups) return FP4Q_ERR_NULL;
   if ((out_dtype != FP4Q_F32 && out_dtype != FP4Q_BF16) || (scatter != 0 && scatter != 1) || (gated != 0 && gated != 1))
     return FP4Q_ERR_ARG;
@@ -982,7 +1000,7 @@ extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const u
     return FP4Q_ERR_ALIGN;
   if (k % 128 == 0 && (!kv_aligned(a_scales, 4) || !kv_aligned(b_scales, 4))) return FP4Q_ERR_ALIGN;
   GroupedArgs a{a_codes, a_scales, b_codes, b_scales, groups_of(*groups), (int)a_rows, (int)gather, scatter, (int)n,
-                (int)k, (int)(gated ? n / 2 : n), 0, 1, alpha, c, ldc, status};
+                (int)k, (int)(gated ? n / 2 : n), 0, 1, alpha, c, ldc, status, zeroed};
   bool fits = true;
   with_type(out_dtype, [&](auto op) {
     using O = std::remove_pointer_t<decltype(op)>;
@@ -991,4 +1009,29 @@ extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const u
   });
   if (!fits) return FP4Q_ERR_SHAPE;
   return hip_status();
+}
+
+}  // namespace
+}  // namespace fp4q
+
+using namespace fp4q;
+
+extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows,
+                                                 const uint8_t *b_codes, const uint8_t *b_scales,
+                                                 const fp4q_row_groups_t *groups, int64_t n, int64_t k,
+                                                 int64_t gather, int scatter, int gated, float alpha,
+                                                 fp4q_dtype_t out_dtype, void *c, int64_t ldc, void *workspace,
+                                                 size_t workspace_bytes, void *stream) {
+  return grouped_call(a_codes, a_scales, a_rows, b_codes, b_scales, groups, n, k, gather, scatter, gated, alpha, out_dtype,
+                      c, ldc, workspace, workspace_bytes, stream, false);
+}
+
+extern "C" fp4q_status_t fp4q_gemm_mxfp4_grouped_zeroed(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows,
+                                                        const uint8_t *b_codes, const uint8_t *b_scales,
+                                                        const fp4q_row_groups_t *groups, int64_t n, int64_t k,
+                                                        int64_t gather, int scatter, int gated, float alpha,
+                                                        fp4q_dtype_t out_dtype, void *c, int64_t ldc,
+                                                        void *workspace, size_t workspace_bytes, void *stream) {
+  return grouped_call(a_codes, a_scales, a_rows, b_codes, b_scales, groups, n, k, gather, scatter, gated, alpha, out_dtype,
+                      c, ldc, workspace, workspace_bytes, stream, true);
 }

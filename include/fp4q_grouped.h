@@ -130,6 +130,14 @@ fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const uint8_t *a_s
                                       int scatter, int gated, float alpha, fp4q_dtype_t out_dtype, void *c,
                                       int64_t ldc, void *workspace, size_t workspace_bytes, void *stream);
 
+/* The same, and rows of C that belong to entries of no group become zeros:
+ * for a fresh C that is read as a whole, as fp4q_quantize_mxfp4 does. */
+fp4q_status_t fp4q_gemm_mxfp4_grouped_zeroed(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows,
+                                             const uint8_t *b_codes, const uint8_t *b_scales,
+                                             const fp4q_row_groups_t *groups, int64_t n, int64_t k, int64_t gather,
+                                             int scatter, int gated, float alpha, fp4q_dtype_t out_dtype, void *c,
+                                             int64_t ldc, void *workspace, size_t workspace_bytes, void *stream);
+
 /* out[t] = sum over j of weights[t][j] * y[t * top_k + j], plus add[t].
  *   y, dtype  [tokens * top_k] rows of n, ld_y elements apart.
  *   weights  [tokens][top_k] float32; chosen [tokens][top_k] int32 or NULL:

@@ -127,3 +127,92 @@ def test_gates_to_float32(rows, k, alpha):
     e = np.exp(-np.abs(z))
     ref = np.where(z < 0, z * e, z) / (1.0 + e) * up
     _within(got, ref, 6.4 * U * np.abs(ref) + 2.0 ** -140)
+
+
+def _poisoned(monkeypatch):
+    """Fresh floating tensors hold NaN."""
+    empty = torch.empty
+
+    def fresh(*a, **kw):
+        t = empty(*a, **kw)
+        return t.fill_(math.nan) if t.is_floating_point() else t
+
+    monkeypatch.setattr(torch, "empty", fresh)
+
+
+SHAPES = [  # tokens, groups, top_k, k, n
+    (9, 3, 2, 64, 40), (9, 3, 2, 512, 66), (100, 16, 4, 704, 130), (100, 16, 4, 1024, 520), (90, 40, 6, 4608, 258),
+    (1500, 6, 2, 640, 256), (700, 2, 2, 768, 320), (4096, 6, 2, 512, 4000),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,groups,top_k,k,n", SHAPES)
+def test_fresh_rows_of_no_group_are_zeros(tokens, groups, top_k, k, n, dtype, monkeypatch):
+    """Half of the entries, and all of them, of no group: their rows of a result that the call makes are zeros, in the
+    groups' order and scattered; the others are what a given result gets."""
+    fq = _fq()
+    rng = np.random.default_rng(k)
+    ids = np.stack([rng.permutation(groups)[:top_k] for _ in range(tokens)]).astype(np.int32)
+    ids[rng.random(ids.shape) < 0.5] = -1
+    a = (rng.integers(0, 256, (tokens, k // 2)).astype(np.uint8), rng.integers(122, 129, (tokens, k // 32)).astype(np.uint8))
+    b = (rng.integers(0, 256, (groups, n, k // 2)).astype(np.uint8),
+         rng.integers(122, 129, (groups, n, k // 32)).astype(np.uint8))
+    a, b = _dev(*a), _dev(*b)
+    for which in (ids, np.full_like(ids, -1)):
+        off, order = GR.group_rows(which, groups)
+        live, gr = int(off[-1]), fq.RowGroups(*_dev(off, order))
+        rows = torch.from_numpy(order).long().to(DEV)
+        for gated in (False, True):
+            for scatter in (False, True):
+                given = torch.full((tokens * top_k, n // 2 if gated else n), 7.0, dtype=dtype, device=DEV)
+                kw = dict(gather=top_k, gated=gated, scatter=scatter, alpha=0.0625, check=True)
+                fq.gemm_mxfp4_grouped(a, b, gr, out=given, **kw)
+                with monkeypatch.context() as m:
+                    _poisoned(m)
+                    got = fq.gemm_mxfp4_grouped(a, b, gr, out_dtype=dtype, **kw)
+                if scatter:
+                    got, given = got[rows], given[rows]
+                assert (given[live:] == 7.0).all()
+                assert (got[live:] == 0.0).all() and torch.equal(got[:live], given[:live])
+
+
+@pytest.mark.parametrize("tokens", [5, 40, 200])
+def test_layer_of_experts_with_padding(tokens, monkeypatch):
+    """Tokens that are padding (every expert off), tokens with fewer experts than choices, and an expert that nobody may
+    use, through every step of a layer, whose data errors are all looked at."""
+    fq = _fq()
+    experts, k, hidden, inner = 12, 3, 256, 192
+    g = torch.Generator().manual_seed(tokens)
+    x = torch.randn(tokens, hidden, generator=g).bfloat16().to(DEV)
+    logits = torch.randn(tokens, experts, generator=g)
+    logits[torch.rand(tokens, generator=g) < 0.3] = -math.inf
+    logits[0], logits[1, 2:], logits[:, 7] = -math.inf, -math.inf, -math.inf
+    logits = logits.to(DEV)
+    up = fq.quantize_mxfp4((torch.randn(experts * 2 * inner, hidden, generator=g) * hidden ** -0.5).to(DEV))
+    down = fq.quantize_mxfp4((torch.randn(experts * hidden, inner, generator=g) * inner ** -0.5).to(DEV))
+    up = (up.codes.view(experts, 2 * inner, -1), up.scales.view(experts, 2 * inner, -1))
+    down = (down.codes.view(experts, hidden, -1), down.scales.view(experts, hidden, -1))
+    with monkeypatch.context() as m:
+        _poisoned(m)
+        r = fq.route_experts(logits, k, score="sigmoid", check=True)
+        xq = fq.quantize_mxfp4(x, check=True)
+        z = fq.gemm_mxfp4_grouped(xq, up, r.groups, gather=k, gated=True, out_dtype=torch.bfloat16, check=True)
+        zq = fq.quantize_mxfp4(z, check=True)
+        y = fq.gemm_mxfp4_grouped(zq, down, r.groups, scatter=True, out_dtype=torch.bfloat16, check=True)
+        out = fq.combine_experts(y.view(tokens, k, hidden), r.weights, r.experts, add=x)
+        bare = fq.combine_experts(y.view(tokens, k, hidden), r.weights, add=x)
+    w, ids, _ = GR.route(_np(logits), k, score="sigmoid")
+    np.testing.assert_array_equal(_np(r.experts), ids)
+    assert (ids == -1).any() and torch.equal(out, bare)
+    off, rows = GR.group_rows(ids, experts)
+    live = int(off[-1])
+    hat = lambda c, s: GM.decode_mxfp4_64(_np(c), _np(s))
+    dec = lambda p: np.stack([hat(c, s) for c, s in zip(*p)])
+    ref, mag = GR.products(hat(zq.codes, zq.scales), dec(down), off, rows)
+    want, size = np.zeros((tokens * k, hidden)), np.zeros((tokens * k, hidden))
+    want[rows[:live]], size[rows[:live]] = ref[:live], mag[:live]
+    _within(y, want, (2 * math.ceil(inner / 64) + 2) * U * size, torch.bfloat16)
+    ref, mag = GR.combine(_np(y).reshape(tokens, k, hidden), _np(r.weights), ids, _np(x))
+    _within(out, ref, (k + 1) * U * mag, torch.bfloat16)
+    assert torch.equal(out[0], x[0])

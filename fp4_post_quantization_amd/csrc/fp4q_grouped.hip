@@ -234,7 +234,7 @@ __device__ __forceinline__ GroupTile group_tile(const GroupedArgs &a, const Tile
 
 constexpr int kRowBytes = 128;  // code bytes of a row and stage: 256 elements of K
 
-template <typename OutT, bool GATED, int WGM, int WGN, int TM, int TN>
+template <bool GATED, int WGM, int WGN, int TM, int TN>
 struct RingShape {
   static constexpr int ROWB = kRowBytes;
   static constexpr int WAVES = WGM * WGN, THREADS = 64 * WAVES;
@@ -274,7 +274,7 @@ __device__ const u32x4 kZeroCodes = {0, 0, 0, 0};
 
 template <typename OutT, bool GATED, bool TAIL, int NS, int WGM, int WGN, int TM, int TN>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArgs a) {
-  using S = RingShape<OutT, GATED, WGM, WGN, TM, TN>;
+  using S = RingShape<GATED, WGM, WGN, TM, TN>;
   static_assert(!TAIL || NS == 2, "scales that come through registers are a stage ahead");
   constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, BN = S::BN;
   constexpr int CPR = S::CPR, KS = S::KS, SPR = S::SPR, STAGE = S::STAGE;
@@ -409,10 +409,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_ring_kernel(GroupedArg
     i32x8 a[TM], b[TN];
     int sa[TM], sb[TN];
   };
-  auto scale_word = [&](const uint8_t *p) {
-    if constexpr (SPR == 8) return (int)*reinterpret_cast<const uint32_t *>(p + 4 * h);
-    else return (int)*reinterpret_cast<const uint16_t *>(p + 2 * h);
-  };
+  auto scale_word = [&](const uint8_t *p) { return (int)*reinterpret_cast<const uint32_t *>(p + 4 * h); };
   const int lane_sw = fp4q_gemm::swz<ROWB>(l32);  // of every row a lane reads: they differ by multiples of 32
   auto read_ops = [&](int slot, auto ks_c, Ops &o, const Ops &prev) {
     constexpr int ks = decltype(ks_c)::value;
@@ -634,7 +631,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs
 template <typename OutT, bool GATED>
 __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
   constexpr int WGN = 4, TM = 4, TN = 2;
-  using S = RingShape<OutT, GATED, 2, WGN, TM, TN>;
+  using S = RingShape<GATED, 2, WGN, TM, TN>;
   constexpr int ROWB = kRowBytes, WAVES = S::WAVES, BM = S::BM, CPR = S::CPR, KS = S::KS, SPR = S::SPR;
   constexpr int STAGE = S::STAGE, RPL = 1024 / ROWB, LOADS = BM / RPL / WAVES;  // 1 KB loads of A, and of B, a wave
   constexpr int RPS = 256 / SPR;  // rows of a scale load: a wave's first is A's, its second B's

@@ -55,9 +55,6 @@ struct LoraArgs {
   uint32_t *status;
 };
 
-__device__ __forceinline__ bf16x8 load_bf16x8(const uint16_t *p) {
-  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4 *>(p));
-}
 __device__ __forceinline__ bf16x8 zero_bf16x8() { return __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0}); }
 
 constexpr int kLoraWaves = 4, kLoraThreads = 64 * kLoraWaves;

@@ -122,8 +122,8 @@ size_t fp4q_route_experts_workspace_bytes(int64_t tokens, int64_t experts, int64
  * output tiles (about 2^36 values of C) is refused with FP4Q_ERR_SHAPE.
  *
  * Arithmetic: as fp4q_gemm_mxfp4's (products of decoded elements are exact,
- * sums are float32); the order of a sum depends on n, k, the number of
- * groups and entries, and not on the other rows. */
+ * sums are float32); the order of a sum depends on n, k and the numbers of
+ * groups, entries and rows of A, and not on what the rows hold. */
 fp4q_status_t fp4q_gemm_mxfp4_grouped(const uint8_t *a_codes, const uint8_t *a_scales, int64_t a_rows,
                                       const uint8_t *b_codes, const uint8_t *b_scales,
                                       const fp4q_row_groups_t *groups, int64_t n, int64_t k, int64_t gather,

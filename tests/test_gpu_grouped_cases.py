@@ -216,3 +216,46 @@ def test_layer_of_experts_with_padding(tokens, monkeypatch):
     ref, mag = GR.combine(_np(y).reshape(tokens, k, hidden), _np(r.weights), ids, _np(x))
     _within(out, ref, (k + 1) * U * mag, torch.bfloat16)
     assert torch.equal(out[0], x[0])
+
+
+FAR = [  # groups, rows a group, k, n: more groups than one step of the search takes
+    (65, 30, 512, 300), (70, 28, 704, 260), (200, 10, 512, 130), (200, 10, 704, 130), (80, 12, 4096, 300),
+    (70, 80, 768, 64), (70, 80, 640, 64), (65, 200, 512, 498), (130, 200, 512, 758), (512, 200, 512, 256),
+    (513, 200, 512, 256), (2048, 3, 512, 40), (2048, 3, 96, 40),
+]
+
+
+@pytest.mark.parametrize("empty", [False, True])
+@pytest.mark.parametrize("groups,rows,k,n", FAR)
+def test_groups_past_the_first_64(groups, rows, k, n, empty):
+    """Groups of different lengths, and runs of empty ones across every step of 64: around those places, at both ends and
+    at random ones, results against 64 bits; rows past the last group stay."""
+    fq = _fq()
+    rng = np.random.default_rng(groups + k)
+    share = rng.uniform(0.5, 1.5, groups)
+    if empty:
+        for g in range(60, groups, 64):
+            share[g:g + 8] = 0
+        share[0] = share[-1] = 0
+    counts = rng.multinomial(groups * rows - 3, share / share.sum())
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    live = int(off[-1])
+    entries, tokens = live + 3, 64
+    gather = -(-entries // tokens)
+    order = rng.permutation(entries).astype(np.int32)
+    a = (rng.integers(0, 256, (tokens, k // 2)).astype(np.uint8), rng.integers(122, 129, (tokens, k // 32)).astype(np.uint8))
+    b = (rng.integers(0, 256, (groups, n, k // 2)).astype(np.uint8),
+         rng.integers(122, 129, (groups, n, k // 32)).astype(np.uint8))
+    ah = GM.decode_mxfp4_64(*a)
+    out = torch.full((entries, n), math.nan, device=DEV)
+    fq.gemm_mxfp4_grouped(_dev(*a), _dev(*b), fq.RowGroups(*_dev(off, order)), gather=gather, out=out, check=True)
+    assert out[live:].isnan().all() and not out[:live].isnan().any()
+    near = {g + d for g in list(range(0, groups, 64)) + [groups] for d in (-3, -2, -1, 0, 1, 4, 5)}
+    look = sorted({g for g in near if 0 <= g < groups} | set(rng.integers(0, groups, 12).tolist()))
+    got = _np(out)
+    for g in look:
+        p = slice(int(off[g]), int(off[g + 1]))
+        x, w = ah[order[p] // gather], GM.decode_mxfp4_64(b[0][g], b[1][g])
+        ref, mag = x @ w.T, np.abs(x) @ np.abs(w).T
+        err = np.abs(got[p] - ref)
+        assert (err <= (2 * math.ceil(k / 64) + 3) * U * mag).all(), g

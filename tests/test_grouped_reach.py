@@ -10,7 +10,7 @@ import pytest
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 from test_grouped_host import ANY, DEEP, FEW, PERSIST, RING, _lib, _tiles, host  # noqa: E402,F401
-from test_gpu_grouped_cases import SHAPES  # noqa: E402
+from test_gpu_grouped_cases import FAR, SHAPES  # noqa: E402
 
 
 def _reached(t, k):
@@ -23,6 +23,12 @@ EVERY = {(ANY, 64, False), (FEW, 16, False), (RING, 64, False), (RING, 64, True)
 
 def test_cases_with_rows_of_no_group_reach_every_kernel(host):  # noqa: F811
     assert {_reached(_tiles(host, t * top, g, n, k), k) for t, g, top, k, n in SHAPES} >= EVERY
+
+
+def test_cases_past_64_groups_reach_every_kernel(host):  # noqa: F811
+    far = {g: _reached(_tiles(host, g * rows, g, n, k), k) for g, rows, k, n in FAR if rows == 200}
+    assert far[65] == far[130] == far[512] == (PERSIST, 256, False) and far[513] == (RING, 128, False)
+    assert {_reached(_tiles(host, g * rows, g, n, k), k) for g, rows, k, n in FAR} >= EVERY - {(FEW, 16, False)}
 
 
 @pytest.mark.parametrize("at,value,want", [

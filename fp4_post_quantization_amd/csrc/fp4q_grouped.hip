@@ -207,7 +207,8 @@ __global__ __launch_bounds__(kAnyThreads) void grouped_any_kernel(GroupedArgs a)
 // so that a lane's scale bytes of a stage are one word, of which the instruction selects byte ks.  What differs is
 // where rows come from: a lane loads the entry numbers of the rows that it stages once, before the loop.
 // TAIL, where K is no multiple of 256: chunks past a row's end are loaded from zeros, and scales, whose rows need not
-// be aligned, come through registers.
+// be aligned, come through registers, where they are put in place as they arrive: the next stage's products begin only
+// when the loads of the one after it, just issued, have landed, so that every stage shows a trip to memory.
 //
 // Gated: block column j of a wave is gates for even j and the ups of the same columns for odd j, so that both meet in
 // a lane's registers.
@@ -626,8 +627,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void grouped_few_kernel(GroupedArgs
 // The ring in tiles of 256 x 256 for many of them (K a multiple of 256, from 512 on; up to kPersistGroups groups): one
 // workgroup a CU walks tiles gridDim apart, and loads the next tile's first stages while it finishes the one before.
 // Started anew, a tile costs 8 us beside its stages (2.4 us for 256 elements of K): the search for its
-// group, its rows' numbers, the first loads, the stores.  Here the groups' tiles are summed once into LDS, the next
-// tile's rows are asked for when a tile begins, and its loads follow the last ones of the tile without a gap.
+// group, its rows' numbers, the first loads, the stores.  Here the groups' tiles are summed once into LDS, and the next
+// tile's loads follow the last ones of the tile without a gap.  Its rows are looked up when a tile begins; where they are
+// gathered, that is up to six trips to memory one after the other, each number being checked before the next is asked for.
 template <typename OutT, bool GATED>
 __global__ __launch_bounds__(512) void grouped_persist_kernel(GroupedArgs a) {
   constexpr int WGN = 4, TM = 4, TN = 2;

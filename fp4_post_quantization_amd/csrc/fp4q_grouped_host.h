@@ -97,15 +97,16 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
   }
   const int64_t rows = entries / (groups < entries ? groups : (entries ? entries : 1));  // of a group, on average
   // Measured, us, gate and up products of 4096 x 1536 unless said:
-  // few rows (16 x 32) where all of a call's tiles run at once, two a CU: one token of 8 experts 12.0, in tiles of 64 x
-  // 128 14.5; 16 tokens (3600 tiles) 71 and 53.
-  if (k % 128 == 0 && tiles(kFewRows16, kFewCols) <= 512) {
+  // few rows (16 x 32) where a call has at most one tile a CU: 2 rows on 4096 x 4096 7.2, in tiles of 64 x 128 10.0; on
+  // 14336 x 4096 19.6 and 25.6; 4 rows on 1408 x 2048 5.1 and 7.3.  With more the tiles of 64 rows are faster: 8 rows of 8
+  // experts (384 tiles) 11.6 and 11.3, on 2048 x 2048 (512) 11.8 and 7.6, of 16 tokens (3600) 70 and 43.
+  if (k % 128 == 0 && tiles(kFewRows16, kFewCols) <= kCus) {
     t = ProductTiles{kFewTiles, kFewRows16, kFewCols, 4, 0};
   } else if (rows <= 64) {
-    // 64 rows up to 64 a group: 16 tokens of 128 experts 51, with 128 52; 64 tokens 91 and 100; 512 (32 rows) 115 and
-    // 117; 1000 (62 rows) 130 and 130; 1500 (94 rows) 155 and 142.  Two stages more in flight where K has many, at two
-    // workgroups a CU instead of three: 46, 91, 110 and 129; 64 tokens of 8 experts on 14336 x 4096 46 and 41; 1000
-    // tokens on 768 x 4096 73 and 84.
+    // 64 rows up to 64 a group: 16 tokens of 128 experts 47, with 128 50; 64 tokens 92 and 100; 512 (32 rows) 115 and
+    // 116; 1000 (62 rows) 130 and 130; 1500 (94 rows) 157 and 145.  A third stage in flight where K has many, at two
+    // workgroups a CU instead of three: 43, 89, 105 and 126; 64 tokens of 8 experts on 14336 x 4096 44 and 40; 1000
+    // tokens on 768 x 4096 74 and 85.
     t = ProductTiles{k % 256 == 0 && k >= 4096 ? kDeepTiles : kRingTiles, 64, 128, run(64), 0};
   } else {
     const int64_t live = groups < entries ? groups : entries;
@@ -113,8 +114,10 @@ inline ProductTiles product_tiles(int64_t entries, int64_t groups, int64_t n, in
       return ceil_div((entries / r + live / 2) * ceil_div(n, c), at_once);
     };
     // 256 x 256, one a CU, where it takes fewer rounds of 1.55 times the length than 128 x 128, two a CU: 2500 tokens
-    // of 128 experts (156 rows) 165 and 183; 4096 tokens (256) 212 and 262; 768 x 4096 154 and 196; 2048 rows on 4096 x
-    // 4096 200 and 243; 512 rows on 4096 x 4096 (two rounds, the second a quarter full) 75 and 68; 94 rows 157 and 142.
+    // of 128 experts (156 rows) 173 and 187; 4096 tokens (256) 215 and 253; 768 x 4096 151 and 192; 2048 rows on 4096 x
+    // 4096 192 and 244; 512 rows on 4096 x 4096 (two rounds, the second a quarter full) 74 and 68; 94 rows 149 and 145.
+    // All of it goes by the average, entries of no group included: the offsets are on the device.  2048 tokens of 128
+    // experts, 8 each, take 167; with nine of ten on the same 8 experts 198.
     if (k % 256 == 0 && k >= 512 && groups <= kPersistGroups &&
         155 * rounds(256, 256, 256) <= 100 * rounds(128, 128, 512))
       t = ProductTiles{kPersistTiles, 256, 256, 16, 0};
@@ -183,8 +186,9 @@ inline fp4q_status_t lora_check_sizes(int64_t entries, int64_t groups, int64_t n
   return FP4Q_OK;
 }
 
-// few: B meets 16 rows at a time, else 64 (8191 rows, rank 64, N 14336: 119 us, with 32 134), but 32 in float32 and for
-// ranks beyond 64, which take twice the registers and LDS (4000 rows, rank 128, N 4096: 39 us, with 64 41).
+// few: B meets 16 rows at a time, else 64 (8191 rows, rank 64, N 14336: 131 us, with 32 145), but 32 in float32 and for
+// ranks beyond 64, which take twice the registers and LDS (4000 rows, rank 128, N 4096: 42 us, with 64 the same; rank 256
+// does not fit a CU's LDS twice).
 // splits: of K, over workgroups.
 struct LoraPlan {
   bool few;

@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kSortThreads) void place_kernel(SortArgs a) {
   place_entries<false, kSortWaves>(a, begin, want < a.entries ? want : a.entries, first, lds);
 }
 
-// Counts of the ids of a block; reports those past the last group.  solo: all of it by one workgroup.
+// Counts of the ids of a block; reports those past the last group.
 __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a, uint16_t *counts, uint32_t *status) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int *sum = reinterpret_cast<int *>(lds);

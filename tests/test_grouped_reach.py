@@ -31,6 +31,13 @@ def test_cases_past_64_groups_reach_every_kernel(host):  # noqa: F811
     assert {_reached(_tiles(host, g * rows, g, n, k), k) for g, rows, k, n in FAR} >= EVERY - {(FEW, 16, False)}
 
 
+def test_few_rows_take_small_tiles_up_to_one_a_cu(host):  # noqa: F811
+    kind = lambda *s: _tiles(host, *s)["kind"]
+    assert kind(2, 8, 4096, 4096) == kind(2, 8, 4096, 14336) == kind(4, 16, 2048, 1408) == FEW  # 256 tiles of 16 x 32
+    assert kind(8, 256, 2048, 2048) == kind(8, 60, 1408, 2048) == kind(2, 8, 4128, 2048) == RING
+    assert kind(8, 128, 1536, 4096) == kind(4, 4, 2080, 4096) == DEEP
+
+
 @pytest.mark.parametrize("at,value,want", [
     (0, None, "ERR_NULL"), (3, None, "ERR_NULL"), (13, None, "ERR_NULL"), (15, None, "ERR_WORKSPACE"), (16, 256, "ERR_WORKSPACE"),
     (12, 5, "ERR_ARG"), (9, 2, "ERR_ARG"), (10, -1, "ERR_ARG"), (7, 48, "ERR_SHAPE"), (6, -1, "ERR_SHAPE"),

@@ -3,12 +3,14 @@
 //
 // A tile is rows of one group times columns of its matrix.  Few rows a group are
 // bound by the matrices' bytes: 16 tokens of 128 experts, 8 each, gate and up
-// rows of 4096 x 1536 read 276 MB in 43 us (6.4 TB/s, part of it from the last
-// level cache).  Many are bound by the steps of the LDS ring, as in the plain
-// product, and by rows that fill no tile: 4096 tokens (256 rows a group on
-// average, 1.5 tiles of 256) 201 us, 2.0 PFLOP/s of the entries' products and 3
-// of the tiles'; 8192 tokens of 8 experts, two each, on 4096 x 4096 195 us, 2.8
-// PFLOP/s.  product_tiles() chooses the kernel.
+// rows of 4096 x 1536 read 276 MB in 54 us (5.1 TB/s, the rate of a large copy)
+// where eight layers' matrices follow each other, and in 43 where the same ones
+// are read again, a sixth of them from the last level cache.  Many are bound by
+// the steps of the LDS ring, as in the plain product, and by rows that fill no
+// tile: 4096 tokens (256 rows a group on average, 1.5 tiles of 256) 203 to 218
+// us, 2.0 PFLOP/s of the entries' products and 3 of the tiles'; 8192 tokens of 8
+// experts, two each, on 4096 x 4096 181 to 199 us, 2.8 PFLOP/s.  product_tiles()
+// chooses the kernel.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -48,8 +50,8 @@ __device__ __forceinline__ int a_row(const GroupedArgs &a, int p, int e) {
 }
 
 // Zeros in the rows of C of entries of no group, a row a workgroup of whatever kernel at a time: they are read like any
-// other by what quantizes or sums C next.  (A call with none of them: one load a workgroup, 12.3 us instead of 12.0 for
-// one token of 8 experts; 333 tokens of which every seventh is padding 18.5 instead of 17.9.)
+// other by what quantizes or sums C next.  (A call with none of them: one load a workgroup, 11.9 us instead of 11.7 for
+// one token of 8 experts; 333 tokens of which every seventh is padding 18.8 instead of 18.1.)
 template <typename OutT>
 __device__ __forceinline__ void zero_rest(const GroupedArgs &a) {
   constexpr int VEC = 16 / (int)sizeof(OutT);

@@ -22,9 +22,10 @@
 // Both read through LDS what the matrix core wants by rows: a load of 16 bytes a
 // lane takes 16 cycles where its first 16 lanes read one run of memory, and 64
 // where they read 16 rows (8191 rows, rank 64, K 4096: shrink 31 us so, 21 by
-// LDS; expand to 14336 columns 115 with y and out in the operand's layout too, 90
-// now; 64 requests on 32 adapters, rank 64, N 4096: 9.6 -> 5.0).  Then y and out
-// bound it for many rows (the latter at 5.3 TB/s), B and two launches for few.
+// LDS; expand to 14336 columns, with two parts of u, 115 with y and out in the
+// operand's layout too, and 90; with all three parts 95; 64 requests on 32
+// adapters, rank 64, N 4096: 9.6 -> 5.0).  Then y and out bound it for many rows
+// (5.0 TB/s), B and two launches for few.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
